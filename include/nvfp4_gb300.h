@@ -359,6 +359,93 @@ fp4_status fp4_qadamw_v_encode(const float* v, int64_t rows, int64_t cols, int64
 fp4_status fp4_qadamw_v_decode(const fp4_tensor* in, const uint16_t* mean, float* v_out,
                                int64_t ldo, void* stream);
 
+/* ---------------------------------------------------------------------------
+ * Token log probabilities (the loss on a language model's logits, and what a
+ * server reports beside its tokens).  For row t of logits z (T x V, BF16 or
+ * FP32 by `dtype`, FP4_OUT_BF16 / FP4_OUT_F32; row pitch ld elements) and the
+ * distribution p = softmax(z / temperature):
+ *   m = max_j z_j,  S = sum_j exp((z_j - m) / temperature)
+ *   stats[t]       = (m, S)                    (so lse = m / temperature + ln S)
+ *   logprob[t]     = (z_target - m) / temperature - ln S
+ *   entropy[t]     = ln S - sum_j e_j x_j / S  (x_j = (z_j - m) / temperature)
+ *   top_index[t]   = the top_k tokens of the largest logits, largest first, equal
+ *                    logits by the lower index; top_logprob[t] their log probabilities.
+ * FP32 arithmetic, one read of the logits; deterministic.
+ *
+ * A logit of -inf is a banned token: probability 0, log probability -inf.  A row
+ * of nothing else has stats (-inf, 0), entropy 0, log probabilities -inf and
+ * top_index 0, 1, ....  A target < 0 does not count: logprob 0.  A target >= V
+ * gives NaN.  A row with NaN or +inf gives NaN for everything but top_index, where
+ * NaN ranks above +inf.
+ *
+ * logits: aligned to its element, ld >= V, any V in [1, 2^31 - 64].  targets
+ * (int64 [T]) and logprob go together (both NULL: not wanted); entropy NULL: not
+ * wanted; stats is always written.  0 <= top_k <= 32 (and <= V); top_index int64
+ * and top_logprob FP32, both [T][top_k].  T = 0 is a call without work.
+ * temperature > 0, finite. */
+fp4_status fp4_token_logprobs(const void* logits, int dtype, int64_t T, int64_t V, int64_t ld,
+                              float temperature, const int64_t* targets, int top_k, float* logprob,
+                              float* entropy, float* stats, float* top_logprob, int64_t* top_index,
+                              void* stream);
+
+/* Its gradient: dlogits of sum_t g_logprob[t] logprob[t] + g_entropy[t] entropy[t]
+ * + sum_i g_top[t][i] top_logprob[t][i], with stats, entropy (needed with
+ * g_entropy) and top_index as the forward call left them, same temperature:
+ *   dz_j = (p_j (-G - g_entropy (ln p_j + entropy)) + [j = target] g_logprob
+ *           + sum_i [j = top_index_i] g_top_i) / temperature,   G = all g_logprob and g_top
+ * rounded once to dlogits' type (the logits').  A banned token's entry is 0, and so
+ * is a row of banned tokens; a target < 0 contributes nothing.  A target >= V or a
+ * top_index outside [0, V) makes its row NaN.
+ * Any of g_logprob, g_entropy, g_top may be NULL (zero).  dlogits: row pitch ldd;
+ * it may be logits itself (then ldd = ld), else they may not overlap. */
+fp4_status fp4_token_logprobs_bwd(const void* logits, int dtype, int64_t T, int64_t V, int64_t ld,
+                                  float temperature, const int64_t* targets, const float* stats,
+                                  const float* entropy, const float* g_logprob, const float* g_entropy,
+                                  int top_k, const int64_t* top_index, const float* g_top, void* dlogits,
+                                  int64_t ldd, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * One AdamW step over many tensors (decoupled weight decay).  Per element, every
+ * operator one FP32 operation in this order (so a step is reproducible to the bit):
+ *   g = grad * grad_scale
+ *   m = beta1 m + (1 - beta1) g;   v = beta2 v + (1 - beta2) (g g)
+ *   param = param (1 - lr weight_decay) - size (m / (sqrt(v) root + eps)),
+ *   size = lr / (1 - beta1^step),  root = 1 / sqrt(1 - beta2^step)   (FP64, then FP32)
+ * then model (if given) = bf16(param).
+ *
+ * state_bits 32: m and v are FP32.  state_bits 8: m is E4M3, v E5M2, each with one
+ * scale byte b (2^(b - 127)) per 128 consecutive elements (the last block may be
+ * short): the least power of two with which the block's largest finite magnitude
+ * fits the format.  param uses the new moments before they are rounded.  FP4_ROUND_SR:
+ * 16 random bits per value by Philox4x32-10, key = seed, counter (j lo, j hi, 2 i + w, step)
+ * for elements 8j..8j+7 of tensor i (w = 0: m, 1: v), halves of the words in order, low
+ * half first; a value rounds up in magnitude iff its position between its neighbours,
+ * plus the fraction, reaches 1.  FP4_ROUND_RTN: nearest even; a moment whose change per
+ * step is below half a step of its format then stands still, so SR is the mode for
+ * training.  A positive v never rounds to 0.  A moment that is not finite is held as NaN.
+ * Zeroed codes and scales are the states' start.
+ *
+ * grad_scale (optional, device): multiplies every gradient (a clipping coefficient);
+ * if it is not finite the call leaves everything as it was.
+ * Pointers are aligned to their elements; with all of them 16-byte aligned (codes
+ * 8-byte) the kernel uses wide accesses.  A tensor with numel 0 is skipped; the others'
+ * buffers may not overlap.  grad_dtype: FP4_OUT_BF16 or FP4_OUT_F32 for all tensors.
+ * lr, eps >= 0, 0 <= beta < 1, 1 <= step < 2^32.  n = 0 is a call without work. */
+typedef struct {
+    float* param;
+    const void* grad;
+    void* m;
+    void* v;
+    uint8_t* m_scale;  /* 8-bit states: ceil(numel / 128) bytes; else NULL */
+    uint8_t* v_scale;
+    void* model;       /* BF16 copy of param, or NULL */
+    int64_t numel;
+    double weight_decay;
+} fp4_adamw_tensor;
+fp4_status fp4_adamw_step(const fp4_adamw_tensor* tensors, int n, int grad_dtype, int state_bits,
+                          double lr, double beta1, double beta2, double eps, int64_t step,
+                          int round_mode, uint64_t seed, const float* grad_scale, void* stream);
+
 /* Synchronise `stream`, then read and clear the device status word.
  * Returns FP4_ERR_TIMEOUT if any kernel recorded an expired wait. */
 fp4_status fp4_check_status(void* stream);

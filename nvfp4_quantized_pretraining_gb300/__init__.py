@@ -37,7 +37,7 @@ EXPORTS = ["fp4_scale_bytes", "fp4_amax", "fp4_quantize", "fp4_quantize_transpos
            "fp4_linear_fwd", "fp4_linear_fwd_noalloc", "fp4_linear_bwd", "fp4_lora_factor_grad_workspace",
            "fp4_lora_factor_grad", "fp4_lora_cholqr_workspace", "fp4_lora_cholqr", "fp4_lora_realign_workspace",
            "fp4_lora_realign", "fp4_newton_schulz_workspace", "fp4_newton_schulz", "fp4_qadamw_v_encode",
-           "fp4_qadamw_v_decode", "fp4_check_status", "fp4_last_error", "fp4_launch_count",
+           "fp4_qadamw_v_decode", "fp4_token_logprobs", "fp4_token_logprobs_bwd", "fp4_adamw_step", "fp4_check_status", "fp4_last_error", "fp4_launch_count",
            "fp4_debug_convert", "fp4_debug_sr_round", "fp4_debug_force_counter64", "fp4_mma_peak_probe"]
 
 
@@ -53,6 +53,13 @@ class CTensor(ctypes.Structure):
                 ("rows", ctypes.c_int64), ("cols", ctypes.c_int64)]
 
 
+class CAdamWTensor(ctypes.Structure):
+    """Mirror of ``fp4_adamw_tensor``."""
+    _fields_ = [("param", ctypes.c_void_p), ("grad", ctypes.c_void_p), ("m", ctypes.c_void_p), ("v", ctypes.c_void_p),
+                ("m_scale", ctypes.c_void_p), ("v_scale", ctypes.c_void_p), ("model", ctypes.c_void_p),
+                ("numel", ctypes.c_int64), ("weight_decay", ctypes.c_double)]
+
+
 _lib = None
 
 
@@ -64,8 +71,8 @@ def lib() -> ctypes.CDLL:
     if not os.path.exists(LIB_PATH):
         raise RuntimeError(f"CUDA library {LIB_PATH} is missing: run nvfp4_quantized_pretraining_gb300.build.build()")
     L = ctypes.CDLL(LIB_PATH)
-    P, i64, u64, u32, i32, f32 = (ctypes.c_void_p, ctypes.c_int64, ctypes.c_uint64, ctypes.c_uint32,
-                                  ctypes.c_int, ctypes.c_float)
+    P, i64, u64, u32, i32, f32, f64 = (ctypes.c_void_p, ctypes.c_int64, ctypes.c_uint64, ctypes.c_uint32,
+                                       ctypes.c_int, ctypes.c_float, ctypes.c_double)
     T = ctypes.POINTER(CTensor)
     sig = {
         "fp4_scale_bytes": (i64, [i64, i64]),
@@ -96,6 +103,9 @@ def lib() -> ctypes.CDLL:
                                     P]),
         "fp4_qadamw_v_encode": (i32, [P, i64, i64, i64, T, P, P]),
         "fp4_qadamw_v_decode": (i32, [T, P, P, i64, P]),
+        "fp4_token_logprobs": (i32, [P, i32, i64, i64, i64, f32, P, i32, P, P, P, P, P, P]),
+        "fp4_token_logprobs_bwd": (i32, [P, i32, i64, i64, i64, f32, P, P, P, P, P, i32, P, P, P, i64, P]),
+        "fp4_adamw_step": (i32, [P, i32, i32, i32, f64, f64, f64, f64, i64, i32, u64, P, P]),
         "fp4_check_status": (i32, [P]),
         "fp4_last_error": (ctypes.c_char_p, []),
         "fp4_launch_count": (u64, []),
@@ -497,6 +507,162 @@ def fp4_qadamw_v_decode(q: NVFP4Tensor, mean: torch.Tensor, out: torch.Tensor | 
     ct = q.c()
     _check(lib().fp4_qadamw_v_decode(ctypes.byref(ct), mean.data_ptr(), out.data_ptr(), ldo, _stream(stream)))
     return out
+
+
+@dataclass
+class TokenLogprobs:
+    """Result of ``fp4_token_logprobs`` for T rows: ``logprob`` float32 [T] (None without targets), ``entropy``
+    float32 [T] (None if not wanted), ``stats`` float32 [T, 2] = (max logit, sum of exp((z - max) / temperature)),
+    ``top_logprob`` float32 and ``top_index`` int64 [T, top_k], and the ``temperature`` of the call."""
+    logprob: torch.Tensor | None
+    entropy: torch.Tensor | None
+    stats: torch.Tensor
+    top_logprob: torch.Tensor
+    top_index: torch.Tensor
+    temperature: float
+
+
+def _logits_2d(x: torch.Tensor, name: str):
+    """(dtype code, T, V, row pitch) of a matrix of logits; the pitch of fewer than two rows is not used."""
+    if x.dtype not in (torch.bfloat16, torch.float32) or x.dim() != 2 or not x.is_cuda or x.stride(1) != 1:
+        raise ValueError(f"{name} must be a 2-D CUDA bfloat16 or float32 tensor with unit column stride")
+    T, V = x.shape
+    ld = x.stride(0) if T > 1 else max(V, 1)
+    if ld < V:
+        raise ValueError(f"{name}: rows overlap (row stride {ld} < {V})")
+    return OUT_F32 if x.dtype == torch.float32 else OUT_BF16, T, V, ld
+
+
+def _check_vector(t, shape, dtype, device, name: str) -> None:
+    """An optional per-row argument: contiguous, exact shape and dtype, on ``device``."""
+    if t is not None and (t.dtype != dtype or t.device != device or not t.is_contiguous()
+                          or tuple(t.shape) != tuple(shape)):
+        raise ValueError(f"{name} must be a contiguous {tuple(shape)} {dtype} tensor on {device} "
+                         f"(got {tuple(t.shape)} {t.dtype} on {t.device})")
+
+
+def fp4_token_logprobs(logits: torch.Tensor, targets: torch.Tensor | None = None, top_k: int = 0,
+                       temperature: float = 1.0, entropy: bool = True, stream=None) -> TokenLogprobs:
+    """Log probabilities of ``targets`` (int64 [T]; negative: the row does not count) under
+    softmax(logits / temperature), the entropy, and the ``top_k`` (at most 32) likeliest tokens of each row,
+    equal logits by the lower index.  logits: T x V bfloat16 or float32; -inf bans a token."""
+    dtype, T, V, ld = _logits_2d(logits, "logits")
+    dev = logits.device
+    _check_vector(targets, (T,), torch.int64, dev, "targets")
+    f32 = torch.float32
+    r = TokenLogprobs(torch.empty(T, dtype=f32, device=dev) if targets is not None else None,
+                      torch.empty(T, dtype=f32, device=dev) if entropy else None,
+                      torch.empty((T, 2), dtype=f32, device=dev),
+                      torch.empty((T, max(top_k, 0)), dtype=f32, device=dev),
+                      torch.empty((T, max(top_k, 0)), dtype=torch.int64, device=dev), float(temperature))
+    _check(lib().fp4_token_logprobs(logits.data_ptr(), dtype, T, V, ld, r.temperature, _ptr(targets), top_k,
+                                    _ptr(r.logprob), _ptr(r.entropy), r.stats.data_ptr(), r.top_logprob.data_ptr(),
+                                    r.top_index.data_ptr(), _stream(stream)))
+    return r
+
+
+def fp4_token_logprobs_bwd(logits: torch.Tensor, saved: TokenLogprobs, targets: torch.Tensor | None = None,
+                           g_logprob=None, g_entropy=None, g_top=None, dlogits=None, stream=None) -> torch.Tensor:
+    """Gradient of sum(g_logprob logprob) + sum(g_entropy entropy) + sum(g_top top_logprob) with respect to the
+    logits, from the forward call's result.  Pass ``dlogits=logits`` to write over them."""
+    dtype, T, V, ld = _logits_2d(logits, "logits")
+    dev, f32, k = logits.device, torch.float32, saved.top_index.shape[1]
+    _check_vector(targets, (T,), torch.int64, dev, "targets")
+    _check_vector(saved.stats, (T, 2), f32, dev, "saved.stats")
+    _check_vector(saved.entropy, (T,), f32, dev, "saved.entropy")
+    _check_vector(saved.top_index, (T, k), torch.int64, dev, "saved.top_index")
+    for g, shape, name in ((g_logprob, (T,), "g_logprob"), (g_entropy, (T,), "g_entropy"), (g_top, (T, k), "g_top")):
+        _check_vector(g, shape, f32, dev, name)
+    dlogits = torch.empty((T, V), dtype=logits.dtype, device=dev) if dlogits is None else dlogits
+    _check_out(dlogits, (T, V), logits.dtype, dev, "dlogits")
+    ldd = dlogits.stride(0) if T > 1 else max(V, 1)
+    _check(lib().fp4_token_logprobs_bwd(logits.data_ptr(), dtype, T, V, ld, saved.temperature, _ptr(targets),
+                                        saved.stats.data_ptr(), _ptr(saved.entropy), _ptr(g_logprob),
+                                        _ptr(g_entropy), k, _ptr(saved.top_index) if k else None,
+                                        _ptr(g_top) if k else None, dlogits.data_ptr(), ldd, _stream(stream)))
+    return dlogits
+
+
+ADAMW_BLOCK = 128  # elements that share a scale byte of an 8-bit moment
+
+
+class AdamWTensors:
+    """The tensors of an AdamW step, built once and passed to ``fp4_adamw_step`` every step (it keeps the tensors,
+    whose values may change; a new tensor needs a new list).
+
+    params: float32; grads: all bfloat16 or all float32; m, v: float32 moments, or float8_e4m3fn and
+    float8_e5m2 codes with ``m_scale``/``v_scale`` (uint8, one byte per 128 elements; ``moments`` makes zeroed
+    ones); model: optional bfloat16 copies of the parameters that the step writes (None entries: no copy);
+    weight_decay: one number, or one per tensor.  Tensors are contiguous, of any shape."""
+
+    def __init__(self, params, grads, m, v, m_scale=None, v_scale=None, model=None, weight_decay=0.0):
+        n = len(params)
+        decay = [float(weight_decay)] * n if isinstance(weight_decay, (int, float)) else [float(w) for w in weight_decay]
+        lists = {"grads": grads, "m": m, "v": v, "weight_decay": decay}
+        lists.update((k, x) for k, x in (("m_scale", m_scale), ("v_scale", v_scale), ("model", model)) if x is not None)
+        for name, x in lists.items():
+            if len(x) != n:
+                raise ValueError(f"{name} has {len(x)} entries for {n} parameters")
+        if (m_scale is None) != (v_scale is None):
+            raise ValueError("m_scale and v_scale must both be given (8-bit moments) or both be None")
+        self.bits = 32 if m_scale is None else 8
+        self.grad_dtype = grads[0].dtype if n else torch.float32
+        if self.grad_dtype not in (torch.bfloat16, torch.float32):
+            raise ValueError(f"grads must be bfloat16 or float32 (got {self.grad_dtype})")
+        self.device = params[0].device if n else None
+        kinds = (torch.float32, torch.float32) if self.bits == 32 else (torch.float8_e4m3fn, torch.float8_e5m2)
+
+        def check(t, numel, dtype, name, i):
+            if t.dtype != dtype or not t.is_cuda or t.device != self.device or not t.is_contiguous() or t.numel() != numel:
+                raise ValueError(f"{name}[{i}] must be a contiguous {dtype} tensor of {numel} elements on {self.device} "
+                                 f"(got {tuple(t.shape)} {t.dtype} on {t.device})")
+
+        self.c = (CAdamWTensor * n)()
+        for i in range(n):
+            p, c = params[i], self.c[i]
+            num = p.numel()
+            check(p, num, torch.float32, "params", i)
+            check(grads[i], num, self.grad_dtype, "grads", i)
+            check(m[i], num, kinds[0], "m", i)
+            check(v[i], num, kinds[1], "v", i)
+            c.param, c.grad, c.m, c.v = p.data_ptr(), grads[i].data_ptr(), m[i].data_ptr(), v[i].data_ptr()
+            if self.bits == 8:
+                blocks = (num + ADAMW_BLOCK - 1) // ADAMW_BLOCK
+                check(m_scale[i], blocks, torch.uint8, "m_scale", i)
+                check(v_scale[i], blocks, torch.uint8, "v_scale", i)
+                c.m_scale, c.v_scale = m_scale[i].data_ptr(), v_scale[i].data_ptr()
+            if model is not None and model[i] is not None:
+                check(model[i], num, torch.bfloat16, "model", i)
+                c.model = model[i].data_ptr()
+            c.numel, c.weight_decay = num, decay[i]
+        self.n = n
+        self.tensors = (list(params), list(grads), list(m), list(v), m_scale and list(m_scale),
+                        v_scale and list(v_scale), model and list(model))
+
+    @staticmethod
+    def moments(param: torch.Tensor, bits: int = 8):
+        """Zeroed (m, v, m_scale, v_scale) for one parameter; the scales are None with 32 bits."""
+        if bits == 32:
+            return torch.zeros_like(param), torch.zeros_like(param), None, None
+        if bits != 8:
+            raise ValueError(f"bits {bits} is not 8 or 32")
+        blocks = (param.numel() + ADAMW_BLOCK - 1) // ADAMW_BLOCK
+        byte = lambda *shape: torch.zeros(shape, dtype=torch.uint8, device=param.device)  # noqa: E731
+        return (byte(*param.shape).view(torch.float8_e4m3fn), byte(*param.shape).view(torch.float8_e5m2), byte(blocks),
+                byte(blocks))
+
+
+def fp4_adamw_step(tensors: AdamWTensors, step: int, lr: float, betas=(0.9, 0.95), eps: float = 1e-8, round_mode=SR,
+                   seed: int = 0, grad_scale: torch.Tensor | None = None, stream=None) -> None:
+    """One AdamW step (``step`` counts from 1) over all ``tensors``, in place.  ``grad_scale``: optional float32
+    device scalar that multiplies the gradients; not finite, the step changes nothing.  ``round_mode``/``seed``:
+    how 8-bit moments round (SR: Philox, the same bits for the same seed and step)."""
+    if grad_scale is not None and (grad_scale.dtype != torch.float32 or grad_scale.numel() != 1
+                                   or grad_scale.device != tensors.device):
+        raise ValueError(f"grad_scale must be one float32 number on {tensors.device}")
+    _check(lib().fp4_adamw_step(tensors.c, tensors.n, OUT_F32 if tensors.grad_dtype == torch.float32 else OUT_BF16,
+                                tensors.bits, lr, betas[0], betas[1], eps, step, round_mode, seed, _ptr(grad_scale),
+                                _stream(stream)))
 
 
 def fp4_check_status(stream=None) -> None:

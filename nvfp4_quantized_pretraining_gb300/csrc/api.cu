@@ -7,6 +7,7 @@
 #include <cstring>
 #include <string>
 
+#include "api_util.h"
 #include "kernels.h"
 #include "nvfp4_gb300.h"
 
@@ -17,8 +18,7 @@ void count_launch() { g_launches.fetch_add(1, std::memory_order_relaxed); }
 
 static thread_local std::string t_err = "no error";
 
-static fp4_status fail(fp4_status st, const char* fmt, ...) __attribute__((format(printf, 2, 3)));
-static fp4_status fail(fp4_status st, const char* fmt, ...) {
+fp4_status fail(fp4_status st, const char* fmt, ...) {
   char buf[512];
   va_list ap;
   va_start(ap, fmt);
@@ -28,14 +28,7 @@ static fp4_status fail(fp4_status st, const char* fmt, ...) {
   return st;
 }
 
-#define CUDA_TRY(expr)                                                                      \
-  do {                                                                                      \
-    cudaError_t e_ = (expr);                                                                \
-    if (e_ != cudaSuccess)                                                                  \
-      return fail(FP4_ERR_CUDA, "%s failed: %s", #expr, cudaGetErrorString(e_));            \
-  } while (0)
-
-static int sm_count() {
+int sm_count() {
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return 148;
   static std::atomic<int> cache[64];
@@ -48,9 +41,6 @@ static int sm_count() {
   if (dev >= 0 && dev < 64) cache[dev].store(n);
   return n;
 }
-
-static bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-static size_t round256(size_t x) { return (x + 255) & ~size_t(255); }
 
 static int64_t scale_bytes(int64_t rows, int64_t cols) {
   const int64_t kb = cols / 16;

@@ -1,0 +1,162 @@
+// C ABI of what surrounds the NVFP4 block in a training step: token log probabilities with
+// their gradient, and the AdamW step.  Argument validation only; the contracts are in
+// include/nvfp4_gb300.h.
+#include <cmath>
+
+#include "api_util.h"
+#include "kernels.h"
+#include "nvfp4_gb300.h"
+
+namespace nvfp4 {
+
+static fp4_status check_dtype(int dtype, const char* name) {
+  if (dtype != FP4_OUT_BF16 && dtype != FP4_OUT_F32)
+    return fail(FP4_ERR_INVALID_ARG, "%s %d is not BF16 (0) or FP32 (1)", name, dtype);
+  return FP4_OK;
+}
+
+// A T x V matrix of logits (or its gradient).
+static fp4_status check_logits(const void* p, int dtype, int64_t T, int64_t V, int64_t ld, const char* name) {
+  if (!p) return fail(FP4_ERR_INVALID_ARG, "%s is NULL", name);
+  if (ld < V) return fail(FP4_ERR_INVALID_ARG, "%s: ld %lld < V %lld", name, (long long)ld, (long long)V);
+  if (!aligned_to(p, dtype == FP4_OUT_F32 ? 4 : 2))
+    return fail(FP4_ERR_MISALIGNED, "%s must be aligned to its element", name);
+  if (T > 1 && ld > (int64_t(1) << 60) / T) return fail(FP4_ERR_UNSUPPORTED_SHAPE, "%s too large", name);
+  return FP4_OK;
+}
+static fp4_status check_logprob_sizes(int64_t T, int64_t V, float temperature, int top_k) {
+  if (T < 0 || V < 1) return fail(FP4_ERR_INVALID_ARG, "T %lld, V %lld: T >= 0 and V >= 1 needed", (long long)T, (long long)V);
+  if (T > INT32_MAX / 16 || V > INT32_MAX - 64)
+    return fail(FP4_ERR_UNSUPPORTED_SHAPE, "T %lld (at most 2^27) or V %lld (below 2^31 - 64) too large", (long long)T, (long long)V);
+  if (!(temperature > 0.0f) || !std::isfinite(temperature) || !std::isfinite(1.0f / temperature))
+    return fail(FP4_ERR_INVALID_ARG, "temperature %g must be positive and finite", (double)temperature);
+  if (top_k < 0 || top_k > 32 || top_k > V)
+    return fail(FP4_ERR_INVALID_ARG, "top_k %d must be in [0, 32] and at most V", top_k);
+  return FP4_OK;
+}
+static fp4_status check_aligned(const void* p, uintptr_t n, const char* name) {
+  return aligned_to(p, n) ? FP4_OK
+                          : fail(FP4_ERR_MISALIGNED, "%s must be %d-byte aligned", name, (int)n);
+}
+
+}  // namespace nvfp4
+
+using namespace nvfp4;
+
+extern "C" {
+
+fp4_status fp4_token_logprobs(const void* logits, int dtype, int64_t T, int64_t V, int64_t ld, float temperature,
+                              const int64_t* targets, int top_k, float* logprob, float* entropy, float* stats,
+                              float* top_logprob, int64_t* top_index, void* stream) {
+  pdl_chain_break();  // the call's first kernel is ordered after all earlier stream work
+  fp4_status st;
+  if ((st = check_dtype(dtype, "dtype")) || (st = check_logprob_sizes(T, V, temperature, top_k))) return st;
+  if (T == 0) return FP4_OK;
+  if ((st = check_logits(logits, dtype, T, V, ld, "logits"))) return st;
+  if (!stats) return fail(FP4_ERR_INVALID_ARG, "stats is NULL");
+  if ((targets == nullptr) != (logprob == nullptr))
+    return fail(FP4_ERR_INVALID_ARG, "targets and logprob must both be given or both be NULL");
+  if (top_k > 0 && (!top_logprob || !top_index))
+    return fail(FP4_ERR_INVALID_ARG, "top_k %d needs top_logprob and top_index", top_k);
+  if ((st = check_aligned(targets, 8, "targets")) || (st = check_aligned(logprob, 4, "logprob")) ||
+      (st = check_aligned(entropy, 4, "entropy")) || (st = check_aligned(stats, 8, "stats")) ||
+      (st = check_aligned(top_logprob, 4, "top_logprob")) || (st = check_aligned(top_index, 8, "top_index")))
+    return st;
+  LogprobArgs a{logits, dtype == FP4_OUT_F32, T, V, ld, 1.0f / temperature, targets, top_k,
+                logprob, entropy, stats, top_logprob, top_index};
+  CUDA_TRY(launch_token_logprobs(a, sm_count(), static_cast<cudaStream_t>(stream)));
+  return FP4_OK;
+}
+
+fp4_status fp4_token_logprobs_bwd(const void* logits, int dtype, int64_t T, int64_t V, int64_t ld, float temperature,
+                                  const int64_t* targets, const float* stats, const float* entropy,
+                                  const float* g_logprob, const float* g_entropy, int top_k, const int64_t* top_index,
+                                  const float* g_top, void* dlogits, int64_t ldd, void* stream) {
+  pdl_chain_break();  // the call's first kernel is ordered after all earlier stream work
+  fp4_status st;
+  if ((st = check_dtype(dtype, "dtype")) || (st = check_logprob_sizes(T, V, temperature, top_k))) return st;
+  if (T == 0) return FP4_OK;
+  if ((st = check_logits(logits, dtype, T, V, ld, "logits")) || (st = check_logits(dlogits, dtype, T, V, ldd, "dlogits")))
+    return st;
+  if (!stats) return fail(FP4_ERR_INVALID_ARG, "stats is NULL");
+  if (dlogits == logits && ldd != ld)
+    return fail(FP4_ERR_INVALID_ARG, "in place, ldd %lld must equal ld %lld", (long long)ldd, (long long)ld);
+  if (g_logprob && !targets) return fail(FP4_ERR_INVALID_ARG, "g_logprob needs targets");
+  if (g_entropy && !entropy) return fail(FP4_ERR_INVALID_ARG, "g_entropy needs entropy");
+  if (g_top && (top_k == 0 || !top_index)) return fail(FP4_ERR_INVALID_ARG, "g_top needs top_k > 0 and top_index");
+  if ((st = check_aligned(targets, 8, "targets")) || (st = check_aligned(stats, 8, "stats")) ||
+      (st = check_aligned(entropy, 4, "entropy")) || (st = check_aligned(g_logprob, 4, "g_logprob")) ||
+      (st = check_aligned(g_entropy, 4, "g_entropy")) || (st = check_aligned(g_top, 4, "g_top")) ||
+      (st = check_aligned(top_index, 8, "top_index")))
+    return st;
+  LogprobBwdArgs a{logits, dtype == FP4_OUT_F32, T, V, ld, 1.0f / temperature, g_logprob ? targets : nullptr, stats,
+                   entropy, g_logprob, g_entropy, g_top ? top_k : 0, top_index, g_top, dlogits, ldd};
+  CUDA_TRY(launch_token_logprobs_bwd(a, sm_count(), static_cast<cudaStream_t>(stream)));
+  return FP4_OK;
+}
+
+fp4_status fp4_adamw_step(const fp4_adamw_tensor* tensors, int n, int grad_dtype, int state_bits, double lr,
+                          double beta1, double beta2, double eps, int64_t step, int round_mode, uint64_t seed,
+                          const float* grad_scale, void* stream) {
+  pdl_chain_break();  // the call's first kernel is ordered after all earlier stream work
+  fp4_status st;
+  if ((st = check_dtype(grad_dtype, "grad_dtype"))) return st;
+  if (n < 0 || (n > 0 && !tensors)) return fail(FP4_ERR_INVALID_ARG, "n %d tensors at %p", n, (const void*)tensors);
+  if (state_bits != 8 && state_bits != 32) return fail(FP4_ERR_INVALID_ARG, "state_bits %d is not 8 or 32", state_bits);
+  if (round_mode != FP4_ROUND_RTN && round_mode != FP4_ROUND_SR)
+    return fail(FP4_ERR_INVALID_ARG, "round_mode %d is not RTN (0) or SR (1)", round_mode);
+  if (!(lr >= 0.0) || !std::isfinite(lr) || !(eps >= 0.0) || !std::isfinite(eps))
+    return fail(FP4_ERR_INVALID_ARG, "lr %g and eps %g must be finite and not negative", lr, eps);
+  if (!(beta1 >= 0.0 && beta1 < 1.0) || !(beta2 >= 0.0 && beta2 < 1.0))
+    return fail(FP4_ERR_INVALID_ARG, "beta1 %g and beta2 %g must be in [0, 1)", beta1, beta2);
+  if (step < 1 || step > INT64_C(0xFFFFFFFF)) return fail(FP4_ERR_INVALID_ARG, "step %lld must be in [1, 2^32)", (long long)step);
+  if ((st = check_aligned(grad_scale, 4, "grad_scale"))) return st;
+  int64_t total = 0;
+  const uintptr_t gsize = grad_dtype == FP4_OUT_F32 ? 4 : 2, ssize = state_bits == 32 ? 4 : 1;
+  for (int i = 0; i < n; ++i) {  // everything is checked before anything is launched
+    const fp4_adamw_tensor& t = tensors[i];
+    if (t.numel < 0) return fail(FP4_ERR_INVALID_ARG, "tensor %d: numel %lld", i, (long long)t.numel);
+    if (t.numel > (int64_t(1) << 40)) return fail(FP4_ERR_UNSUPPORTED_SHAPE, "tensor %d: numel %lld too large", i, (long long)t.numel);
+    if (!std::isfinite(t.weight_decay)) return fail(FP4_ERR_INVALID_ARG, "tensor %d: weight decay not finite", i);
+    if (t.numel == 0) continue;
+    total += t.numel;
+    if (!t.param || !t.grad || !t.m || !t.v || (state_bits == 8 && (!t.m_scale || !t.v_scale)))
+      return fail(FP4_ERR_INVALID_ARG, "tensor %d has a NULL buffer", i);
+    if (!aligned_to(t.param, 4) || !aligned_to(t.grad, gsize) || !aligned_to(t.m, ssize) || !aligned_to(t.v, ssize) ||
+        !aligned_to(t.model, 2))
+      return fail(FP4_ERR_MISALIGNED, "tensor %d: a buffer is not aligned to its element", i);
+  }
+  if (total > (int64_t(1) << 42)) return fail(FP4_ERR_UNSUPPORTED_SHAPE, "%lld elements: too many", (long long)total);
+  AdamWScalars a{};
+  a.b1 = static_cast<float>(beta1), a.c1 = static_cast<float>(1.0 - beta1);
+  a.b2 = static_cast<float>(beta2), a.c2 = static_cast<float>(1.0 - beta2);
+  a.size = static_cast<float>(lr / (1.0 - std::pow(beta1, static_cast<double>(step))));
+  a.root = static_cast<float>(1.0 / std::sqrt(1.0 - std::pow(beta2, static_cast<double>(step))));
+  a.eps = static_cast<float>(eps);
+  a.step = static_cast<uint32_t>(step);
+  a.seed = seed;
+  a.grad_scale = grad_scale;
+  // runs of at most a launch's capacity; a tensor's random streams go by its place in the whole list
+  constexpr int kMost = 400;
+  AdamWEntry e[kMost];
+  const int most = adamw_capacity() < kMost ? adamw_capacity() : kMost;
+  for (int first = 0; first < n; first += most) {
+    const int count = n - first < most ? n - first : most;
+    int64_t work = 0;
+    for (int i = 0; i < count; ++i) {
+      const fp4_adamw_tensor& t = tensors[first + i];
+      const uintptr_t sa = state_bits == 32 ? 16 : 8;
+      const bool vec = aligned16(t.param) && aligned16(t.grad) && aligned_to(t.m, sa) && aligned_to(t.v, sa) &&
+                       aligned16(t.model);
+      e[i] = AdamWEntry{t.param, t.grad, t.m, t.v, t.m_scale, t.v_scale, t.model, t.numel,
+                        static_cast<float>(1.0 - lr * t.weight_decay), vec ? 1u : 0u};
+      work += t.numel;
+    }
+    if (work == 0) continue;
+    CUDA_TRY(launch_adamw(e, count, first, grad_dtype == FP4_OUT_BF16, state_bits, round_mode == FP4_ROUND_SR, a,
+                          sm_count(), static_cast<cudaStream_t>(stream)));
+  }
+  return FP4_OK;
+}
+
+}  // extern "C"

@@ -170,4 +170,52 @@ cudaError_t launch_vt_encode(const float* v, int64_t rows, int64_t cols, int64_t
 cudaError_t launch_vt_decode(const void* codes, const void* scales, const float* scale, const uint16_t* mean,
                              int64_t rows, int64_t cols, float* out, int64_t ldo, int num_sms, cudaStream_t s);
 
+// AdamW over a list of tensors (at most adamw_capacity() per launch; every numel > 0).
+struct AdamWEntry {
+  float* param;
+  const void* grad;   // BF16 or FP32
+  void *m, *v;        // FP32, or E4M3 / E5M2 codes
+  uint8_t *m_scale, *v_scale;  // 8-bit states: one byte per 128 elements
+  void* model;        // BF16 copy of param, or nullptr
+  int64_t numel;
+  float keep;         // 1 - lr * weight decay
+  uint32_t vector;    // every pointer allows 8-element accesses
+};
+struct AdamWScalars {
+  float b1, c1, b2, c2, size, root, eps;
+  uint32_t step;
+  uint64_t seed;
+  const float* grad_scale;  // device, or nullptr
+};
+int adamw_capacity();
+cudaError_t launch_adamw(const AdamWEntry* t, int n, int first_tensor, bool grad_bf16, int bits, bool sr,
+                         const AdamWScalars& a, int num_sms, cudaStream_t s);
+
+// Log probabilities of tokens (and their gradient); see the C header for the arguments.
+struct LogprobArgs {
+  const void* logits;
+  int f32;
+  int64_t T, V, ld;
+  float scale;  // 1 / temperature
+  const int64_t* targets;
+  int top_k;
+  float *logprob, *entropy, *stats, *top_logprob;
+  int64_t* top_index;
+};
+cudaError_t launch_token_logprobs(const LogprobArgs& a, int num_sms, cudaStream_t s);
+struct LogprobBwdArgs {
+  const void* logits;
+  int f32;
+  int64_t T, V, ld;
+  float scale;
+  const int64_t* targets;
+  const float *stats, *entropy, *g_logprob, *g_entropy;
+  int top_k;
+  const int64_t* top_index;
+  const float* g_top;
+  void* dlogits;
+  int64_t ldd;
+};
+cudaError_t launch_token_logprobs_bwd(const LogprobBwdArgs& a, int num_sms, cudaStream_t s);
+
 }  // namespace nvfp4

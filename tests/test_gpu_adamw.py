@@ -1,0 +1,383 @@
+"""The AdamW step over many tensors.
+
+FP32 moments: against the formula in 64 bits.  m and v are two products and a sum of one rounding each, so they err by at
+most 3 2^-24 of the sum of their terms' magnitudes; the update goes through five more operations (each 2^-24 relative) and
+two roundings at the size of the parameter.
+8-bit moments: codes, scale bytes and parameters bit for bit against the same operations in NumPy FP32 and integers (every
+step of the contract is one FP32 operation), and the decoded moments against 64 bits: within one step of the 8-bit
+format of the unrounded value (stochastic) or half a step (nearest), plus the FP32 bound above."""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+DEV = "cuda"
+B1, B2, EPS, LR = 0.9, 0.95, 1e-8, 3e-3
+
+
+@pytest.fixture(scope="module")
+def F():
+    import __graft_entry__
+    __graft_entry__.build()
+    import nvfp4_quantized_pretraining_gb300 as F
+    return F
+
+
+def make(sizes, grad_dtype, seed):
+    g = torch.Generator().manual_seed(seed)
+    p = [torch.randn(n, generator=g) for n in sizes]
+    grads = [(torch.randn(n, generator=g) * 10.0 ** float(torch.randn((), generator=g))).to(grad_dtype) for n in sizes]
+    m = [torch.randn(n, generator=g) * 0.1 for n in sizes]
+    v = [torch.rand(n, generator=g) * 0.1 for n in sizes]
+    return p, grads, m, v
+
+
+def reference(p, g, m, v, step, decay, gs=1.0):
+    """The formula in 64 bits, and the bounds."""
+    p, g, m, v = (np.asarray(a, dtype=np.float64) for a in (p, g, m, v))
+    g = g * gs
+    u = 2.0 ** -24
+    m1, v1 = B1 * m + (1 - B1) * g, B2 * v + (1 - B2) * g * g
+    bm = 4 * u * (np.abs(B1 * m) + np.abs((1 - B1) * g)) + 1e-44
+    bv = 5 * u * v1 + 1e-44
+    upd = LR / (1 - B1 ** step) * m1 / (np.sqrt(v1 / (1 - B2 ** step)) + EPS)
+    p1 = p * (1 - LR * decay) - upd
+    with np.errstate(invalid="ignore", divide="ignore"):
+        rel = np.where(m1 != 0, bm / np.abs(m1), 0.0)
+    bp = 2 * u * np.abs(p) + u * np.abs(p1) + np.abs(upd) * (rel + 12 * u) + 1e-44
+    return p1, m1, v1, bp, bm, bv
+
+
+def f64(t):
+    return t.double().cpu().numpy()
+
+
+SIZES = [[1], [7], [128], [129, 1, 0, 5000], [2048, 2049, 2047], [300_001], [64] * 60 + [12345]]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("grad_dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("sizes", SIZES, ids=[str(len(s)) + "x" + str(s[0]) for s in SIZES])
+def test_fp32_moments(F, sizes, grad_dtype):
+    p, g, m, v = make(sizes, grad_dtype, len(sizes) + sizes[0])
+    decay = [0.1 * (i % 3) for i in range(len(sizes))]
+    d = lambda x: [t.clone().to(DEV) for t in x]  # noqa: E731
+    dp, dg, dm, dv = d(p), d(g), d(m), d(v)
+    model = [torch.empty(n, dtype=torch.bfloat16, device=DEV) if i % 2 == 0 else None for i, n in enumerate(sizes)]
+    plan = F.AdamWTensors(dp, dg, dm, dv, model=model, weight_decay=decay)
+    F.fp4_adamw_step(plan, 3, LR, (B1, B2), EPS)
+    torch.cuda.synchronize()
+    for i in range(len(sizes)):
+        p1, m1, v1, bp, bm, bv = reference(p[i], g[i].float(), m[i], v[i], 3, decay[i])
+        assert (np.abs(f64(dm[i]) - m1) <= bm).all() and (np.abs(f64(dv[i]) - v1) <= bv).all()
+        assert (np.abs(f64(dp[i]) - p1) <= bp).all(), np.max(np.abs(f64(dp[i]) - p1) / bp)
+        if model[i] is not None:
+            assert torch.equal(model[i], dp[i].bfloat16())
+
+
+# ---- 8-bit moments: the contract's operations in NumPy -----------------------------------------------------------
+def philox(low, stream, step, seed):
+    """Words of Philox4x32-10 for counters (low, 0, stream, step)."""
+    mask = np.uint64(0xFFFFFFFF)
+    c = [low.astype(np.uint64), np.zeros_like(low, np.uint64), np.full(low.shape, stream, np.uint64),
+         np.full(low.shape, step, np.uint64)]
+    k0, k1 = seed & 0xFFFFFFFF, seed >> 32
+    for _ in range(10):
+        a, b = c[0] * np.uint64(0xD2511F53), c[2] * np.uint64(0xCD9E8D57)
+        c = [(b >> np.uint64(32)) ^ c[1] ^ np.uint64(k0), b & mask, (a >> np.uint64(32)) ^ c[3] ^ np.uint64(k1), a & mask]
+        k0, k1 = (k0 + 0x9E3779B9) & 0xFFFFFFFF, (k1 + 0xBB67AE85) & 0xFFFFFFFF
+    return c
+
+
+def random16(n, stream, step, seed):
+    j = np.arange((n + 7) // 8, dtype=np.uint64)
+    w = np.stack(philox(j, stream, step, seed), 1)
+    return np.stack((w & np.uint64(0xFFFF), w >> np.uint64(16)), 2).reshape(-1)[:n].astype(np.int64)
+
+
+def encode(a, top, mantissa, rnd):
+    """Codes and scale bytes of FP32 values, by exact integer arithmetic on value / step in 64 bits."""
+    n = a.size
+    blocks = -(-n // 128)
+    x = np.zeros(blocks * 128)
+    x[:n] = a
+    x = x.reshape(blocks, 128)
+    fin = np.isfinite(x)
+    amax = np.where(fin, np.abs(x), 0.0).max(1)
+    byte = np.zeros(blocks, np.int64)
+    for b in range(blocks):
+        e = -127
+        if amax[b] > 0:
+            e = max(-127, math.frexp(amax[b])[1] - 1 - top - 1)
+            while amax[b] > 1.75 * 2.0 ** (top + e):
+                e += 1
+        byte[b] = e + 127
+    y = np.abs(np.where(fin, x, 0.0)) * np.exp2(127.0 - byte)[:, None]
+    bias = 7 if mantissa == 3 else 15
+    least = 1 - bias
+    ex = np.maximum(np.floor(np.log2(np.maximum(y, 1e-300))), least)
+    ex = np.where(np.exp2(ex) > y, np.maximum(ex - 1, least), ex)
+    # position in steps of 2^(ex - mantissa); in FP32 after lining up with its own subnormals
+    t = y / np.exp2(ex - mantissa)
+    bits = 23 - mantissa
+    # (below 2^-126 of the lined-up pattern FP32 keeps 2^-149: the fraction in 2^-bits, nearest even)
+    frac = np.rint(t * 2.0 ** bits).astype(np.int64)
+    r = np.zeros(blocks * 128, np.int64)
+    if rnd is not None:
+        r[:n] = rnd
+        add = r.reshape(blocks, 128) << (bits - 16)
+    else:
+        add = (1 << (bits - 1)) - 1 + (frac >> bits & 1)
+    q = frac + add >> bits
+    # steps above the binade's start, as a code: subnormals have exponent field 0
+    code = np.where(ex == least, q, (ex - least).astype(np.int64) * (1 << mantissa) + q)
+    if mantissa == 2:
+        code = np.where((code == 0) & (x > 0), 1, code)
+    code = np.where(fin, code, 0x7F)
+    code = code | np.where(np.signbit(x), 0x80, 0)
+    return code.reshape(-1)[:n].astype(np.uint8), byte.astype(np.uint8)
+
+
+def step32(p, g, m, v, step, decay, gs=None):
+    f = np.float32
+    with np.errstate(all="ignore"):
+        if gs is not None:
+            g = g * f(gs)
+        m = f(B1) * m + f(1 - B1) * g
+        v = f(B2) * v + f(1 - B2) * (g * g)
+        size, root = f(LR / (1 - B1 ** step)), f(1 / math.sqrt(1 - B2 ** step))
+        p = p * f(1 - LR * decay) - size * (m / (np.sqrt(v) * root + f(EPS)))
+    return p, m, v
+
+
+def decode(code, byte, kind):
+    val = torch.from_numpy(code.copy()).view(kind).float().numpy()
+    return (val * np.exp2(byte.astype(np.float64) - 127).repeat(128)[:val.size]).astype(np.float32)
+
+
+def state8(F, p, m, v):
+    out = []
+    for a, b, c in zip(p, m, v):
+        cm, sm = encode(b.numpy(), 8, 3, None)
+        cv, sv = encode(c.numpy(), 15, 2, None)
+        out.append((cm, cv, sm, sv))
+    return out
+
+
+KINDS = (torch.float8_e4m3fn, torch.float8_e5m2)
+
+
+def to_device(states):
+    t = lambda a: torch.from_numpy(a.copy()).to(DEV)  # noqa: E731
+    return ([t(s[0]).view(KINDS[0]) for s in states], [t(s[1]).view(KINDS[1]) for s in states],
+            [t(s[2]) for s in states], [t(s[3]) for s in states])
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("sr", [True, False])
+@pytest.mark.parametrize("grad_dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("sizes", SIZES, ids=[str(len(s)) + "x" + str(s[0]) for s in SIZES])
+def test_8bit_moments_bit_for_bit(F, sizes, grad_dtype, sr):
+    p, g, m, v = make(sizes, grad_dtype, 100 + len(sizes) + sizes[0])
+    for t in m + v:
+        t *= torch.exp2(torch.randint(-12, 13, t.shape).float() * (torch.rand(t.shape) < 0.3))  # wide blocks
+    decay = [0.1 * (i % 3) for i in range(len(sizes))]
+    st = state8(F, p, m, v)
+    dm, dv, dms, dvs = to_device(st)
+    dp, dg = [t.clone().to(DEV) for t in p], [t.to(DEV) for t in g]
+    plan = F.AdamWTensors(dp, dg, dm, dv, dms, dvs, weight_decay=decay)
+    seed = (7 << 32) + 12345
+    cur = [(a.numpy(),) + s for a, s in zip(p, st)]
+    for step in (1, 2, 300):
+        F.fp4_adamw_step(plan, step, LR, (B1, B2), EPS, round_mode=F.SR if sr else F.RTN, seed=seed)
+        torch.cuda.synchronize()
+        for i, n in enumerate(sizes):
+            if n == 0:
+                continue
+            q, cm, cv, sm, sv = cur[i]
+            q, m32, v32 = step32(q, g[i].float().numpy(), decode(cm, sm, KINDS[0]), decode(cv, sv, KINDS[1]), step, decay[i])
+            cm, sm = encode(m32, 8, 3, random16(n, 2 * i, step, seed) if sr else None)
+            cv, sv = encode(v32, 15, 2, random16(n, 2 * i + 1, step, seed) if sr else None)
+            cur[i] = (q, cm, cv, sm, sv)
+            assert np.array_equal(dp[i].cpu().numpy().view(np.int32), q.view(np.int32)), (step, i)
+            assert np.array_equal(dms[i].cpu().numpy(), sm) and np.array_equal(dvs[i].cpu().numpy(), sv)
+            assert np.array_equal(dm[i].view(torch.uint8).cpu().numpy(), cm), (step, i)
+            assert np.array_equal(dv[i].view(torch.uint8).cpu().numpy(), cv), (step, i)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("sr", [True, False])
+def test_8bit_moments_near_64_bits(F, sr):
+    n = 5000
+    p, g, m, v = make([n], torch.float32, 4)
+    st = state8(F, p, m, v)
+    m0, v0 = decode(st[0][0], st[0][2], KINDS[0]), decode(st[0][1], st[0][3], KINDS[1])
+    dm, dv, dms, dvs = to_device(st)
+    dp = [p[0].clone().to(DEV)]
+    F.fp4_adamw_step(F.AdamWTensors(dp, [g[0].to(DEV)], dm, dv, dms, dvs, weight_decay=0.1), 5, LR, (B1, B2), EPS,
+                     round_mode=F.SR if sr else F.RTN, seed=3)
+    torch.cuda.synchronize()
+    p1, m1, v1, bp, bm, bv = reference(p[0], g[0], m0, v0, 5, 0.1)
+    assert (np.abs(f64(dp[0]) - p1) <= bp).all()
+    for got, scale, want, bound, kind, mant, least in ((dm, dms, m1, bm, KINDS[0], 3, -6), (dv, dvs, v1, bv, KINDS[1], 2, -14)):
+        byte = scale[0].cpu().numpy()
+        val = decode(got[0].view(torch.uint8).cpu().numpy(), byte, kind).astype(np.float64)
+        unit = np.exp2(byte.astype(np.float64) - 127).repeat(128)[:n]
+        step = np.exp2(np.maximum(np.floor(np.log2(np.maximum(np.abs(want) / unit, 1e-300))), least) - mant) * unit
+        assert (np.abs(val - want) <= step * (1.0 if sr else 0.5) * (1 + 1e-6) + bound).all()
+
+
+def test_philox_of_this_file(F, oracle_mod):
+    for low, stream, step, seed in ((0, 0, 1, 0), (77, 5, 300, (7 << 32) + 12345), (4_000_000_000, 9, 2, 1 << 63)):
+        mine = [int(w[0]) for w in philox(np.array([low], np.uint64), stream, step, seed)]
+        key = np.array([seed & 0xFFFFFFFF, seed >> 32], np.uint32)
+        ref = oracle_mod.philox4x32_10(np.array([low, 0, stream, step], np.uint32), key)
+        assert mine == [int(w) for w in ref]
+
+
+@pytest.mark.gpu
+def test_stochastic_rounding_is_unbiased_and_a_seeds_own(F):
+    # beta1 = 0, one block: m = g; 512 equal blocks draw 512 x 128 independent roundings of the same number
+    n, x = 512 * 128, 0.3
+    g = torch.full((n,), x, device=DEV)
+    g[::128] = 1.0  # fixes every block's scale: 1.0 is held exactly, 0.3 lies between two codes
+    got = {}
+    for seed in (1, 1, 2):
+        z = torch.zeros(n, device=DEV)
+        m, v, ms, vs = F.AdamWTensors.moments(z)
+        F.fp4_adamw_step(F.AdamWTensors([z], [g], [m], [v], [ms], [vs]), 1, LR, (0.0, B2), EPS, seed=seed)
+        val = decode(m.view(torch.uint8).cpu().numpy(), ms.cpu().numpy(), KINDS[0])
+        if seed in got:
+            assert np.array_equal(got[seed], val)
+        got[seed] = val
+        rest = val.reshape(512, 128)[:, 1:].astype(np.float64)
+        step = 2.0 ** -5  # 0.3 in [2^-2, 2^-1): steps of 2^-2 / 8
+        frac = x / step - math.floor(x / step)
+        sigma = step * math.sqrt(frac * (1 - frac) / rest.size)
+        assert abs(rest.mean() - x) < 6 * sigma + x * 2.0 ** -16
+    assert not np.array_equal(got[1], got[2])
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("bits", [8, 32])
+def test_unaligned_tensors_match_aligned_ones(F, bits):
+    n = 3001
+    p, g, m, v = make([n], torch.bfloat16, 8)
+
+    def run(offset):
+        def place(t):
+            buf = torch.zeros(n + 64, dtype=torch.uint8 if t.element_size() == 1 else t.dtype, device=DEV)
+            out = buf[offset:offset + n]
+            if t.element_size() == 1:
+                out = out.view(t.dtype)
+            out.copy_(t.to(DEV))
+            return out
+        dp, dg = place(p[0]), place(g[0])
+        model = place(torch.zeros(n, dtype=torch.bfloat16))
+        if bits == 32:
+            dm, dv, s = place(m[0]), place(v[0]), (None, None)
+            plan = F.AdamWTensors([dp], [dg], [dm], [dv], model=[model])
+        else:
+            cm, cv, sm, sv = to_device(state8(F, p, m, v))
+            dm, dv, s = place(cm[0]), place(cv[0]), (sm, sv)
+            plan = F.AdamWTensors([dp], [dg], [dm], [dv], sm, sv, model=[model])
+        F.fp4_adamw_step(plan, 2, LR, seed=5)
+        torch.cuda.synchronize()
+        byte = lambda t: t.contiguous().view(torch.uint8).cpu()  # noqa: E731
+        return [byte(t) for t in (dp, dm, dv, model)]
+
+    for a, b in zip(run(0), run(3)):
+        assert torch.equal(a, b)
+
+
+@pytest.mark.gpu
+def test_grad_scale_and_skipped_steps(F):
+    p, g, m, v = make([1000], torch.float32, 2)
+    for gs in (0.25, math.nan, math.inf, -math.inf):
+        dp, dm, dv = [p[0].clone().to(DEV)], [m[0].clone().to(DEV)], [v[0].clone().to(DEV)]
+        plan = F.AdamWTensors(dp, [g[0].to(DEV)], dm, dv)
+        F.fp4_adamw_step(plan, 4, LR, (B1, B2), EPS, grad_scale=torch.tensor([gs], device=DEV))
+        torch.cuda.synchronize()
+        if math.isfinite(gs):
+            p1, m1, v1, bp, bm, bv = reference(p[0], g[0], m[0], v[0], 4, 0.0, gs)
+            assert (np.abs(f64(dp[0]) - p1) <= bp).all() and (np.abs(f64(dm[0]) - m1) <= bm).all()
+        else:
+            assert torch.equal(dp[0].cpu(), p[0]) and torch.equal(dm[0].cpu(), m[0]) and torch.equal(dv[0].cpu(), v[0])
+
+
+@pytest.mark.gpu
+def test_numbers_that_are_not_finite_stay_with_their_element(F):
+    n = 256
+    p, g, m, v = make([n], torch.float32, 6)
+    g[0][5], g[0][9], g[0][200] = math.nan, math.inf, 1e30
+    st = state8(F, p, m, v)
+    dm, dv, dms, dvs = to_device(st)
+    dp = [p[0].clone().to(DEV)]
+    F.fp4_adamw_step(F.AdamWTensors(dp, [g[0].to(DEV)], dm, dv, dms, dvs), 2, LR, (B1, B2), EPS, round_mode=F.RTN)
+    torch.cuda.synchronize()
+    q, m32, v32 = step32(p[0].numpy(), g[0].numpy(), decode(st[0][0], st[0][2], KINDS[0]),
+                         decode(st[0][1], st[0][3], KINDS[1]), 2, 0.0)
+    cm, sm = encode(m32, 8, 3, None)
+    cv, sv = encode(v32, 15, 2, None)
+    bad = [5, 9]
+    got = dm[0].view(torch.uint8).cpu().numpy()
+    assert list(got[bad] & 0x7F) == [0x7F, 0x7F]
+    keep = np.setdiff1d(np.arange(n), bad)
+    assert np.array_equal(got[keep], cm[keep]) and np.array_equal(dms[0].cpu().numpy(), sm)
+    assert np.array_equal(dv[0].view(torch.uint8).cpu().numpy()[keep], cv[keep])
+    assert np.array_equal(dp[0].cpu().numpy()[keep], q[keep])
+
+
+@pytest.mark.gpu
+def test_more_tensors_than_one_launch_holds(F):
+    sizes = [3 + i % 5 for i in range(901)]
+    p, g, m, v = make(sizes, torch.float32, 12)
+    d = lambda x: [t.clone().to(DEV) for t in x]  # noqa: E731
+    dp = d(p)
+    st = state8(F, p, m, v)
+    dm, dv, dms, dvs = to_device(st)
+    plan = F.AdamWTensors(dp, d(g), dm, dv, dms, dvs)
+    n = F.fp4_launch_count()
+    F.fp4_adamw_step(plan, 1, LR, (B1, B2), EPS, seed=9)
+    torch.cuda.synchronize()
+    assert F.fp4_launch_count() - n == 3
+    for i in (0, 399, 400, 799, 800, 900):
+        q, m32, v32 = step32(p[i].numpy(), g[i].numpy(), decode(st[i][0], st[i][2], KINDS[0]),
+                             decode(st[i][1], st[i][3], KINDS[1]), 1, 0.0)
+        cm, _ = encode(m32, 8, 3, random16(sizes[i], 2 * i, 1, 9))
+        assert np.array_equal(dp[i].cpu().numpy(), q) and np.array_equal(dm[i].view(torch.uint8).cpu().numpy(), cm)
+    F.fp4_adamw_step(F.AdamWTensors([], [], [], []), 1, LR)
+    assert F.fp4_launch_count() - n == 3
+
+
+def test_refusals(F):
+    # host-side checks only; nothing is launched
+    L, a = F.lib(), 1 << 20
+    c = (F.CAdamWTensor * 1)()
+
+    def call(bits=8, dtype=0, lr=1e-3, b1=0.9, b2=0.95, eps=1e-8, step=1, mode=1, gs=None, n=1, **t):
+        f = dict(param=a, grad=a, m=a, v=a, m_scale=a, v_scale=a, model=None, numel=128, weight_decay=0.0)
+        f.update(t)
+        for k, x in f.items():
+            setattr(c[0], k, x)
+        return L.fp4_adamw_step(c, n, dtype, bits, lr, b1, b2, eps, step, mode, 0, gs, None)
+
+    bad = F.FP4_ERR_INVALID_ARG
+    assert call(bits=4) == bad and call(dtype=3) == bad and call(mode=2) == bad and call(n=-1) == bad
+    assert call(lr=-1.0) == bad and call(lr=math.nan) == bad and call(eps=-1.0) == bad
+    assert call(b1=1.0) == bad and call(b2=-0.1) == bad and call(step=0) == bad and call(step=1 << 32) == bad
+    assert call(numel=-1) == bad and call(weight_decay=math.inf) == bad
+    for name in ("param", "grad", "m", "v", "m_scale", "v_scale"):
+        assert call(**{name: None}) == bad
+    mis = F.FP4_ERR_MISALIGNED
+    assert call(param=a + 2) == mis and call(grad=a + 1) == mis and call(model=a + 1) == mis and call(gs=a + 2) == mis
+    assert call(bits=32, m=a + 2) == mis and call(dtype=1, grad=a + 2) == mis
+    assert call(numel=1 << 41) == F.FP4_ERR_UNSUPPORTED_SHAPE
+    assert L.fp4_adamw_step(None, 1, 0, 8, 1e-3, 0.9, 0.95, 1e-8, 1, 1, 0, None, None) == bad
+    assert call(numel=0, param=None) == F.FP4_OK and call(n=0) == F.FP4_OK
+    z = torch.zeros(4)
+    with pytest.raises(ValueError):
+        F.AdamWTensors([z], [z], [z], [z])  # not on a GPU
+    with pytest.raises(ValueError):
+        F.AdamWTensors([z], [], [z], [z])

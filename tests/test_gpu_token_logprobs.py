@@ -1,0 +1,364 @@
+"""Token log probabilities, entropy, top alternatives and their gradient against the definitions in 64 bits.
+
+Bounds.  With x2 = (z - m) log2(e) / T the kernel forms each term 2^x2 from an x2 that carries the rounding of the
+difference, of the constant and of the product (3 2^-24 |x2|) and an exponential good to 2^-22; a thread adds at most
+V / 512 + 16 terms one after the other (each addition 2^-24), and the joins add a few more.  So
+  |S' / S - 1| <= tS = 2^-22 + 3 2^-24 mean|x2| + (V / 512 + 64) 2^-24       (mean under p),
+ln S errs by tS + 2^-23 |ln S|, a log probability by that and 2^-22 |x|, the entropy by (2 + mean|x|) (tS + 2^-22), and an
+entry of the gradient by (|A| + |B x|) p (tS + 2^-21 + 2^-22 |x|), and half a step of its type."""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+DEV = "cuda"
+INF = math.inf
+
+
+@pytest.fixture(scope="module")
+def F():
+    import __graft_entry__
+    __graft_entry__.build()
+    import nvfp4_quantized_pretraining_gb300 as F
+    return F
+
+
+def make(T, V, dtype, seed, masked=False, scale=3.0):
+    g = torch.Generator().manual_seed(seed)
+    z = torch.randn((T, V), generator=g) * scale
+    targets = torch.randint(0, V, (T,), generator=g)
+    if masked:
+        z[torch.rand((T, V), generator=g) < 0.4] = -INF
+        targets[::5] = -100
+    return z.to(dtype).to(DEV), targets.to(DEV)
+
+
+def reference(z, targets, temperature, top_k):
+    """All outputs in 64 bits, and the bounds' means."""
+    a = z.double().cpu().numpy()
+    T, V = a.shape
+    with np.errstate(all="ignore"):
+        m = a.max(1)
+        empty = np.isneginf(m)
+        x = np.where(np.isneginf(a), -INF, (a - np.where(empty, 0.0, m)[:, None]) / temperature)
+        e = np.exp(x)
+        S = e.sum(1)
+        ln_s = np.log(S)
+        p = np.where(empty[:, None], 0.0, e / S[:, None])
+        px = np.where(np.isneginf(a), 0.0, p * x)
+        H = np.where(empty, 0.0, ln_s - px.sum(1))
+        lp = np.where(np.isneginf(a), -INF, x - ln_s[:, None])
+    t = targets.cpu().numpy()
+    logprob = np.where(t < 0, 0.0, lp[np.arange(T), np.maximum(t, 0)])
+    # largest first, equal ones by the lower index
+    order = np.argsort(-a, axis=1, kind="stable")[:, :top_k]
+    mean_x = -px.sum(1)
+    tS = 2.0 ** -22 + 3 * 2.0 ** -24 * mean_x / math.log(2) + (V / 512 + 64) * 2.0 ** -24
+    return dict(m=m, S=S, ln_s=ln_s, p=p, x=x, H=H, lp=lp, logprob=logprob, order=order, mean_x=mean_x, tS=tS,
+                empty=empty, targets=t, a=a)
+
+
+def near(got, want, bound, what):
+    got = got.double().cpu().numpy()
+    same = (got == want) | (np.isnan(got) & np.isnan(want))
+    with np.errstate(invalid="ignore"):
+        ok = same | (np.abs(got - want) <= bound)
+    assert ok.all(), f"{what}: {int((~ok).sum())} beyond the bound; got {got[~ok][:3]}, want {want[~ok][:3]}"
+
+
+def check_forward(F, z, targets, temperature=1.0, top_k=0):
+    r = F.fp4_token_logprobs(z, targets, top_k=top_k, temperature=temperature)
+    torch.cuda.synchronize()
+    w = reference(z, targets, temperature, top_k)
+    T = z.shape[0]
+    with np.errstate(invalid="ignore"):
+        d_ln = w["tS"] + 2.0 ** -23 * np.abs(w["ln_s"])
+        x_t = np.where(w["targets"] < 0, 0.0, w["x"][np.arange(T), np.maximum(w["targets"], 0)])
+        near(r.stats[:, 0], w["m"], 0.0, "max")
+        near(r.stats[:, 1], w["S"], w["tS"] * w["S"], "sum")
+        near(r.logprob, w["logprob"], d_ln + 2.0 ** -22 * np.abs(x_t), "logprob")
+        near(r.entropy, w["H"], (2 + w["mean_x"]) * (w["tS"] + 2.0 ** -22) + 2.0 ** -23 * np.abs(w["ln_s"]), "entropy")
+        assert tuple(r.top_index.shape) == (T, top_k)
+        if top_k:
+            assert np.array_equal(r.top_index.cpu().numpy(), w["order"])
+            x_k = np.take_along_axis(w["x"], w["order"], 1)
+            near(r.top_logprob, np.take_along_axis(w["lp"], w["order"], 1), d_ln[:, None] + 2.0 ** -22 * np.abs(x_k),
+                 "top_logprob")
+    return r, w
+
+
+SHAPES = [(1, 1), (3, 2), (2, 7), (1, 31), (5, 64), (4, 1000), (2, 1001), (1, 4099), (3, 8192), (1, 50021), (2, 131072),
+          (7, 32000), (160, 2049), (700, 513), (1, 300001)]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("T,V", SHAPES)
+def test_forward(F, T, V, dtype):
+    z, targets = make(T, V, dtype, T * 1000 + V)
+    for top_k in {0, 1, min(V, 5), min(V, 32)}:
+        check_forward(F, z, targets, 1.0, top_k)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("temperature", [0.1, 0.7, 3.0])
+def test_temperature_and_masks(F, dtype, temperature):
+    z, targets = make(6, 3001, dtype, 9, masked=True)
+    z[2] = -INF
+    check_forward(F, z, targets, temperature, 20)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_rows_at_the_edge(F, dtype):
+    V = 2500
+    low = torch.finfo(dtype).min
+    z = torch.zeros((9, V), dtype=dtype, device=DEV)  # row 0: all equal
+    z[1] = low            # the type's lowest value throughout
+    z[2] = -INF           # nothing allowed
+    z[3] = -INF
+    z[3, 1234] = 2.0      # one token allowed
+    z[4] = low
+    z[4, V - 1] = 0.0     # lowest values used as a mask
+    z[5, ::2] = -0.0      # signed zeros are equal
+    z[6] = torch.arange(V, device=DEV).to(dtype)          # ascending: the largest sit together, with ties in BF16
+    z[7] = torch.arange(V, 0, -1, device=DEV).to(dtype)
+    z[8] = 30000.0
+    z[8, 7] = 30208.0
+    targets = torch.tensor([5, 7, 3, 1234, V - 1, 1, V - 1, 0, 7], device=DEV)
+    for k in (1, 8, 32):
+        check_forward(F, z, targets, 1.0, k)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_many_equal_logits_give_the_lowest_indices(F, dtype):
+    # over a thousand ties at the threshold, and the winners all inside one thread's share
+    z = torch.full((3, 40000), -1.0, dtype=dtype, device=DEV)
+    z[0, 20000:22000] = 4.0
+    z[1, 100:108] = 9.0
+    z[1, 39990:] = 9.0
+    z[2, 12345] = 1.0
+    targets = torch.tensor([20000, 100, 0], device=DEV)
+    check_forward(F, z, targets, 1.0, 32)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_nan_and_infinity(F, dtype):
+    V = 5000
+    z, _ = make(4, V, dtype, 3)
+    z[0, 17] = math.nan
+    z[1, 4000] = INF
+    z[1, 4990] = math.nan
+    z[2] = -INF
+    z[2, 9] = math.nan
+    targets = torch.tensor([1, 2, 3, V], device=DEV)  # (the last one is out of range)
+    r = F.fp4_token_logprobs(z, targets, top_k=3)
+    torch.cuda.synchronize()
+    assert torch.isnan(r.logprob).all()
+    assert torch.isnan(r.entropy[:3]).all() and torch.isfinite(r.entropy[3])
+    assert torch.isnan(r.stats[:3]).all() and torch.isnan(r.top_logprob[:3]).all()
+    top = r.top_index.cpu().numpy()
+    assert top[0, 0] == 17 and list(top[1, :2]) == [4990, 4000] and list(top[2]) == [9, 0, 1]
+    want = np.argsort(-z[0].double().cpu().numpy()[np.arange(V) != 17], kind="stable")[:2]
+    assert list(top[0, 1:]) == [int(i + (i >= 17)) for i in want]
+    d = F.fp4_token_logprobs_bwd(z, r, targets, g_logprob=torch.ones(4, device=DEV))
+    torch.cuda.synchronize()
+    assert torch.isnan(d).all()
+
+
+def reference_gradient(w, temperature, gl, gh, gt, top_index):
+    T, V = w["a"].shape
+    t = w["targets"]
+    own = np.zeros((T, V))
+    rows = np.arange(T)
+    gl = np.where(t < 0, 0.0, gl) if gl is not None else np.zeros(T)
+    np.add.at(own, (rows, np.maximum(t, 0)), gl)
+    G = gl.copy()
+    if gt is not None:
+        np.add.at(own, (rows[:, None], top_index), gt)
+        G = G + gt.sum(1)
+    gh = np.zeros(T) if gh is None else gh
+    with np.errstate(invalid="ignore"):
+        lnp = np.where(w["p"] > 0, w["lp"], 0.0)
+        a = -G[:, None] - gh[:, None] * (lnp + w["H"][:, None])
+        d = np.where(np.isneginf(w["a"]), 0.0, (w["p"] * a + own) / temperature)
+        x = np.where(np.isneginf(w["a"]), 0.0, w["x"])
+        size = (np.abs(G) + np.abs(gh) * (np.abs(w["H"]) + np.where(w["empty"], 0.0, np.abs(w["ln_s"]))))[:, None]
+        bound = w["p"] * (size + np.abs(gh[:, None] * x)) / temperature * \
+            (w["tS"][:, None] + 2.0 ** -21 + 2.0 ** -22 * np.abs(x)) + 2.0 ** -23 * np.abs(own) / temperature
+    return d, np.where(w["empty"][:, None], 0.0, bound) + 1e-37
+
+
+def check_backward(F, z, targets, temperature, top_k, use, in_place=False, pad=0):
+    T, V = z.shape
+    g = torch.Generator().manual_seed(T + V)
+    gl = torch.randn(T, generator=g).to(DEV) if "l" in use else None
+    gh = torch.randn(T, generator=g).to(DEV) * 0.3 if "h" in use else None
+    gt = torch.randn((T, top_k), generator=g).to(DEV) if "t" in use else None
+    r = F.fp4_token_logprobs(z, targets, top_k=top_k, temperature=temperature)
+    w = reference(z, targets, temperature, top_k)
+    out = None
+    if in_place:
+        out = z
+    elif pad:
+        out = torch.empty((T, V + pad), dtype=z.dtype, device=DEV)[:, :V]
+    d = F.fp4_token_logprobs_bwd(z, r, targets, g_logprob=gl, g_entropy=gh, g_top=gt, dlogits=out)
+    torch.cuda.synchronize()
+    n = lambda a: None if a is None else a.double().cpu().numpy()  # noqa: E731
+    want, bound = reference_gradient(w, temperature, n(gl), n(gh), n(gt), w["order"])
+    half = 2.0 ** -8 if z.dtype == torch.bfloat16 else 2.0 ** -23
+    near(d, want, bound * (1 + half) + half * np.abs(want), "dlogits")
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("T,V", [(1, 1), (3, 7), (2, 1001), (4, 8192), (1, 50021), (3, 32000), (150, 520)])
+def test_backward(F, T, V, dtype):
+    z, targets = make(T, V, dtype, T + 7 * V)
+    k = min(V, 6)
+    for use, top in (("l", 0), ("lh", 0), ("lht", k), ("t", k), ("h", k)):
+        check_backward(F, z, targets, 1.0, top, use)
+    check_backward(F, z.clone(), targets, 0.6, k, "lht", in_place=True)
+    check_backward(F, z.clone(), targets, 0.6, 0, "lh", in_place=True)
+    check_backward(F, z, targets, 1.0, k, "lht", pad=3)  # rows aligned differently from the logits'
+    check_backward(F, z, targets, 1.0, 0, "lh", pad=3)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_backward_with_masks_and_equal_entries(F, dtype):
+    z, targets = make(8, 3001, dtype, 5, masked=True)
+    z[3] = -INF
+    targets[6] = int(z[6].float().argmax())  # the target among the top entries
+    targets[7] = int((z[7] == -INF).nonzero()[0])  # a banned target
+    for use, top in (("lh", 0), ("lht", 32), ("t", 1)):
+        check_backward(F, z, targets, 0.8, top, use)
+
+
+@pytest.mark.gpu
+def test_gradient_against_differences(F):
+    # the forward kernel's own FP32 results, differenced: a loss of T rows, a random direction of length h
+    T, V, temperature, k = 6, 2003, 0.9, 4
+    g = torch.Generator().manual_seed(1)
+    z = (torch.randn((T, V), generator=g) * 2).to(DEV)
+    z.scatter_(1, torch.arange(k, device=DEV).repeat(T, 1) * 400 + 3, 9.0 + torch.arange(k, device=DEV).repeat(T, 1).float())
+    targets = torch.randint(0, V, (T,), generator=g).to(DEV)
+    gl, gh, gt = (torch.randn(s, generator=g).to(DEV) for s in ((T,), (T,), (T, k)))
+    direction = torch.randn((T, V), generator=g).to(DEV)
+
+    def loss(a):
+        r = F.fp4_token_logprobs(a, targets, top_k=k, temperature=temperature)
+        return float((gl * r.logprob).double().sum() + (gh * r.entropy).double().sum() + (gt * r.top_logprob).double().sum())
+
+    r = F.fp4_token_logprobs(z, targets, top_k=k, temperature=temperature)
+    d = F.fp4_token_logprobs_bwd(z, r, targets, g_logprob=gl, g_entropy=gh, g_top=gt)
+    want = float((d.double() * direction.double()).sum())
+    h = 1e-2
+    got = (loss(z + h * direction) - loss(z - h * direction)) / (2 * h)
+    # third-derivative term h^2, and the forward's rounding (T (k + 2) values near 10, 2^-20 each) over h
+    assert abs(got - want) <= 2e-2 * max(1.0, abs(want)), (got, want)
+
+
+@pytest.mark.gpu
+def test_strides_streams_and_repeats(F):
+    big = torch.randn((40, 3003), device=DEV)
+    targets = torch.randint(0, 2999, (20,), device=DEV)
+    for z in (big[::2, 2:3001], big[:20, :2999], big.bfloat16()[::2, 3:3002], big[5:6, 1:3000]):
+        t = targets[:z.shape[0]]
+        r, _ = check_forward(F, z, t, 1.0, 7)
+        again = F.fp4_token_logprobs(z, t, top_k=7)
+        assert torch.equal(r.stats, again.stats) and torch.equal(r.entropy, again.entropy)
+        assert torch.equal(r.logprob, again.logprob) and torch.equal(r.top_logprob, again.top_logprob)
+        check_backward(F, z, t, 1.0, 7, "lht")
+    side = torch.cuda.Stream()
+    z = big[:, :3000].contiguous()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        r = F.fp4_token_logprobs(z, None, top_k=2, entropy=False)
+    side.synchronize()
+    assert r.logprob is None and r.entropy is None
+    assert torch.equal(r.stats[:, 0], z.amax(1)) and torch.equal(r.top_index[:, 0], z.argmax(1))
+
+
+@pytest.mark.gpu
+def test_a_row_beyond_32_bit_offsets(F):
+    # the last rows start more than 2^32 bytes and 2^31 elements into the tensor
+    T, V = 70000, 32000
+    z = torch.zeros((T, V), dtype=torch.bfloat16, device=DEV)
+    rows = [0, 33553, 67108, 67109, T - 1]
+    for i, r in enumerate(rows):
+        z[r, 100 * i + 5] = 5.0
+    targets = torch.full((T,), -1, dtype=torch.int64, device=DEV)
+    for i, r in enumerate(rows):
+        targets[r] = 100 * i + 5
+    got = F.fp4_token_logprobs(z, targets, top_k=1)
+    d = F.fp4_token_logprobs_bwd(z, got, targets, g_logprob=torch.ones(T, device=DEV), dlogits=z)
+    torch.cuda.synchronize()
+    want = 5.0 - math.log(math.exp(5.0) + V - 1)
+    for i, r in enumerate(rows):
+        assert abs(float(got.logprob[r]) - want) < 1e-4 and int(got.top_index[r, 0]) == 100 * i + 5
+        assert abs(float(d[r, 100 * i + 5]) - (1 - math.exp(want))) < 4e-3
+    assert float(d[1].abs().max()) == 0.0
+
+
+@pytest.mark.gpu
+def test_no_rows(F):
+    z = torch.empty((0, 100), device=DEV)
+    t = torch.empty(0, dtype=torch.int64, device=DEV)
+    n = F.fp4_launch_count()
+    r = F.fp4_token_logprobs(z, t, top_k=3)
+    d = F.fp4_token_logprobs_bwd(z, r, t, g_logprob=torch.empty(0, device=DEV))
+    assert r.top_index.shape == (0, 3) and d.shape == (0, 100) and F.fp4_launch_count() == n
+
+
+def test_refusals(F):
+    # host-side checks only; nothing is launched
+    L, p = F.lib(), 1 << 20
+    ok = [p, 0, 4, 100, 100, 1.0, p, 5, p, p, p, p, p, None]
+
+    def call(**change):
+        a = list(ok)
+        for k, v in change.items():
+            a[int(k[1:])] = v
+        return L.fp4_token_logprobs(*a)
+
+    assert call(_0=None) == F.FP4_ERR_INVALID_ARG
+    assert call(_1=2) == F.FP4_ERR_INVALID_ARG
+    assert call(_2=-1) == F.FP4_ERR_INVALID_ARG
+    assert call(_2=1 << 28) == F.FP4_ERR_UNSUPPORTED_SHAPE
+    assert call(_3=0) == F.FP4_ERR_INVALID_ARG
+    assert call(_3=1 << 31, _4=1 << 31) == F.FP4_ERR_UNSUPPORTED_SHAPE
+    assert call(_4=99) == F.FP4_ERR_INVALID_ARG
+    for bad in (0.0, -1.0, math.inf, math.nan, 1e-45):
+        assert call(_5=bad) == F.FP4_ERR_INVALID_ARG
+    assert call(_6=None) == F.FP4_ERR_INVALID_ARG and call(_8=None) == F.FP4_ERR_INVALID_ARG
+    assert call(_7=33) == F.FP4_ERR_INVALID_ARG and call(_7=-1) == F.FP4_ERR_INVALID_ARG
+    assert call(_3=3, _4=3, _7=4) == F.FP4_ERR_INVALID_ARG
+    assert call(_10=None) == F.FP4_ERR_INVALID_ARG
+    assert call(_11=None) == F.FP4_ERR_INVALID_ARG and call(_12=None) == F.FP4_ERR_INVALID_ARG
+    assert call(_0=p + 1) == F.FP4_ERR_MISALIGNED and call(_1=1, _0=p + 2) == F.FP4_ERR_MISALIGNED
+    assert call(_12=p + 4) == F.FP4_ERR_MISALIGNED and call(_10=p + 4) == F.FP4_ERR_MISALIGNED
+    assert "aligned" in F.fp4_last_error()
+    ok = [p, 0, 4, 100, 100, 1.0, p, p, p, p, p, 5, p, p, 2 * p, 100, None]
+    L_bwd = L.fp4_token_logprobs_bwd
+
+    def bwd(**change):
+        a = list(ok)
+        for k, v in change.items():
+            a[int(k[1:])] = v
+        return L_bwd(*a)
+
+    assert bwd(_7=None) == F.FP4_ERR_INVALID_ARG          # stats
+    assert bwd(_6=None) == F.FP4_ERR_INVALID_ARG          # g_logprob without targets
+    assert bwd(_8=None) == F.FP4_ERR_INVALID_ARG          # g_entropy without entropy
+    assert bwd(_12=None) == F.FP4_ERR_INVALID_ARG         # g_top without top_index
+    assert bwd(_14=None) == F.FP4_ERR_INVALID_ARG
+    assert bwd(_14=p, _15=104) == F.FP4_ERR_INVALID_ARG   # in place with another pitch
+    assert bwd(_15=99) == F.FP4_ERR_INVALID_ARG
+    assert bwd(_14=2 * p + 1) == F.FP4_ERR_MISALIGNED
+    with pytest.raises(ValueError):
+        F.fp4_token_logprobs(torch.zeros((2, 3)))
