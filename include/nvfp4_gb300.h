@@ -360,6 +360,60 @@ fp4_status fp4_qadamw_v_decode(const fp4_tensor* in, const uint16_t* mean, float
                                int64_t ldo, void* stream);
 
 /* ---------------------------------------------------------------------------
+ * FP8 linear layer, one scale per block of 128: for the projections that a
+ * recipe keeps out of 4 bits (language-model head, sensitive layers).
+ *
+ * An FP8 tensor of rows x cols:
+ *   codes:  E4M3, rows x fp4_fp8_code_pitch(cols) bytes (cols rounded up to 128), row-major,
+ *           zeros past cols.
+ *   scales: fp4_fp8_scale_bytes(rows, cols) bytes: byte b of (row r, block k of 128 columns) stands
+ *           for 2^(b - 127) (UE8M0).  In the layout the tensor core reads: 128-row x 4-block atoms of
+ *           512 bytes, ordered by 128-row block, then by group of 4 blocks; inside an atom byte
+ *           (r % 32) * 16 + ((r % 128) / 32) * 4 + k % 4.  Padding bytes are zero.
+ * Both device pointers, 16-byte aligned.  A block's scale is the least power of two (not below
+ * 2^-127) with which its largest finite magnitude is at most 448; code = E4M3_rn(x / scale), exact
+ * but for that one rounding.  Inf and NaN become NaN and take no part in the scale. */
+typedef struct {
+    void* codes;
+    void* scales;
+    int64_t rows;
+    int64_t cols;
+} fp4_fp8_tensor;
+int64_t fp4_fp8_code_pitch(int64_t cols);
+int64_t fp4_fp8_scale_bytes(int64_t rows, int64_t cols);
+
+/* x (rows x cols BF16, row pitch ld, any sizes from 1, aligned to its element; 16-byte aligned rows are
+ * read in wide accesses) to FP8, from one read.  block_rows 1: blocks of 1 x 128 along each output's rows
+ * (activations, gradients); 128: blocks of 128 x 128 (weights; the two forms then hold the same values).
+ * out_row: rows x cols; out_col: cols x rows, the transposed tensor.  Either may be NULL. */
+fp4_status fp4_fp8_quantize(const void* x, int64_t rows, int64_t cols, int64_t ld, int block_rows,
+                            const fp4_fp8_tensor* out_row, const fp4_fp8_tensor* out_col, void* stream);
+
+/* C (M x N, BF16 or FP32 by c_dtype, row pitch ldc) = A B^T of the values of A (M x K) and B (N x K):
+ * exact products, FP32 accumulation, one rounding.  Any M, N, K from 1.  C aligned to its element;
+ * with 16-byte aligned rows it is written in wide accesses. */
+fp4_status fp4_fp8_gemm(const fp4_fp8_tensor* A, const fp4_fp8_tensor* B, void* C, int c_dtype, int64_t ldc,
+                        void* stream);
+
+/* Y (M x N BF16) = X W^T: X (M x K BF16, pitch ldx) quantized in blocks of 1 x 128, Wq N x K (blocks of
+ * 128 x 128 or 1 x 128).  xqT_saved (K x M, caller-owned; NULL: not wanted) receives X's column form for
+ * dW.  M = 0 without xqT_saved is a call without work.
+ * ws: fp4_fp8_linear_fwd_workspace(M, N, K) bytes, 256-byte aligned, scratch. */
+size_t fp4_fp8_linear_fwd_workspace(int64_t M, int64_t N, int64_t K);
+fp4_status fp4_fp8_linear_fwd(const void* X, int64_t M, int64_t K, int64_t ldx, const fp4_fp8_tensor* Wq, void* Y,
+                              int64_t ldy, const fp4_fp8_tensor* xqT_saved, void* ws, size_t ws_bytes,
+                              void* stream);
+
+/* dX (M x K BF16) = dY W with WqT (K x N), dW (N x K, BF16 or FP32) = dY^T X with xqT_saved (K x M):
+ * dY (M x N BF16, pitch lddy) quantized in blocks of 1 x 128 along N for dX, and of 128 tokens for dW.
+ * dX or dW may be NULL (not wanted; its operand is then not looked at).
+ * ws: fp4_fp8_linear_bwd_workspace(M, N, K) bytes, 256-byte aligned, scratch. */
+size_t fp4_fp8_linear_bwd_workspace(int64_t M, int64_t N, int64_t K);
+fp4_status fp4_fp8_linear_bwd(const void* dY, int64_t M, int64_t N, int64_t lddy, const fp4_fp8_tensor* WqT,
+                              const fp4_fp8_tensor* xqT_saved, void* dX, int64_t lddx, void* dW, int dw_dtype,
+                              int64_t lddw, void* ws, size_t ws_bytes, void* stream);
+
+/* ---------------------------------------------------------------------------
  * Token log probabilities (the loss on a language model's logits, and what a
  * server reports beside its tokens).  For row t of logits z (T x V, BF16 or
  * FP32 by `dtype`, FP4_OUT_BF16 / FP4_OUT_F32; row pitch ld elements) and the

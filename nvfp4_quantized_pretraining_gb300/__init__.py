@@ -37,7 +37,9 @@ EXPORTS = ["fp4_scale_bytes", "fp4_amax", "fp4_quantize", "fp4_quantize_transpos
            "fp4_linear_fwd", "fp4_linear_fwd_noalloc", "fp4_linear_bwd", "fp4_lora_factor_grad_workspace",
            "fp4_lora_factor_grad", "fp4_lora_cholqr_workspace", "fp4_lora_cholqr", "fp4_lora_realign_workspace",
            "fp4_lora_realign", "fp4_newton_schulz_workspace", "fp4_newton_schulz", "fp4_qadamw_v_encode",
-           "fp4_qadamw_v_decode", "fp4_token_logprobs", "fp4_token_logprobs_bwd", "fp4_adamw_step", "fp4_check_status", "fp4_last_error", "fp4_launch_count",
+           "fp4_qadamw_v_decode", "fp4_fp8_code_pitch", "fp4_fp8_scale_bytes", "fp4_fp8_quantize", "fp4_fp8_gemm",
+           "fp4_fp8_linear_fwd_workspace", "fp4_fp8_linear_bwd_workspace", "fp4_fp8_linear_fwd",
+           "fp4_fp8_linear_bwd", "fp4_token_logprobs", "fp4_token_logprobs_bwd", "fp4_adamw_step", "fp4_check_status", "fp4_last_error", "fp4_launch_count",
            "fp4_debug_convert", "fp4_debug_sr_round", "fp4_debug_force_counter64", "fp4_mma_peak_probe"]
 
 
@@ -51,6 +53,12 @@ class CTensor(ctypes.Structure):
     """Mirror of ``fp4_tensor``."""
     _fields_ = [("codes", ctypes.c_void_p), ("scales", ctypes.c_void_p), ("scale", ctypes.c_void_p),
                 ("rows", ctypes.c_int64), ("cols", ctypes.c_int64)]
+
+
+class CFP8Tensor(ctypes.Structure):
+    """Mirror of ``fp4_fp8_tensor``."""
+    _fields_ = [("codes", ctypes.c_void_p), ("scales", ctypes.c_void_p), ("rows", ctypes.c_int64),
+                ("cols", ctypes.c_int64)]
 
 
 class CAdamWTensor(ctypes.Structure):
@@ -103,6 +111,14 @@ def lib() -> ctypes.CDLL:
                                     P]),
         "fp4_qadamw_v_encode": (i32, [P, i64, i64, i64, T, P, P]),
         "fp4_qadamw_v_decode": (i32, [T, P, P, i64, P]),
+        "fp4_fp8_code_pitch": (i64, [i64]),
+        "fp4_fp8_scale_bytes": (i64, [i64, i64]),
+        "fp4_fp8_quantize": (i32, [P, i64, i64, i64, i32, P, P, P]),
+        "fp4_fp8_gemm": (i32, [P, P, P, i32, i64, P]),
+        "fp4_fp8_linear_fwd_workspace": (ctypes.c_size_t, [i64, i64, i64]),
+        "fp4_fp8_linear_bwd_workspace": (ctypes.c_size_t, [i64, i64, i64]),
+        "fp4_fp8_linear_fwd": (i32, [P, i64, i64, i64, P, P, i64, P, P, ctypes.c_size_t, P]),
+        "fp4_fp8_linear_bwd": (i32, [P, i64, i64, i64, P, P, P, i64, P, i32, i64, P, ctypes.c_size_t, P]),
         "fp4_token_logprobs": (i32, [P, i32, i64, i64, i64, f32, P, i32, P, P, P, P, P, P]),
         "fp4_token_logprobs_bwd": (i32, [P, i32, i64, i64, i64, f32, P, P, P, P, P, i32, P, P, P, i64, P]),
         "fp4_adamw_step": (i32, [P, i32, i32, i32, f64, f64, f64, f64, i64, i32, u64, P, P]),
@@ -128,8 +144,8 @@ def _check(status: int) -> None:
 
 
 def _stream(stream) -> int:
-    if stream is None:
-        return torch.cuda.current_stream().cuda_stream
+    if stream is None:  # the current device's current stream, without building a Stream object
+        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
     if isinstance(stream, torch.cuda.Stream):
         return stream.cuda_stream
     return int(stream)
@@ -507,6 +523,161 @@ def fp4_qadamw_v_decode(q: NVFP4Tensor, mean: torch.Tensor, out: torch.Tensor | 
     ct = q.c()
     _check(lib().fp4_qadamw_v_decode(ctypes.byref(ct), mean.data_ptr(), out.data_ptr(), ldo, _stream(stream)))
     return out
+
+
+FP8_BLOCK = 128  # elements that share a scale byte
+
+
+class FP8Tensor:
+    """Device buffers of one FP8 tensor (rows x cols, one power-of-two scale per block of 128 columns).
+
+    codes: uint8 [rows, cols rounded up to 128], E4M3; scales: uint8, UE8M0 bytes in the MMA layout."""
+
+    def __init__(self, codes: torch.Tensor, scales: torch.Tensor, rows: int, cols: int):
+        self.codes, self.scales, self.rows, self.cols = codes, scales, rows, cols
+        self._c = CFP8Tensor(codes.data_ptr(), scales.data_ptr(), rows, cols)
+        self._ref = ctypes.addressof(self._c)
+
+    @staticmethod
+    def empty(rows: int, cols: int, device="cuda") -> "FP8Tensor":
+        pitch = -(-cols // FP8_BLOCK) * FP8_BLOCK
+        codes = torch.empty((rows, pitch), dtype=torch.uint8, device=device)
+        scales = torch.empty(-(-rows // 128) * -(-cols // 512) * 512, dtype=torch.uint8, device=device)
+        return FP8Tensor(codes, scales, rows, cols)
+
+    def c(self) -> int:
+        """Address of the C descriptor (valid while this object lives)."""
+        return self._ref
+
+    def values(self) -> torch.Tensor:
+        """The codes as a float8_e4m3fn view [rows, cols] (values in units of their block's scale)."""
+        return self.codes.view(torch.float8_e4m3fn)[:, :self.cols]
+
+
+def _check_fp8(q, rows: int, cols: int, device, name: str) -> None:
+    if not isinstance(q, FP8Tensor) or (q.rows, q.cols) != (rows, cols) or q.codes.device != device:
+        what = f"{q.rows} x {q.cols} on {q.codes.device}" if isinstance(q, FP8Tensor) else type(q).__name__
+        raise ValueError(f"{name} must be a {rows} x {cols} FP8Tensor on {device} (got {what})")
+
+
+def _out_2d(t, rows: int, cols: int, dtypes, device, name: str) -> torch.Tensor:
+    """``t`` checked, or a new rows x cols tensor whose rows start on 16 bytes (so that kernels store wide)."""
+    if t is not None:
+        _check_out(t, (rows, cols), dtypes, device, name)
+        return t
+    dtype = dtypes[0]
+    unit = 16 // dtype.itemsize
+    if cols % unit == 0:
+        return torch.empty((rows, cols), dtype=dtype, device=device)
+    return torch.empty((rows, -(-cols // unit) * unit), dtype=dtype, device=device)[:, :cols]
+
+
+def _pitch(t: torch.Tensor) -> int:
+    """Row pitch of a 2-D tensor; one row has its width."""
+    return t.stride(0) if t.shape[0] > 1 else max(t.shape[1], 1)
+
+
+def fp4_fp8_quantize(x: torch.Tensor, block_rows: int = 1, out: FP8Tensor | None = None, stream=None) -> FP8Tensor:
+    """BF16 x to FP8, blocks of ``block_rows`` (1: activations, 128: weights) x 128."""
+    R, C, _ = _bf16_2d(x, "x")
+    out = FP8Tensor.empty(R, C, x.device) if out is None else out
+    _check_fp8(out, R, C, x.device, "out")
+    _check(lib().fp4_fp8_quantize(x.data_ptr(), R, C, _pitch(x), block_rows, out.c(), None, _stream(stream)))
+    return out
+
+
+def fp4_fp8_quantize_transposed(x: torch.Tensor, block_rows: int = 1, out: FP8Tensor | None = None,
+                                stream=None) -> FP8Tensor:
+    """BF16 x (R x C) to the FP8 tensor of its transpose (C x R), blocks along x's rows."""
+    R, C, _ = _bf16_2d(x, "x")
+    out = FP8Tensor.empty(C, R, x.device) if out is None else out
+    _check_fp8(out, C, R, x.device, "out")
+    _check(lib().fp4_fp8_quantize(x.data_ptr(), R, C, _pitch(x), block_rows, None, out.c(), _stream(stream)))
+    return out
+
+
+def fp4_fp8_quantize_dual(x: torch.Tensor, block_rows: int = 1, out_row: FP8Tensor | None = None,
+                          out_col: FP8Tensor | None = None, stream=None):
+    """Both forms from one read of x."""
+    R, C, _ = _bf16_2d(x, "x")
+    out_row = FP8Tensor.empty(R, C, x.device) if out_row is None else out_row
+    out_col = FP8Tensor.empty(C, R, x.device) if out_col is None else out_col
+    _check_fp8(out_row, R, C, x.device, "out_row")
+    _check_fp8(out_col, C, R, x.device, "out_col")
+    _check(lib().fp4_fp8_quantize(x.data_ptr(), R, C, _pitch(x), block_rows, out_row.c(), out_col.c(),
+                                  _stream(stream)))
+    return out_row, out_col
+
+
+def fp4_fp8_gemm(A: FP8Tensor, B: FP8Tensor, out=None, out_dtype=torch.bfloat16, stream=None) -> torch.Tensor:
+    """A B^T (M x N) of two FP8 tensors with the same number of columns."""
+    dev = A.codes.device
+    _check_fp8(B, B.rows, A.cols, dev, "B")
+    if out is None and out_dtype not in (torch.bfloat16, torch.float32):
+        raise ValueError(f"out_dtype must be bfloat16 or float32 (got {out_dtype})")
+    out = _out_2d(out, A.rows, B.rows, (torch.bfloat16, torch.float32) if out is not None else (out_dtype,), dev, "out")
+    _check(lib().fp4_fp8_gemm(A.c(), B.c(), out.data_ptr(), OUT_F32 if out.dtype == torch.float32 else OUT_BF16,
+                              _pitch(out), _stream(stream)))
+    return out
+
+
+def fp8_linear_fwd_workspace(M: int, N: int, K: int) -> int:
+    return int(lib().fp4_fp8_linear_fwd_workspace(M, N, K))
+
+
+def fp8_linear_bwd_workspace(M: int, N: int, K: int) -> int:
+    return int(lib().fp4_fp8_linear_bwd_workspace(M, N, K))
+
+
+def fp4_fp8_linear_fwd(X: torch.Tensor, Wq: FP8Tensor, Y=None, xqT_saved: FP8Tensor | None = None, save: bool = True,
+                       workspace=None, stream=None):
+    """Y = X W^T (M x N BF16).  Returns (Y, xqT_saved); with ``save=False`` (inference) the column form of X for the
+    weight gradient is not made and the second value is None."""
+    M, K, _ = _bf16_2d(X, "X")
+    dev, N = X.device, Wq.rows
+    _check_fp8(Wq, N, K, dev, "Wq")
+    Y = _out_2d(Y, M, N, (torch.bfloat16,), dev, "Y")
+    if xqT_saved is None and save:
+        xqT_saved = FP8Tensor.empty(K, M, dev)
+    if xqT_saved is not None:
+        _check_fp8(xqT_saved, K, M, dev, "xqT_saved")
+    if workspace is None:
+        workspace = torch.empty(fp8_linear_fwd_workspace(M, N, K), dtype=torch.uint8, device=dev)
+    _check(lib().fp4_fp8_linear_fwd(X.data_ptr(), M, K, _pitch(X), Wq.c(), Y.data_ptr(), _pitch(Y),
+                                    None if xqT_saved is None else xqT_saved.c(), workspace.data_ptr(),
+                                    workspace.numel(), _stream(stream)))
+    return Y, xqT_saved
+
+
+def fp4_fp8_linear_bwd(dY: torch.Tensor, WqT: FP8Tensor | None, xqT_saved: FP8Tensor | None, dX=None, dW=None,
+                       dw_dtype=torch.bfloat16, workspace=None, stream=None):
+    """dX = dY W, dW = dY^T X.  Returns (dX, dW); without ``WqT`` or ``xqT_saved`` that gradient is not made (None)."""
+    M, N, _ = _bf16_2d(dY, "dY")
+    dev = dY.device
+    if WqT is None and xqT_saved is None:
+        raise ValueError("neither WqT nor xqT_saved is given")
+    K = WqT.rows if WqT is not None else xqT_saved.rows
+    if WqT is not None:
+        _check_fp8(WqT, K, N, dev, "WqT")
+        dX = _out_2d(dX, M, K, (torch.bfloat16,), dev, "dX")
+    elif dX is not None:
+        raise ValueError("dX needs WqT")
+    if xqT_saved is not None:
+        _check_fp8(xqT_saved, K, M, dev, "xqT_saved")
+        if dW is None and dw_dtype not in (torch.bfloat16, torch.float32):
+            raise ValueError(f"dw_dtype must be bfloat16 or float32 (got {dw_dtype})")
+        dW = _out_2d(dW, N, K, (torch.bfloat16, torch.float32) if dW is not None else (dw_dtype,), dev, "dW")
+    elif dW is not None:
+        raise ValueError("dW needs xqT_saved")
+    if workspace is None:
+        workspace = torch.empty(fp8_linear_bwd_workspace(M, N, K), dtype=torch.uint8, device=dev)
+    _check(lib().fp4_fp8_linear_bwd(dY.data_ptr(), M, N, _pitch(dY), None if WqT is None else WqT.c(),
+                                    None if xqT_saved is None else xqT_saved.c(), _ptr(dX),
+                                    0 if dX is None else _pitch(dX), _ptr(dW),
+                                    OUT_F32 if dW is not None and dW.dtype == torch.float32 else OUT_BF16,
+                                    0 if dW is None else _pitch(dW), workspace.data_ptr(), workspace.numel(),
+                                    _stream(stream)))
+    return dX, dW
 
 
 @dataclass

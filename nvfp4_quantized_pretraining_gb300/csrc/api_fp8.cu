@@ -1,0 +1,154 @@
+// C ABI of the FP8 linear layer: argument validation and the composition of its passes.  The contracts
+// are in include/nvfp4_gb300.h.
+#include "api_util.h"
+#include "kernels.h"
+#include "nvfp4_gb300.h"
+
+namespace nvfp4 {
+
+constexpr int64_t kMaxRows = INT64_C(65535) * 128;  // a grid dimension of 128-row tiles
+
+static fp4_status check_fp8(const fp4_fp8_tensor* t, const char* name) {
+  if (!t) return fail(FP4_ERR_INVALID_ARG, "%s is NULL", name);
+  if (!t->codes || !t->scales) return fail(FP4_ERR_INVALID_ARG, "%s has a NULL buffer", name);
+  if (!aligned16(t->codes) || !aligned16(t->scales))
+    return fail(FP4_ERR_MISALIGNED, "%s buffers must be 16-byte aligned", name);
+  if (t->rows < 1 || t->cols < 1)
+    return fail(FP4_ERR_INVALID_ARG, "%s is %lld x %lld", name, (long long)t->rows, (long long)t->cols);
+  if (t->rows > kMaxRows || t->cols > kMaxRows || t->rows > (int64_t(1) << 38) / t->cols)
+    return fail(FP4_ERR_UNSUPPORTED_SHAPE, "%s %lld x %lld too large", name, (long long)t->rows, (long long)t->cols);
+  return FP4_OK;
+}
+static fp4_status check_shape(const fp4_fp8_tensor* t, int64_t rows, int64_t cols, const char* name) {
+  if (t->rows != rows || t->cols != cols)
+    return fail(FP4_ERR_INVALID_ARG, "%s is %lld x %lld, expected %lld x %lld", name, (long long)t->rows,
+                (long long)t->cols, (long long)rows, (long long)cols);
+  return FP4_OK;
+}
+// A BF16 or FP32 matrix of any pitch, aligned to its element.
+static fp4_status check_matrix(const void* x, int64_t rows, int64_t cols, int64_t ld, int size, const char* name) {
+  if (!x) return fail(FP4_ERR_INVALID_ARG, "%s is NULL", name);
+  if (rows < 1 || cols < 1) return fail(FP4_ERR_INVALID_ARG, "%s is %lld x %lld", name, (long long)rows, (long long)cols);
+  if (ld < cols) return fail(FP4_ERR_INVALID_ARG, "%s: ld %lld < cols %lld", name, (long long)ld, (long long)cols);
+  if (!aligned_to(x, size)) return fail(FP4_ERR_MISALIGNED, "%s must be aligned to its element", name);
+  if (rows > kMaxRows || cols > kMaxRows || ld > (int64_t(1) << 40))
+    return fail(FP4_ERR_UNSUPPORTED_SHAPE, "%s %lld x %lld too large", name, (long long)rows, (long long)cols);
+  return FP4_OK;
+}
+static Fp8Out out_of(const fp4_fp8_tensor* t) {
+  return Fp8Out{t->codes, t->scales, static_cast<uint32_t>(t->cols), fp8_pitch(t->cols)};
+}
+static fp4_status check_ws(const void* ws, size_t bytes, size_t need) {
+  if (!ws || bytes < need || !aligned_to(ws, 256))
+    return fail(FP4_ERR_WORKSPACE, "workspace needs %zu bytes, 256-byte aligned (got %zu)", need, bytes);
+  return FP4_OK;
+}
+static size_t tensor_bytes(int64_t rows, int64_t cols) {
+  return round256(static_cast<size_t>(rows) * fp8_pitch(cols)) + round256(fp8_scale_size(rows, cols));
+}
+// A rows x cols tensor placed in the workspace at `at` (moved past it).
+static fp4_fp8_tensor take(uint8_t*& at, int64_t rows, int64_t cols) {
+  fp4_fp8_tensor t{at, at + round256(static_cast<size_t>(rows) * fp8_pitch(cols)), rows, cols};
+  at += tensor_bytes(rows, cols);
+  return t;
+}
+static fp4_status gemm(const fp4_fp8_tensor& A, const fp4_fp8_tensor& B, void* C, int c_dtype, int64_t ldc, cudaStream_t s) {
+  const Fp8GemmArgs g{A.codes, A.scales, B.codes, B.scales, A.rows, B.rows, A.cols, C, c_dtype == FP4_OUT_F32, ldc};
+  CUDA_TRY(launch_fp8_gemm(g, sm_count(), s));
+  return FP4_OK;
+}
+static fp4_status quantize(const void* x, int64_t rows, int64_t cols, int64_t ld, bool square, const fp4_fp8_tensor* row,
+                           const fp4_fp8_tensor* col, cudaStream_t s) {
+  Fp8Out r{}, c{};
+  if (row) r = out_of(row);
+  if (col) c = out_of(col);
+  CUDA_TRY(launch_fp8_quantize(x, rows, cols, ld, square, row ? &r : nullptr, col ? &c : nullptr, s));
+  return FP4_OK;
+}
+
+}  // namespace nvfp4
+
+using namespace nvfp4;
+
+extern "C" {
+
+int64_t fp4_fp8_code_pitch(int64_t cols) { return cols < 1 ? 0 : fp8_pitch(cols); }
+int64_t fp4_fp8_scale_bytes(int64_t rows, int64_t cols) { return rows < 1 || cols < 1 ? 0 : fp8_scale_size(rows, cols); }
+
+fp4_status fp4_fp8_quantize(const void* x, int64_t rows, int64_t cols, int64_t ld, int block_rows,
+                            const fp4_fp8_tensor* out_row, const fp4_fp8_tensor* out_col, void* stream) {
+  pdl_chain_break();  // the call's first kernel is ordered after all earlier stream work
+  fp4_status st;
+  if ((st = check_matrix(x, rows, cols, ld, 2, "x"))) return st;
+  if (block_rows != 1 && block_rows != 128) return fail(FP4_ERR_INVALID_ARG, "block_rows %d is not 1 or 128", block_rows);
+  if (!out_row && !out_col) return fail(FP4_ERR_INVALID_ARG, "no output tensor");
+  if (out_row && ((st = check_fp8(out_row, "out_row")) || (st = check_shape(out_row, rows, cols, "out_row")))) return st;
+  if (out_col && ((st = check_fp8(out_col, "out_col")) || (st = check_shape(out_col, cols, rows, "out_col")))) return st;
+  return quantize(x, rows, cols, ld, block_rows == 128, out_row, out_col, static_cast<cudaStream_t>(stream));
+}
+
+fp4_status fp4_fp8_gemm(const fp4_fp8_tensor* A, const fp4_fp8_tensor* B, void* C, int c_dtype, int64_t ldc,
+                        void* stream) {
+  pdl_chain_break();  // the call's first kernel is ordered after all earlier stream work
+  fp4_status st;
+  if ((st = check_fp8(A, "A")) || (st = check_fp8(B, "B"))) return st;
+  if (A->cols != B->cols)
+    return fail(FP4_ERR_INVALID_ARG, "A has %lld columns, B %lld", (long long)A->cols, (long long)B->cols);
+  if (c_dtype != FP4_OUT_BF16 && c_dtype != FP4_OUT_F32) return fail(FP4_ERR_INVALID_ARG, "c_dtype %d", c_dtype);
+  if ((st = check_matrix(C, A->rows, B->rows, ldc, c_dtype == FP4_OUT_F32 ? 4 : 2, "C"))) return st;
+  return gemm(*A, *B, C, c_dtype, ldc, static_cast<cudaStream_t>(stream));
+}
+
+size_t fp4_fp8_linear_fwd_workspace(int64_t M, int64_t N, int64_t K) {
+  return M < 1 || N < 1 || K < 1 ? 0 : tensor_bytes(M, K);
+}
+size_t fp4_fp8_linear_bwd_workspace(int64_t M, int64_t N, int64_t K) {
+  return M < 1 || N < 1 || K < 1 ? 0 : tensor_bytes(M, N) + tensor_bytes(N, M);
+}
+
+fp4_status fp4_fp8_linear_fwd(const void* X, int64_t M, int64_t K, int64_t ldx, const fp4_fp8_tensor* Wq, void* Y,
+                              int64_t ldy, const fp4_fp8_tensor* xqT_saved, void* ws, size_t ws_bytes, void* stream) {
+  pdl_chain_break();  // the call's first kernel is ordered after all earlier stream work
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  fp4_status st;
+  if ((st = check_fp8(Wq, "Wq"))) return st;
+  if (M == 0 && !xqT_saved) return FP4_OK;
+  if ((st = check_matrix(X, M, K, ldx, 2, "X"))) return st;
+  const int64_t N = Wq->rows;
+  if ((st = check_shape(Wq, N, K, "Wq")) || (st = check_matrix(Y, M, N, ldy, 2, "Y"))) return st;
+  if (xqT_saved && ((st = check_fp8(xqT_saved, "xqT_saved")) || (st = check_shape(xqT_saved, K, M, "xqT_saved")))) return st;
+  if ((st = check_ws(ws, ws_bytes, fp4_fp8_linear_fwd_workspace(M, N, K)))) return st;
+  uint8_t* at = static_cast<uint8_t*>(ws);
+  const fp4_fp8_tensor xq = take(at, M, K);
+  if ((st = quantize(X, M, K, ldx, false, &xq, xqT_saved, s))) return st;
+  return gemm(xq, *Wq, Y, FP4_OUT_BF16, ldy, s);
+}
+
+fp4_status fp4_fp8_linear_bwd(const void* dY, int64_t M, int64_t N, int64_t lddy, const fp4_fp8_tensor* WqT,
+                              const fp4_fp8_tensor* xqT_saved, void* dX, int64_t lddx, void* dW, int dw_dtype,
+                              int64_t lddw, void* ws, size_t ws_bytes, void* stream) {
+  pdl_chain_break();  // the call's first kernel is ordered after all earlier stream work
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  fp4_status st;
+  if ((st = check_matrix(dY, M, N, lddy, 2, "dY"))) return st;
+  if (!dX && !dW) return fail(FP4_ERR_INVALID_ARG, "neither dX nor dW");
+  if (dX) {
+    if ((st = check_fp8(WqT, "WqT")) || (st = check_shape(WqT, WqT->rows, N, "WqT"))) return st;
+    if ((st = check_matrix(dX, M, WqT->rows, lddx, 2, "dX"))) return st;
+  }
+  if (dW) {
+    if ((st = check_fp8(xqT_saved, "xqT_saved")) || (st = check_shape(xqT_saved, xqT_saved->rows, M, "xqT_saved"))) return st;
+    if (dX && xqT_saved->rows != WqT->rows)
+      return fail(FP4_ERR_INVALID_ARG, "xqT_saved has %lld rows, WqT %lld", (long long)xqT_saved->rows, (long long)WqT->rows);
+    if (dw_dtype != FP4_OUT_BF16 && dw_dtype != FP4_OUT_F32) return fail(FP4_ERR_INVALID_ARG, "dw_dtype %d", dw_dtype);
+    if ((st = check_matrix(dW, N, xqT_saved->rows, lddw, dw_dtype == FP4_OUT_F32 ? 4 : 2, "dW"))) return st;
+  }
+  if ((st = check_ws(ws, ws_bytes, fp4_fp8_linear_bwd_workspace(M, N, dX ? WqT->rows : xqT_saved->rows)))) return st;
+  uint8_t* at = static_cast<uint8_t*>(ws);
+  const fp4_fp8_tensor dyq = take(at, M, N), dyqT = take(at, N, M);
+  if ((st = quantize(dY, M, N, lddy, false, dX ? &dyq : nullptr, dW ? &dyqT : nullptr, s))) return st;
+  if (dX && (st = gemm(dyq, *WqT, dX, FP4_OUT_BF16, lddx, s))) return st;
+  return dW ? gemm(dyqT, *xqT_saved, dW, dw_dtype, lddw, s) : FP4_OK;
+}
+
+}  // extern "C"

@@ -14,6 +14,9 @@ namespace nvfp4 {
 // cuTensorMapEncodeTiled (resolved at run time).  False if the driver rejects it.
 bool make_tmap_2d(CUtensorMap* m, CUtensorMapDataType dt, const void* base, uint64_t inner, uint64_t outer,
                   uint64_t pitch_bytes, uint32_t box_inner, uint32_t box_outer, CUtensorMapSwizzle swizzle);
+// The same, encoded anew on every call.
+bool encode_tmap_2d(CUtensorMap* m, CUtensorMapDataType dt, const void* base, uint64_t inner, uint64_t outer,
+                    uint64_t pitch_bytes, uint32_t box_inner, uint32_t box_outer, CUtensorMapSwizzle swizzle);
 
 // Output buffers of one quantized tensor (device pointers).
 struct QOut {
@@ -217,5 +220,28 @@ struct LogprobBwdArgs {
   int64_t ldd;
 };
 cudaError_t launch_token_logprobs_bwd(const LogprobBwdArgs& a, int num_sms, cudaStream_t s);
+
+// FP8 blocks of 128: row pitch of the codes (a multiple of 128), scale bytes in the MMA layout.
+inline int64_t fp8_pitch(int64_t cols) { return (cols + 127) / 128 * 128; }
+inline int64_t fp8_scale_size(int64_t rows, int64_t cols) { return (rows + 127) / 128 * ((cols + 511) / 512) * 512; }
+struct Fp8Out {
+  void* codes;
+  void* scales;
+  uint32_t cols;  // the stored tensor's (for the column form: the source's rows)
+  int64_t pitch;
+};
+// x rows x cols BF16; square: one scale per 128 x 128 block, else per 1 x 128 block of each form.
+cudaError_t launch_fp8_quantize(const void* x, int64_t rows, int64_t cols, int64_t ld, bool square, const Fp8Out* row,
+                                const Fp8Out* col, cudaStream_t s);
+// C (M x N, pitch ldc) = A B^T, A M x K, B N x K.
+struct Fp8GemmArgs {
+  const void *a_codes, *a_scales, *b_codes, *b_scales;
+  int64_t M, N, K;
+  void* C;
+  int c_f32;
+  int64_t ldc;
+};
+cudaError_t launch_fp8_gemm(const Fp8GemmArgs& g, int num_sms, cudaStream_t s);
+cudaError_t fp8_status_read_clear(unsigned int* out, cudaStream_t s);
 
 }  // namespace nvfp4

@@ -1,0 +1,360 @@
+"""The FP8 linear layer, one power-of-two scale per block of 128, against 64 bits.
+
+Quantization is exact but for one rounding to E4M3, so codes and scale bytes are compared bit for bit with exact integer
+arithmetic in NumPy.  Products: the operands' values are exact on both sides; the tensor core adds K terms in FP32, each
+addition within 2^-23 of a partial sum bounded by S = sum |a b| (its adders may truncate), so an entry errs by at most
+K 2^-23 S, and by half a step of its type; 2^-8 relative for BF16, 2^-23 for FP32.  In norm: the accumulator takes K / 32
+sums, each within 2^-23 of a partial sum that is no larger than the entry's final size, and 2^-20 for what happens inside
+a sum."""
+import ctypes
+import math
+
+import numpy as np
+import pytest
+import torch
+
+DEV = "cuda"
+
+
+@pytest.fixture(scope="module")
+def F():
+    import __graft_entry__
+    __graft_entry__.build()
+    import nvfp4_quantized_pretraining_gb300 as F
+    return F
+
+
+def make(rows, cols, seed, spread=True):
+    g = torch.Generator().manual_seed(seed)
+    x = torch.randn((rows, cols), generator=g)
+    if spread:  # rows and columns of different size, so that a misplaced scale shows
+        x *= torch.exp2(torch.randint(-6, 7, (rows, 1), generator=g).float())
+        x *= torch.exp2(torch.randint(-3, 4, (cols,), generator=g).float())
+    return x.bfloat16()
+
+
+def scale_exponents(x, block_rows):
+    """Least e >= -127 with the block's largest finite magnitude at most 448 2^e, per (row block, column block)."""
+    rows, cols = x.shape
+    R, C = -(-rows // block_rows), -(-cols // 128)
+    p = np.zeros((R * block_rows, C * 128))
+    p[:rows, :cols] = np.where(np.isfinite(x), np.abs(x), 0.0)
+    amax = p.reshape(R, block_rows, C, 128).max((1, 3))
+    e = np.full(amax.shape, -127, np.int64)
+    nz = amax > 0
+    e[nz] = np.maximum(-127, np.ceil(np.log2(amax[nz] / 448.0)).astype(np.int64) - 1)
+    while True:
+        low = amax > 448.0 * np.exp2(e.astype(np.float64))
+        if not low.any():
+            return e
+        e[low] += 1
+
+
+def quantize(x, block_rows):
+    """(codes [rows, cols], exponents per row and column block, values) by counting in steps of the format."""
+    x = np.asarray(x, np.float64)
+    e = scale_exponents(x, block_rows).repeat(block_rows, 0)[:x.shape[0]]
+    full = np.exp2(e.astype(np.float64)).repeat(128, 1)[:, :x.shape[1]]
+    fin = np.isfinite(x)
+    y = np.where(fin, x, 0.0) / full
+    a = np.abs(y)
+    ex = np.maximum(np.floor(np.log2(np.maximum(a, 1e-300))), -6)
+    ex = np.where(np.exp2(ex) > a, np.maximum(ex - 1, -6), ex)
+    n = np.rint(a / np.exp2(ex - 3))  # steps; to even
+    code = ((ex + 6) * 8 + n).astype(np.int64) | np.where(np.signbit(x), 0x80, 0)
+    v = np.copysign(n * np.exp2(ex - 3), x) * full
+    code = np.where(fin, code, code | 0x7F)
+    return code.astype(np.uint8), (e + 127).astype(np.uint8), np.where(fin, v, math.nan)
+
+
+def mma_scales(byte, rows):
+    """Scale bytes [rows, column blocks] in the tensor core's layout, padding zero."""
+    R, C = -(-rows // 128), -(-byte.shape[1] // 4)
+    p = np.zeros((R * 128, C * 4), np.uint8)
+    p[:rows, :byte.shape[1]] = byte
+    # [R][4 row groups][32][C][4] -> [R][C][32][4 row groups][4]
+    return p.reshape(R, 4, 32, C, 4).transpose(0, 3, 2, 1, 4).reshape(-1)
+
+
+def check_tensor(q, x, block_rows):
+    code, byte, v = quantize(x, block_rows)
+    rows, cols = x.shape
+    assert (q.rows, q.cols) == (rows, cols)
+    got = q.codes.cpu().numpy()
+    fin = np.isfinite(x)
+    same = np.where(fin, got[:, :cols] == code, (got[:, :cols] & 0x7F) == 0x7F)
+    assert same.all(), int((~same).sum())
+    assert (got[:, cols:] == 0).all()
+    assert np.array_equal(q.scales.cpu().numpy(), mma_scales(byte, rows))
+    return v
+
+
+SHAPES = [(1, 1), (1, 128), (3, 130), (128, 128), (129, 257), (200, 1000), (77, 2048), (512, 384), (1021, 515)]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("block_rows", [1, 128])
+@pytest.mark.parametrize("rows,cols", SHAPES)
+def test_quantize(F, rows, cols, block_rows):
+    x = make(rows, cols, rows + cols)
+    d, n = x.to(DEV), x.double().numpy()
+    row = F.fp4_fp8_quantize(d, block_rows)
+    col = F.fp4_fp8_quantize_transposed(d, block_rows)
+    r2, c2 = F.fp4_fp8_quantize_dual(d, block_rows)
+    torch.cuda.synchronize()
+    v = check_tensor(row, n, block_rows)
+    vt = check_tensor(col, n.T, block_rows)
+    assert torch.equal(row.codes, r2.codes) and torch.equal(row.scales, r2.scales)
+    assert torch.equal(col.codes, c2.codes) and torch.equal(col.scales, c2.scales)
+    if block_rows == 128:
+        assert np.array_equal(v, vt.T)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("block_rows", [1, 128])
+def test_quantize_special_values(F, block_rows):
+    x = torch.zeros((140, 300))
+    x[0, :] = torch.tensor([448.0, 449.0, -448.0, 1e-30, 0.0] * 60)
+    x[1, 3], x[1, 200] = math.inf, -math.inf
+    x[2, 7] = math.nan
+    x[2, 8] = 3.0
+    x[3, :128] = 2.0 ** torch.arange(-64, 64).float()
+    x[4, 128:256] = 2.0 ** -133            # BF16's smallest, below the least scale
+    x[5, 5] = 3.3e38
+    x[6, :] = -0.0
+    x[131, 299] = 1.75
+    x[131, 298] = 1.7578125                # just above: the next power of two
+    x = x.bfloat16()
+    row, col = F.fp4_fp8_quantize_dual(x.to(DEV), block_rows)
+    torch.cuda.synchronize()
+    n = x.double().numpy()
+    check_tensor(row, n, block_rows)
+    check_tensor(col, n.T, block_rows)
+
+
+@pytest.mark.gpu
+def test_quantize_strides_and_offsets(F):
+    big = make(300, 700, 3).to(DEV)
+    for d in (big[:, 8:520], big[:, 3:516], big[::2, 1:130], big[7:8, 5:]):
+        row, col = F.fp4_fp8_quantize_dual(d)
+        torch.cuda.synchronize()
+        n = d.double().cpu().numpy()
+        check_tensor(row, n, 1)
+        check_tensor(col, n.T, 1)
+
+
+def near(got, a, b, bf16, what):
+    """Entries of a b^T (64-bit values) against the bound of this file's head."""
+    want = a @ b.T
+    acc = a.shape[1] * 2.0 ** -23 * (np.abs(a) @ np.abs(b).T)
+    got = got.double().cpu().numpy()
+    half = 2.0 ** -8 if bf16 else 2.0 ** -23
+    err = np.abs(got - want)
+    ok = err <= acc * (1 + half) + half * np.abs(want) + 1e-38
+    assert ok.all(), f"{what}: {int((~ok).sum())} of {ok.size} beyond the bound, first at {np.argwhere(~ok)[0]}"
+    # that bound grows with K: a lost block of K shows in every 32 columns' norm
+    norm = np.linalg.norm(want)
+    assert np.linalg.norm(err) <= (2.0 ** -8 if bf16 else a.shape[1] / 32 * 2.0 ** -23 + 2.0 ** -20) * norm, what
+
+
+GEMMS = [(1, 1, 1), (1, 300, 128), (5, 129, 130), (128, 128, 512), (256, 256, 640), (257, 130, 1025), (64, 512, 2048),
+         (300, 1000, 384), (33, 2051, 777), (700, 260, 4100), (1000, 1500, 256), (8, 5632, 2048), (17, 640, 9000)]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("M,N,K", GEMMS)
+def test_gemm(F, M, N, K):
+    a, b = make(M, K, 1).to(DEV), make(N, K, 2).to(DEV)
+    A, B = F.fp4_fp8_quantize(a), F.fp4_fp8_quantize(b)
+    va, vb = quantize(a.double().cpu().numpy(), 1)[2], quantize(b.double().cpu().numpy(), 1)[2]
+    for dtype in (torch.bfloat16, torch.float32):
+        c = F.fp4_fp8_gemm(A, B, out_dtype=dtype)
+        torch.cuda.synchronize()
+        F.fp4_check_status()
+        near(c, va, vb, dtype == torch.bfloat16, str(dtype))
+        # an output with odd pitch and its surroundings untouched
+        buf = torch.full((M + 2, N + 3), 7.0, dtype=dtype, device=DEV)
+        F.fp4_fp8_gemm(A, B, out=buf[1:M + 1, 1:N + 1])
+        torch.cuda.synchronize()
+        near(buf[1:M + 1, 1:N + 1], va, vb, dtype == torch.bfloat16, "odd pitch")
+        edge = buf.clone()
+        edge[1:M + 1, 1:N + 1] = 7.0
+        assert (edge == 7.0).all()
+        wide = torch.full((M + 2, N + 40), 7.0, dtype=dtype, device=DEV)[:, :(N + 40) // 8 * 8]
+        out = wide[1:M + 1, 8:8 + N]
+        F.fp4_fp8_gemm(A, B, out=out)
+        torch.cuda.synchronize()
+        assert torch.equal(out, c)
+        out.fill_(7.0)
+        assert (wide == 7.0).all()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("M", [1, 2, 7, 8, 9, 16, 31, 64, 65, 128, 129, 200])
+@pytest.mark.parametrize("N,K", [(384, 4096), (2050, 1100)])
+def test_few_tokens(F, M, N, K):
+    # serving: one or a few tokens, all of the weights
+    x, w = make(M, K, M).to(DEV), (make(N, K, 5).float() * 0.02).bfloat16().to(DEV)
+    Wq = F.fp4_fp8_quantize(w, 128)
+    y, saved = F.fp4_fp8_linear_fwd(x, Wq, save=False)
+    torch.cuda.synchronize()
+    F.fp4_check_status()
+    assert saved is None
+    near(y, quantize(x.double().cpu().numpy(), 1)[2], quantize(w.double().cpu().numpy(), 128)[2], True, "y")
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("M,N,K", [(1, 1, 1), (1, 256, 384), (130, 300, 257), (257, 1000, 520), (640, 512, 256)])
+def test_linear(F, M, N, K):
+    x, w, dy = make(M, K, 1).to(DEV), make(N, K, 2).to(DEV), make(M, N, 3).to(DEV)
+    Wq, WqT = F.fp4_fp8_quantize_dual(w, 128)
+    y, xqT = F.fp4_fp8_linear_fwd(x, Wq)
+    n = lambda t: t.double().cpu().numpy()  # noqa: E731
+    vw = quantize(n(w), 128)[2]
+    near(y, quantize(n(x), 1)[2], vw, True, "y")
+    vxT = check_tensor(xqT, n(x).T, 1)
+    for dtype in (torch.bfloat16, torch.float32):
+        dx, dw = F.fp4_fp8_linear_bwd(dy, WqT, xqT, dw_dtype=dtype)
+        torch.cuda.synchronize()
+        F.fp4_check_status()
+        near(dx, quantize(n(dy), 1)[2], vw.T, True, "dx")
+        near(dw, quantize(n(dy).T, 1)[2], vxT, dtype == torch.bfloat16, "dw")
+    only_dx, none = F.fp4_fp8_linear_bwd(dy, WqT, None)
+    none2, only_dw = F.fp4_fp8_linear_bwd(dy, None, xqT, dw_dtype=dtype)
+    torch.cuda.synchronize()
+    assert none is None and none2 is None and torch.equal(only_dx, dx) and torch.equal(only_dw, dw)
+
+
+@pytest.mark.gpu
+def test_gradients_against_differences(F):
+    # y is linear in x and w on the quantizer's grid: moving one quantized operand to another grid point moves the loss
+    # <dy, y> by exactly <dx, dx-step>; the gradients see dy through its own quantization, so dy is put on the grid first
+    M, N, K = 200, 256, 384
+    x, w, dy = make(M, K, 1, False).to(DEV), make(N, K, 2, False).to(DEV), make(M, N, 3, False).to(DEV)
+    n = lambda t: t.double().cpu().numpy()  # noqa: E731
+    vx, vw = quantize(n(x), 1)[2], quantize(n(w), 128)[2]
+    dy = torch.tensor(np.ldexp(np.sign(n(dy)), np.random.RandomState(0).randint(-3, 4, (M, N)))).bfloat16().to(DEV)
+    g = n(dy)  # powers of two within 2^7 of each other: exact in both forms
+    Wq, WqT = F.fp4_fp8_quantize_dual(w, 128)
+    xqT = F.fp4_fp8_quantize_transposed(x)
+    vxT = quantize(n(x).T, 1)[2]
+    dx, dw = F.fp4_fp8_linear_bwd(dy, WqT, xqT, dw_dtype=torch.float32)
+    h = 0.125
+    rng = np.random.RandomState(1)
+    ex, ew = rng.randint(-1, 2, (M, K)) * h, rng.randint(-1, 2, (N, K)) * h
+    loss = lambda a, b: float((g * (a @ b.T)).sum())  # noqa: E731
+    want_x = (loss(vx + ex, vw) - loss(vx - ex, vw)) / 2
+    want_w = (loss(vxT.T, vw + ew) - loss(vxT.T, vw - ew)) / 2
+    got_x, got_w = float((n(dx) * ex).sum()), float((n(dw) * ew).sum())
+    # BF16 rounding of dx: 2^-9 relative per entry, signs at random over M K entries: six standard deviations
+    assert abs(got_x - want_x) <= 6 * 2.0 ** -9 * np.linalg.norm(n(dx) * ex) + 1e-6 * np.abs(n(dx) * ex).sum()
+    assert abs(got_w - want_w) <= 1e-5 * np.abs(n(dw) * ew).sum()
+
+
+@pytest.mark.gpu
+def test_nan_and_inf_reach_the_outputs(F):
+    x, w = make(40, 300, 1).to(DEV), make(50, 300, 2).to(DEV)
+    x[3, 7], w[9, 200] = math.inf, math.nan
+    for M in (4, 40):
+        y, _ = F.fp4_fp8_linear_fwd(x[:M], F.fp4_fp8_quantize(w, 128))
+        torch.cuda.synchronize()
+        bad = torch.isnan(y)
+        assert bad[3].all() and bad[:, 9].all()
+        bad[3], bad[:, 9] = False, False
+        assert not bad.any()
+
+
+@pytest.mark.gpu
+def test_repeats_streams_and_order(F):
+    x, w = make(300, 1024, 1).to(DEV), make(640, 1024, 2).to(DEV)
+    Wq = F.fp4_fp8_quantize(w, 128)
+    y0, s0 = F.fp4_fp8_linear_fwd(x, Wq)
+    y1, s1 = F.fp4_fp8_linear_fwd(x, Wq)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        y2, _ = F.fp4_fp8_linear_fwd(x, Wq)
+    side.synchronize()
+    assert torch.equal(y0, y1) and torch.equal(y0, y2) and torch.equal(s0.codes, s1.codes)
+    # a call queued behind a copy into its input reads the copied values
+    z = torch.zeros_like(x)
+    for _ in range(4):
+        z.zero_()
+        F.fp4_fp8_linear_fwd(z, Wq)
+        z.copy_(x)
+        y3, _ = F.fp4_fp8_linear_fwd(z, Wq)
+        torch.cuda.synchronize()
+        assert torch.equal(y3, y0)
+
+
+@pytest.mark.gpu
+def test_large_head(F):
+    # the training head's sizes, on sampled rows and columns; the last tiles are partial in M
+    M, N, K = 8000, 32000, 2048
+    g = torch.Generator(device=DEV).manual_seed(0)
+    x = torch.randn((M, K), device=DEV, generator=g).bfloat16()
+    w = (torch.randn((N, K), device=DEV, generator=g) * 0.02).bfloat16()
+    dy = (torch.randn((M, N), device=DEV, generator=g) * 1e-3).bfloat16()
+    Wq, WqT = F.fp4_fp8_quantize_dual(w, 128)
+    y, xqT = F.fp4_fp8_linear_fwd(x, Wq)
+    dx, dw = F.fp4_fp8_linear_bwd(dy, WqT, xqT)
+    torch.cuda.synchronize()
+    F.fp4_check_status()
+    n = lambda t: t.double().cpu().numpy()  # noqa: E731
+    rows = np.array([0, 127, 128, 4095, 4096, 7807, 7808, 7999])
+    cols = np.array([0, 1, 255, 256, 16000, 31743, 31744, 31999])
+    vx, vdy = quantize(n(x[rows]), 1)[2], quantize(n(dy[rows]), 1)[2]
+    vw = quantize(n(w), 128)[2]
+    near(y[rows], vx, vw, True, "y")
+    near(dx[rows], vdy, vw.T.copy(), True, "dx")
+    vdyT, vxT = quantize(n(dy[:, cols]).T, 1)[2], quantize(n(x).T, 1)[2]
+    near(dw[cols], vdyT, vxT, True, "dw")
+
+
+@pytest.mark.gpu
+def test_no_tokens(F):
+    Wq = F.fp4_fp8_quantize(make(64, 64, 1).to(DEV), 128)
+    n = F.fp4_launch_count()
+    y, _ = F.fp4_fp8_linear_fwd(torch.empty((0, 64), dtype=torch.bfloat16, device=DEV), Wq, save=False)
+    assert y.shape == (0, 64) and F.fp4_launch_count() == n
+
+
+def test_refusals(F):
+    # host-side checks only; nothing is launched
+    L, p = F.lib(), 1 << 20
+    bad, mis, shape, ws = F.FP4_ERR_INVALID_ARG, F.FP4_ERR_MISALIGNED, F.FP4_ERR_UNSUPPORTED_SHAPE, F.FP4_ERR_WORKSPACE
+
+    def t(rows, cols, codes=p, scales=p):
+        return ctypes.byref(F.CFP8Tensor(codes, scales, rows, cols))
+
+    q = lambda *a: L.fp4_fp8_quantize(*a, None)  # noqa: E731
+    assert q(None, 4, 8, 8, 1, t(4, 8), None) == bad
+    assert q(p, 0, 8, 8, 1, t(4, 8), None) == bad
+    assert q(p, 4, 8, 7, 1, t(4, 8), None) == bad
+    assert q(p + 1, 4, 8, 8, 1, t(4, 8), None) == mis
+    assert q(p, 4, 8, 8, 64, t(4, 8), None) == bad
+    assert q(p, 4, 8, 8, 1, None, None) == bad
+    assert q(p, 4, 8, 8, 1, t(8, 4), None) == bad and q(p, 4, 8, 8, 1, None, t(4, 8)) == bad
+    assert q(p, 4, 8, 8, 1, t(4, 8, codes=p + 8), None) == mis and q(p, 4, 8, 8, 1, t(4, 8, scales=None), None) == bad
+    assert q(p, 1 << 24, 8, 8, 1, t(1 << 24, 8), None) == shape
+    g = lambda *a: L.fp4_fp8_gemm(*a, None)  # noqa: E731
+    assert g(None, t(4, 8), p, 0, 4) == bad and g(t(4, 8), t(4, 9), p, 0, 4) == bad
+    assert g(t(4, 8), t(4, 8), None, 0, 4) == bad and g(t(4, 8), t(4, 8), p, 2, 4) == bad
+    assert g(t(4, 8), t(4, 8), p, 0, 3) == bad and g(t(4, 8), t(4, 8), p + 2, 1, 4) == mis
+    f = lambda *a: L.fp4_fp8_linear_fwd(*a, None)  # noqa: E731
+    assert f(p, 4, 8, 8, t(16, 9), p, 16, None, p, 1 << 20) == bad
+    assert f(p, 4, 8, 8, t(16, 8), p, 16, t(4, 8), p, 1 << 20) == bad
+    assert f(p, 4, 8, 8, t(16, 8), p, 16, None, p, 16) == ws and f(p, 4, 8, 8, t(16, 8), p, 16, None, p + 8, 1 << 20) == ws
+    assert f(p, -1, 8, 8, t(16, 8), p, 16, None, p, 1 << 20) == bad
+    assert f(p, 0, 8, 8, t(16, 8), p, 16, None, None, 0) == F.FP4_OK
+    b = lambda *a: L.fp4_fp8_linear_bwd(*a, None)  # noqa: E731
+    assert b(p, 4, 16, 16, t(8, 16), t(8, 4), None, 8, None, 0, 8, p, 1 << 20) == bad
+    assert b(p, 4, 16, 16, None, t(8, 4), p, 8, None, 0, 8, p, 1 << 20) == bad
+    assert b(p, 4, 16, 16, t(8, 16), t(9, 4), p, 8, p, 0, 9, p, 1 << 20) == bad
+    assert b(p, 4, 16, 16, t(8, 16), t(8, 5), p, 8, p, 0, 8, p, 1 << 20) == bad
+    assert b(p, 4, 16, 16, t(8, 16), t(8, 4), p, 8, p, 3, 8, p, 1 << 20) == bad
+    assert b(p, 4, 16, 16, t(8, 16), t(8, 4), p, 8, p, 0, 8, p, 100) == ws
+    assert F.fp8_linear_fwd_workspace(0, 4, 4) == 0
+    assert L.fp4_fp8_code_pitch(129) == 256 and L.fp4_fp8_scale_bytes(129, 513) == 2 * 2 * 512
+    with pytest.raises(ValueError):
+        F.fp4_fp8_quantize(torch.zeros((2, 3)))
