@@ -436,7 +436,7 @@ fp4_status fp4_fp8_linear_bwd(const void* dY, int64_t M, int64_t N, int64_t lddy
  * (int64 [T]) and logprob go together (both NULL: not wanted); entropy NULL: not
  * wanted; stats is always written.  0 <= top_k <= 32 (and <= V); top_index int64
  * and top_logprob FP32, both [T][top_k].  T = 0 is a call without work.
- * temperature > 0, finite. */
+ * 1e-20 <= temperature <= 1e20. */
 fp4_status fp4_token_logprobs(const void* logits, int dtype, int64_t T, int64_t V, int64_t ld,
                               float temperature, const int64_t* targets, int top_k, float* logprob,
                               float* entropy, float* stats, float* top_logprob, int64_t* top_index,

@@ -28,8 +28,8 @@ static fp4_status check_logprob_sizes(int64_t T, int64_t V, float temperature, i
   if (T < 0 || V < 1) return fail(FP4_ERR_INVALID_ARG, "T %lld, V %lld: T >= 0 and V >= 1 needed", (long long)T, (long long)V);
   if (T > INT32_MAX / 16 || V > INT32_MAX - 64)
     return fail(FP4_ERR_UNSUPPORTED_SHAPE, "T %lld (at most 2^27) or V %lld (below 2^31 - 64) too large", (long long)T, (long long)V);
-  if (!(temperature > 0.0f) || !std::isfinite(temperature) || !std::isfinite(1.0f / temperature))
-    return fail(FP4_ERR_INVALID_ARG, "temperature %g must be positive and finite", (double)temperature);
+  if (!(temperature >= 1e-20f && temperature <= 1e20f))
+    return fail(FP4_ERR_INVALID_ARG, "temperature %g must be in [1e-20, 1e20]", (double)temperature);
   if (top_k < 0 || top_k > 32 || top_k > V)
     return fail(FP4_ERR_INVALID_ARG, "top_k %d must be in [0, 32] and at most V", top_k);
   return FP4_OK;

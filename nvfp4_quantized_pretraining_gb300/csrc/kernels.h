@@ -220,6 +220,7 @@ struct LogprobBwdArgs {
   int64_t ldd;
 };
 cudaError_t launch_token_logprobs_bwd(const LogprobBwdArgs& a, int num_sms, cudaStream_t s);
+cudaError_t logprob_status_read_clear(unsigned int* out, cudaStream_t s);
 
 // FP8 blocks of 128: row pitch of the codes (a multiple of 128), scale bytes in the MMA layout.
 inline int64_t fp8_pitch(int64_t cols) { return (cols + 127) / 128 * 128; }

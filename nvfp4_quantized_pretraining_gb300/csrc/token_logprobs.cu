@@ -2,18 +2,25 @@
 // entries, and their gradient.
 //
 // Forward: one read of the logits.  Each thread keeps a running maximum m of its logits with
-// S = sum 2^(x2) and E = sum 2^(x2) x2, x2 = (z - m) log2(e) / temperature; when the maximum grows by d,
-// S <- S 2^-d and E <- (E - S d) 2^-d.  Threads, warps and the CTAs of a row's cluster are joined the same
-// way in a fixed order; logprob = x_target - ln S, entropy = ln S - ln 2 E / S.
+// s = sum 2^x, e = sum 2^x x for x = z k2 - c, k2 = log2(e) / temperature, c = ceil(m k2): any reference near
+// the maximum serves, and an integer one makes x a single fused multiply-add and every change of reference an
+// exact power of two (d = c - c': e <- (e + s d) 2^d, s <- s 2^d).  Threads, warps and the CTAs of a row's cluster
+// are joined the same way in a fixed order; S = s 2^(c - m k2), entropy = ln s - ln 2 e / s.
+// Logits far out (|z k2| of 2^30) would leave x without its fraction: below -far they are clamped there (2^x = 0 all
+// the same), and a row whose maximum is beyond +-far / 2 is summed again relative to its maximum.
 //
-// Top k: a thread's maximum costs nothing extra.  The threads form 64 groups; the k-th largest group
+// Top k: a thread's maximum costs nothing extra.  The readers form 64 groups; the k-th largest group
 // maximum tau is a lower bound of the k-th largest logit (k groups hold an element that large), so only
-// threads whose maximum reaches tau are read again (from L2), and the elements >= tau, little more than
-// k of them, are ranked by counting.  Ties that overflow the candidate list, and rows with NaN, take
-// k rounds of a block-wide maximum instead.
+// readers whose maximum reaches tau have their vectors read again (from L2), and the elements >= tau, little
+// more than k of them, are ranked by counting.  Too many above tau: the k-th largest of those at hand is a
+// better bound.  Too many equal to it: an ordered scan takes the lowest indices.  NaN: k rounds of a maximum.
 //
-// Both directions are bound by memory: 2 or 4 bytes per logit forward, twice that backward.
+// Both directions are bound by memory (2 or 4 bytes per logit forward, twice that backward) and, in BF16, nearly as
+// much by issue slots: 6.8 TB/s leaves 11 instructions per logit.  So maxima are packed BF16, products, sums and
+// additions packed FP32 pairs, and the running maximum is looked at once per 4 vectors.
 #include <cuda_bf16.h>
+
+#include <cstring>
 
 #include "common.cuh"
 #include "kernels.h"
@@ -22,11 +29,9 @@ namespace nvfp4 {
 namespace lp {
 
 constexpr int kMaxTop = 32;
-constexpr int kGroups = 64;
-constexpr int kCap = 1024;  // candidates ranked by counting
+constexpr int kCap = 128;  // candidates above tau; as many vectors that hold one; half as many equal to it
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
-// 2^x2 is 0 below this; a banned token's x2 = -inf would make 0 * inf of its entropy term
-constexpr float kFloor = -16384.0f;
+constexpr float kFloor = -16384.0f;  // 2^x is 0 below this
 
 __device__ __forceinline__ float ex2(float x) {
   float r;
@@ -39,7 +44,7 @@ __device__ __forceinline__ float max_nan(float a, float b) {
   return r;
 }
 
-// 16 bytes of logits as FP32 values; kNone fills a lane without elements.
+// 16 bytes of logits; kNone fills a lane without elements.
 template <typename T>
 struct Vec;
 template <>
@@ -52,9 +57,12 @@ struct Vec<float> {
   __device__ static __forceinline__ uint4 pack(const float (&f)[4]) {
     return make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3]));
   }
-  __device__ static __forceinline__ float largest(const uint4&, const float (&f)[4]) {
-    return max_nan(max_nan(f[0], f[1]), max_nan(f[2], f[3]));
+  // the values with those below `low` (a pattern from low_bits()) raised to it; NaN stays
+  __device__ static __forceinline__ uint32_t low_bits(float low) { return __float_as_uint(low); }
+  __device__ static __forceinline__ uint32_t max1(uint32_t a, uint32_t b) {
+    return __float_as_uint(max_nan(__uint_as_float(a), __uint_as_float(b)));
   }
+  __device__ static __forceinline__ float widest(uint32_t w) { return __uint_as_float(w); }
   __device__ static __forceinline__ float load(const float* p) { return *p; }
   __device__ static __forceinline__ void store(float* p, float v) { *p = v; }
 };
@@ -73,15 +81,13 @@ struct Vec<__nv_bfloat16> {
   __device__ static __forceinline__ uint4 pack(const float (&f)[8]) {
     return make_uint4(pack2(f[0], f[1]), pack2(f[2], f[3]), pack2(f[4], f[5]), pack2(f[6], f[7]));
   }
-  __device__ static __forceinline__ uint32_t max2(uint32_t a, uint32_t b) {
+  __device__ static __forceinline__ uint32_t low_bits(float low) { return (__float_as_uint(low) >> 16) * 0x10001u; }
+  __device__ static __forceinline__ uint32_t max1(uint32_t a, uint32_t b) {  // both halves
     uint32_t r;
     asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
     return r;
   }
-  __device__ static __forceinline__ float largest(const uint4& q, const float (&)[8]) {
-    const uint32_t w = max2(max2(q.x, q.y), max2(q.z, q.w));
-    return max_nan(bf16_lo(w), bf16_hi(w));
-  }
+  __device__ static __forceinline__ float widest(uint32_t w) { return max_nan(bf16_lo(w), bf16_hi(w)); }
   __device__ static __forceinline__ float load(const __nv_bfloat16* p) { return __bfloat162float(*p); }
   __device__ static __forceinline__ void store(__nv_bfloat16* p, float v) { *p = __float2bfloat16_rn(v); }
 };
@@ -101,36 +107,17 @@ __device__ __forceinline__ uint64_t entry_of(uint32_t key, uint32_t idx) {
   return (static_cast<uint64_t>(key) << 32) | (0xFFFFFFFFu - idx);
 }
 
+// s = sum 2^x, e = sum 2^x x with x = z k2 - reference(m)
 struct Sum {
-  float m, s, e;  // s = sum 2^x2, e = sum 2^x2 x2 relative to m; m = -inf: nothing yet
+  float m, s, e;
 };
-__device__ __forceinline__ Sum join(const Sum& a, const Sum& b, float k2) {
-  Sum r;
-  r.m = fmaxf(a.m, b.m);
-  // (a side of nothing has s = e = 0; fmaxf also turns -inf - -inf into the floor)
-  const float da = fmaxf((a.m - r.m) * k2, -1e30f), db = fmaxf((b.m - r.m) * k2, -1e30f);
-  const float ca = ex2(da), cb = ex2(db);
-  r.s = a.s * ca + b.s * cb;
-  r.e = (a.e + a.s * da) * ca + (b.e + b.s * db) * cb;
-  return r;
-}
+__device__ __forceinline__ float reference(float m, float k2) { return ceilf(m * k2); }
 
 __device__ __forceinline__ uint32_t cluster_size() {
   uint32_t r;
   asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
   return r;
 }
-__device__ __forceinline__ float ld_cluster_f32(const void* p, uint32_t rank) {
-  float v;
-  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(mapa_shared(smem_u32(p), rank)) : "memory");
-  return v;
-}
-__device__ __forceinline__ uint64_t ld_cluster_u64(const void* p, uint32_t rank) {
-  uint64_t v;
-  asm volatile("ld.shared::cluster.u64 %0, [%1];" : "=l"(v) : "r"(mapa_shared(smem_u32(p), rank)) : "memory");
-  return v;
-}
-
 // A row cut at 16-byte boundaries: `head` elements, `vecs` aligned vectors, `tail` elements.
 struct RowCut {
   uint32_t head, vecs, tail;
@@ -146,241 +133,548 @@ __device__ __forceinline__ RowCut cut_row(const T* row, uint32_t V) {
   return c;
 }
 
-// One cluster of CTAs per row, each CTA a consecutive share of the row's vectors (rank 0 also the
-// edge elements).
-template <typename T, int THREADS, bool TOP>
-__global__ void __launch_bounds__(THREADS) logprob_kernel(const LogprobArgs a) {
+// Roles of a CTA's warps: 8 read the logits out of a ring of shared-memory stages, one thread fills the ring by bulk
+// copies ahead of them and across rows, one warp joins the row's partial sums, finds the top k and writes the
+// results while the readers are at the next row.  (With loads into registers and the joins done by all warps between
+// barriers, 8192 x 32000 BF16 took 104 us, the loads idle during the joins.)
+//
+// A cluster of C CTAs takes a row, each CTA a consecutive share of the row's vectors (rank 0 also the edge
+// elements); shares are joined in rank 0.  Clusters walk the rows, as many as there are of them apart.
+constexpr int kReaders = 256;
+// One joining warp keeps up with the readers; four, each on every fourth row, where they find the top k.
+__host__ __device__ constexpr int joiners_of(bool top) { return top ? 4 : 1; }
+__host__ __device__ constexpr int buffers_of(bool top) { return top ? 4 : 2; }
+__host__ __device__ constexpr int per_sm_of(bool top) { return top ? 2 : 3; }  // CTAs
+__host__ __device__ constexpr int threads_of(bool top) { return kReaders + 32 + 32 * joiners_of(top); }
+constexpr int kStages = 3, kStageVecs = 1024;
+constexpr int kSmemBytes = kStages * kStageVecs * 16;
+constexpr int kMaxCluster = 8;
+
+// What readers leave of a row: per thread the true maximum (-inf: only banned tokens), and the sums relative to
+// reference(max(maximum, -far)).
+struct Partials {
+  float m[kReaders], s[kReaders], e[kReaders];
+};
+template <bool TOP>
+struct Scratch {  // a joining warp's
+  uint4 hit[kCap];
+  uint64_t above[kCap], equal[kCap / 2];
+  uint64_t top[kMaxTop];
+  uint32_t hit_at[kCap];
+  uint8_t list[kReaders];
+};
+template <>
+struct Scratch<false> {};
+
+__device__ __forceinline__ void st_cluster_f32(uint32_t addr, float v) {
+  asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
+}
+__device__ __forceinline__ void st_cluster_u64(uint32_t addr, uint64_t v) {
+  asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(addr), "l"(v) : "memory");
+}
+__device__ __forceinline__ float warp_max(float v) {
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) v = fmaxf(v, __shfl_xor_sync(0xFFFFFFFFu, v, o));
+  return v;
+}
+__device__ __forceinline__ float warp_sum(float v) {
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
+  return v;
+}
+
+// One CTA's share of a row, and what its threads need of it.
+template <typename T>
+struct Share {
+  const T* row;
+  RowCut cut;
+  uint32_t v0, v1, edges;
+  __device__ __forceinline__ const uint4* vec() const { return reinterpret_cast<const uint4*>(row + cut.head); }
+  __device__ __forceinline__ uint32_t edge_index(uint32_t i) const { return i < cut.head ? i : cut.vecs * Vec<T>::N + i; }
+  __device__ __forceinline__ uint32_t index(uint32_t v, int j) const { return cut.head + v * Vec<T>::N + j; }
+};
+template <typename T>
+__device__ __forceinline__ Share<T> share_of(const LogprobArgs& a, int64_t t, uint32_t rank, uint32_t C) {
+  Share<T> h;
+  h.row = static_cast<const T*>(a.logits) + t * a.ld;
+  h.cut = cut_row(h.row, static_cast<uint32_t>(a.V));
+  h.v0 = static_cast<uint32_t>((uint64_t)h.cut.vecs * rank / C);
+  h.v1 = static_cast<uint32_t>((uint64_t)h.cut.vecs * (rank + 1) / C);
+  h.edges = rank == 0 ? h.cut.head + h.cut.tail : 0u;
+  return h;
+}
+
+// The top k of a share by one warp, into x.top (0: nothing left).  maxima: the readers' (shared memory).
+
+template <typename T>
+__device__ __forceinline__ void share_top(const Share<T> h, const float* maxima, float edge, bool odd, uint32_t k,
+                                       Scratch<true>& x) {
   using V8 = Vec<T>;
-  constexpr int N = V8::N, WARPS = THREADS / 32;
-  __shared__ Sum s_sum[WARPS];
-  __shared__ Sum s_cta;
-  __shared__ uint32_t s_group[TOP ? kGroups : 1];
-  __shared__ uint64_t s_cand[TOP ? kCap : 1];
-  __shared__ uint16_t s_list[TOP ? THREADS : 1];
-  __shared__ uint64_t s_top[TOP ? kMaxTop : 1];
-  __shared__ uint64_t s_best[TOP ? WARPS : 1];
-  __shared__ uint32_t s_tau, s_count, s_listed;
+  constexpr int N = V8::N;
+  constexpr uint32_t kAll = 0xFFFFFFFFu;
+  const int lane = threadIdx.x & 31;
+  const uint32_t below = (1u << lane) - 1;
+  const uint4* vec = h.vec();
+  const uint32_t length = (h.v1 - h.v0) * N + h.edges, wanted = min(k, length);
+  const uint32_t edge_key = order_key(edge);
+  x.top[lane] = 0;
+  // the groups: readers lane, + 32, + 64, + 96, and the same from lane + 128
+  auto key = [&](int i) { return order_key(maxima[lane + 32 * i]); };
+  const uint32_t g0 = max(max(key(0), key(1)), max(key(2), key(3))), g1 = max(max(key(4), key(5)), max(key(6), key(7)));
+  uint32_t better0 = 0, better1 = 0;
+#pragma unroll
+  for (int j = 0; j < 32; ++j) {
+    const uint32_t o0 = __shfl_sync(kAll, g0, j), o1 = __shfl_sync(kAll, g1, j);
+    better0 += (o0 > g0 || (o0 == g0 && j < lane)) + (o1 > g0);
+    better1 += (o0 >= g1) + (o1 > g1 || (o1 == g1 && j < lane));
+  }
+  const uint32_t in0 = __ballot_sync(kAll, better0 == k - 1), in1 = __ballot_sync(kAll, better1 == k - 1);
+  uint32_t tau = in0 ? __shfl_sync(kAll, g0, __ffs(in0) - 1) : __shfl_sync(kAll, g1, __ffs(in1) - 1);
+
+  uint32_t above = 0, equal = 0;  // entries in the lists
+  // Fills the lists with the share's elements above tau and, with_equal, those equal to it; false if they do not fit
+  // (the lists then hold as many of them as do).
+  auto collect = [&](bool with_equal) {
+    uint32_t strips = 0;
+    const uint32_t bound = with_equal ? tau : tau + 1;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const bool is = key(i) >= bound;
+      const uint32_t in = __ballot_sync(kAll, is);
+      if (is) x.list[strips + __popc(in & below)] = static_cast<uint8_t>(lane + 32 * i);
+      strips += __popc(in);
+    }
+    __syncwarp();
+    // vectors with such an element
+    const float least = key_value(tau);
+    const uint32_t per = (h.v1 - h.v0 + kReaders - 1) / kReaders;
+    const uint32_t shift = per >= 32 ? 5 : per > 1 ? 32 - __clz(per - 1) : 0;  // 2^shift lanes take a strip's vectors
+    uint32_t hits = 0;
+    for (uint32_t w0 = 0; w0 < per; w0 += 1u << shift) {
+      for (uint32_t q = lane >> shift; q - (lane >> shift) < strips; q += 4 * (32 >> shift)) {
+        uint4 w[4];
+        uint32_t at[4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          const uint32_t p = q + u * (32 >> shift), v = w0 + (lane & ((1u << shift) - 1));
+          at[u] = p < strips && v < per ? h.v0 + x.list[p] + v * kReaders : h.v1;
+          w[u] = at[u] < h.v1 ? vec[at[u]] : make_uint4(V8::kNone, V8::kNone, V8::kNone, V8::kNone);
+        }
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          const float most = V8::widest(V8::max1(V8::max1(w[u].x, w[u].y), V8::max1(w[u].z, w[u].w)));
+          const bool hit = at[u] < h.v1 && (with_equal ? most >= least : most > least);
+          const uint32_t in = __ballot_sync(kAll, hit), to = hits + __popc(in & below);
+          if (hit && to < kCap) x.hit[to] = w[u], x.hit_at[to] = at[u];
+          hits += __popc(in);
+        }
+      }
+    }
+    __syncwarp();
+    // their elements; the edge elements as one more round
+    above = 0, equal = 0;
+    const uint32_t listed = min(hits, (uint32_t)kCap);
+    for (uint32_t i = 0; i < listed + 32; i += 32) {
+      uint32_t over = 0, same = 0, first = 0;
+      float f[N];
+      const bool last = i >= listed;
+      if (last) {
+        first = h.edge_index(lane);
+        over = lane < h.edges && edge_key > tau, same = lane < h.edges && edge_key == tau;
+      } else if (i + lane < listed) {
+        V8::unpack(x.hit[i + lane], f);
+        first = h.index(x.hit_at[i + lane], 0);
+#pragma unroll
+        for (int j = 0; j < N; ++j) over |= (f[j] > least) << j, same |= (f[j] == least) << j;
+      }
+      if (!with_equal) same = 0;
+      uint32_t n = __popc(over) | __popc(same) << 16, before = n;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const uint32_t y = __shfl_up_sync(kAll, before, o);
+        if (lane >= o) before += y;
+      }
+      const uint32_t all = __shfl_sync(kAll, before, 31);
+      before -= n;
+      uint32_t to = above + (before & 0xFFFFu);
+      if (last) {
+        if (over && to < kCap) x.above[to] = entry_of(edge_key, first);
+      } else {
+#pragma unroll
+        for (int j = 0; j < N; ++j)
+          if ((over >> j & 1) && to < kCap) x.above[to++] = entry_of(order_key(f[j]), first + j);
+      }
+      to = equal + (before >> 16);
+      for (; same; same &= same - 1)
+        if (to < kCap / 2) x.equal[to++] = entry_of(tau, first + __ffs(same) - 1);
+      above += all & 0xFFFFu, equal += all >> 16;
+    }
+    __syncwarp();
+    const bool fits = hits <= kCap && above <= kCap && equal <= kCap / 2;
+    above = min(above, (uint32_t)kCap), equal = min(equal, (uint32_t)kCap / 2);
+    return fits;
+  };
+  // The k-th largest of the list `above` (of at least k entries) by counting.
+  auto raise = [&] {
+    uint32_t kth = 0;
+    for (uint32_t i = 0; i < above; i += 32) {
+      uint32_t n = 0;
+      const uint64_t y = i + lane < above ? x.above[i + lane] : 0;
+      for (uint32_t j = 0; j < above; ++j) n += x.above[j] > y;
+      const uint32_t in = __ballot_sync(kAll, i + lane < above && n == k - 1);
+      if (in) kth = __shfl_sync(kAll, static_cast<uint32_t>(y >> 32), __ffs(in) - 1);
+    }
+    return kth;
+  };
+  bool done = false;
+  if (!odd) {
+    for (int pass = 0; pass < 16 && !done; ++pass) {
+      done = collect(true) && above + equal >= wanted;
+      if (done) break;
+      if (collect(false)) {
+        equal = 0;
+        if (above < wanted) {  // more ties than the list holds: the lowest indices among them, in order
+          const uint32_t need = wanted - above;
+          uint32_t taken = 0;
+          auto take = [&](uint32_t bits, uint32_t first) {  // bit j: element first + j equals tau
+            const uint32_t n = __popc(bits);
+            uint32_t before = n;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+              const uint32_t y = __shfl_up_sync(kAll, before, o);
+              if (lane >= o) before += y;
+            }
+            const uint32_t all = __shfl_sync(kAll, before, 31);
+            before -= n;
+            while (bits && taken + before < need) {
+              x.equal[taken + before++] = entry_of(tau, first + __ffs(bits) - 1);
+              bits &= bits - 1;
+            }
+            taken += all;
+          };
+          const bool tie = lane < h.edges && edge_key == tau;
+          take(tie && lane < h.cut.head, h.edge_index(lane));
+          for (uint32_t v = h.v0; v < h.v1 && taken < need; v += 32) {
+            uint32_t bits = 0;
+            if (v + lane < h.v1) {
+              float f[N];
+              V8::unpack(vec[v + lane], f);
+#pragma unroll
+              for (int j = 0; j < N; ++j) bits |= (order_key(f[j]) == tau ? 1u : 0u) << j;
+            }
+            take(bits, h.index(v + lane, 0));
+          }
+          if (taken < need) take(tie && lane >= h.cut.head, h.edge_index(lane));
+          equal = min(taken, need);
+        }
+        done = above + equal >= wanted;
+        break;
+      }
+      if (above < k) break;
+      tau = raise();
+    }
+    __syncwarp();
+  }
+  if (done) {
+    // (the candidates' order in the lists is not fixed, their ranks are)
+    for (uint32_t i = lane; i < above + equal; i += 32) {
+      const uint64_t y = i < above ? x.above[i] : x.equal[i - above];
+      uint32_t n = 0;
+      for (uint32_t j = 0; j < above; ++j) n += x.above[j] > y;
+      for (uint32_t j = 0; j < equal; ++j) n += x.equal[j] > y;
+      if (n < k) x.top[n] = y;
+    }
+  } else {
+    uint64_t last = ~0ull;
+    for (uint32_t r = 0; r < wanted; ++r) {
+      uint64_t best = 0;
+      auto see = [&](float z, uint32_t idx) {
+        const uint64_t y = entry_of(order_key(z), idx);
+        if (y < last && y > best) best = y;
+      };
+#pragma unroll 4
+      for (uint32_t v = h.v0 + lane; v < h.v1; v += 32) {
+        float f[N];
+        V8::unpack(vec[v], f);
+#pragma unroll
+        for (int j = 0; j < N; ++j) see(f[j], h.index(v, j));
+      }
+      if (lane < h.edges) see(edge, h.edge_index(lane));
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const uint64_t other = __shfl_xor_sync(kAll, best, o);
+        best = other > best ? other : best;
+      }
+      last = best;
+      if (lane == 0) x.top[r] = best;
+    }
+  }
+  __syncwarp();
+}
+
+template <typename T, bool TOP>
+__global__ void __launch_bounds__(threads_of(TOP), per_sm_of(TOP)) logprob_kernel(const LogprobArgs a, const float far) {
+  using V8 = Vec<T>;
+  constexpr int N = V8::N, U = kStageVecs / kReaders;
+  constexpr uint32_t B = buffers_of(TOP), J = joiners_of(TOP);
+  extern __shared__ uint4 s_ring[];  // [kStages][kStageVecs]
+  __shared__ uint64_t s_full[kStages], s_free[kStages], s_done[B], s_read[B];
+  __shared__ uint64_t s_pushed[B], s_taken[B];  // rank 0: the other shares arrived; the others: rank 0 has used theirs
+  __shared__ Partials s_part[B];
+  __shared__ Sum s_joined[B][kMaxCluster];
+  __shared__ Scratch<TOP> s_scratch[joiners_of(TOP)];
+  __shared__ uint64_t s_joined_top[B][TOP ? kMaxCluster * kMaxTop : 1];
   const uint32_t rank = cluster_ctarank(), C = cluster_size();
-  const int64_t t = blockIdx.x / C;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const T* row = static_cast<const T*>(a.logits) + t * a.ld;
-  const RowCut cut = cut_row(row, static_cast<uint32_t>(a.V));
-  const uint4* vec = reinterpret_cast<const uint4*>(row + cut.head);
-  const uint32_t v0 = static_cast<uint32_t>((uint64_t)cut.vecs * rank / C);
-  const uint32_t v1 = static_cast<uint32_t>((uint64_t)cut.vecs * (rank + 1) / C);
   const float k2 = a.scale * kLog2e;
   const float neg_inf = __uint_as_float(0xFF800000u);
-
-  float m = neg_inf;
-  float2 s2 = make_float2(0.0f, 0.0f), e2 = make_float2(0.0f, 0.0f);
-  auto grow = [&](float to) {  // the running maximum becomes `to`
-    const float d = fmaxf((m - to) * k2, -1e30f), c = ex2(d);
-    e2.x = (e2.x + s2.x * d) * c, e2.y = (e2.y + s2.y * d) * c;
-    s2.x *= c, s2.y *= c;
-    m = to;
-  };
-  auto add = [&](const uint4& q) {
-    float f[N];
-    V8::unpack(q, f);
-    const float top = V8::largest(q, f);
-    if (top == neg_inf) return;  // nothing but banned tokens (NaN goes on, and makes s NaN)
-    if (top > m) grow(top);
-    const float2 mm = make_float2(-m, -m), kk = make_float2(k2, k2);
-#pragma unroll
-    for (int i = 0; i < N; i += 2) {
-      float2 x = __fmul2_rn(__fadd2_rn(make_float2(f[i], f[i + 1]), mm), kk);
-      x.x = max_nan(x.x, kFloor), x.y = max_nan(x.y, kFloor);
-      const float2 e = make_float2(ex2(x.x), ex2(x.y));
-      s2 = __fadd2_rn(s2, e);
-      e2 = __ffma2_rn(e, x, e2);
-    }
-  };
-  constexpr int U = 4;
-  for (uint32_t i = v0 + tid; i < v1; i += U * THREADS) {
-    uint4 q[U];
-#pragma unroll
-    for (int u = 0; u < U; ++u)
-      q[u] = i + u * THREADS < v1 ? vec[i + u * THREADS]
-                                  : make_uint4(V8::kNone, V8::kNone, V8::kNone, V8::kNone);
-#pragma unroll
-    for (int u = 0; u < U; ++u) add(q[u]);
-  }
-  // the edge elements, one per thread of rank 0
-  const uint32_t edges = rank == 0 ? cut.head + cut.tail : 0u;
-  const uint32_t edge_idx = tid < cut.head ? tid : cut.head + cut.vecs * N + (tid - cut.head);
-  float edge = neg_inf;
-  if (tid < edges) {
-    edge = V8::load(row + edge_idx);
-    if (edge != neg_inf) {
-      if (edge > m) grow(edge);
-      const float x = (edge - m) * k2, e = ex2(x);  // (NaN stays; finite edges are at most m: no floor needed
-      s2.x += e;                                    //  above 2^-16384, where e x is -0)
-      e2.x += x < kFloor ? 0.0f : e * x;
-    }
-  }
-
-  Sum mine{m, s2.x + s2.y, e2.x + e2.y};
-  Sum w = mine;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    Sum other;
-    other.m = __shfl_xor_sync(0xFFFFFFFFu, w.m, o);
-    other.s = __shfl_xor_sync(0xFFFFFFFFu, w.s, o);
-    other.e = __shfl_xor_sync(0xFFFFFFFFu, w.e, o);
-    w = (lane & o) ? join(other, w, k2) : join(w, other, k2);
-  }
-  if (lane == 0) s_sum[warp] = w;
-  if (TOP) {
-    // 64 groups of THREADS / 64 consecutive lanes
-    uint32_t g = order_key(mine.m);
-#pragma unroll
-    for (int o = 1; o < THREADS / kGroups; o <<= 1) g = max(g, __shfl_xor_sync(0xFFFFFFFFu, g, o));
-    if (tid % (THREADS / kGroups) == 0) s_group[tid / (THREADS / kGroups)] = g;
-    if (tid == 0) s_count = 0, s_listed = 0;
-    if (tid < kMaxTop) s_top[tid] = 0;
-  }
-  __syncthreads();
+  const int64_t first = blockIdx.x / C, stride = gridDim.x / C;
   if (tid == 0) {
-    Sum r = s_sum[0];
-#pragma unroll 1
-    for (int i = 1; i < WARPS; ++i) r = join(r, s_sum[i], k2);
-    s_cta = r;
-  }
-
-  if (TOP) {
-    const uint32_t k = a.top_k;
-    const uint32_t length = (v1 - v0) * N + edges;
-    if (tid < kGroups) {
-      const uint32_t g = s_group[tid];
-      uint32_t above = 0;
-#pragma unroll 8
-      for (uint32_t j = 0; j < kGroups; ++j) above += s_group[j] > g || (s_group[j] == g && j < (uint32_t)tid);
-      if (above == k - 1) s_tau = g;
+    for (int i = 0; i < kStages; ++i) {
+      mbar_init(&s_full[i], 1);
+      mbar_init(&s_free[i], kReaders / 32);
     }
-    // NaN hides in a thread's maximum: such rows take the rounds below
-    const bool odd = __syncthreads_or(mine.s != mine.s);
-    const uint32_t tau = s_tau;
-    uint32_t found = 0;
-    if (!odd) {
-      if (tid < edges && order_key(edge) >= tau) {
-        const uint32_t at = atomicAdd(&s_count, 1u);
-        if (at < kCap) s_cand[at] = entry_of(order_key(edge), edge_idx);
-      }
-      if (order_key(mine.m) >= tau) s_list[atomicAdd(&s_listed, 1u)] = static_cast<uint16_t>(tid);
-      __syncthreads();
-      const uint32_t strips = s_listed, per = (v1 - v0 + THREADS - 1) / THREADS;
-      for (uint32_t q = tid; q < strips * per; q += THREADS) {
-        const uint32_t i = v0 + s_list[q / per] + (q % per) * THREADS;
-        if (i >= v1) continue;
-        float f[N];
-        V8::unpack(vec[i], f);
+    for (int i = 0; i < B; ++i) {
+      mbar_init(&s_done[i], kReaders / 32);
+      mbar_init(&s_read[i], 1);
+      mbar_init(&s_pushed[i], max(C, 2u) - 1);
+      mbar_init(&s_taken[i], 1);
+    }
+    fence_mbar_init();
+  }
+  if (C > 1) cluster_sync();  // (rank 0's barrier exists before anyone arrives on it)
+  else __syncthreads();
+  bool ok = true;
+
+  if (warp < kReaders / 32) {
+    // ---------------- readers ----------------
+    uint32_t used = 0, rows = 0;
+    const uint32_t low = V8::low_bits(-far);
+    for (int64_t t = first; t < a.T; t += stride, ++rows) {
+      const Share<T> h = share_of<T>(a, t, rank, C);
+      float m = neg_inf, c = reference(-far, k2);
+      float2 s2 = make_float2(0.0f, 0.0f), e2 = make_float2(0.0f, 0.0f);
+      // (a thread that has met nothing above -far counts its elements as 2^0 of that reference: the first real
+      //  maximum, here or in the join, multiplies them by 2^-2^29 = 0)
+#pragma unroll 1
+      for (uint32_t i = h.v0; i < h.v1; i += kStageVecs, ++used) {
+        const uint32_t st = used % kStages, n = min(h.v1 - i, (uint32_t)kStageVecs);
+        if (ok) ok = mbar_wait(&s_full[st], (used / kStages) & 1);
+        uint4 q[U];
 #pragma unroll
-        for (int j = 0; j < N; ++j) {
-          const uint32_t key = order_key(f[j]);
-          if (key >= tau) {
-            const uint32_t at = atomicAdd(&s_count, 1u);
-            if (at < kCap) s_cand[at] = entry_of(key, cut.head + i * N + j);
+        for (int u = 0; u < U; ++u)
+          q[u] = tid + u * kReaders < n ? s_ring[st * kStageVecs + tid + u * kReaders]
+                                        : make_uint4(V8::kNone, V8::kNone, V8::kNone, V8::kNone);
+        uint32_t top = V8::kNone;
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          top = V8::max1(top, V8::max1(V8::max1(q[u].x, q[u].y), V8::max1(q[u].z, q[u].w)));
+          q[u].x = V8::max1(q[u].x, low), q[u].y = V8::max1(q[u].y, low);
+          q[u].z = V8::max1(q[u].z, low), q[u].w = V8::max1(q[u].w, low);
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&s_free[st]);  // (the values are in registers)
+        const float most = V8::widest(top);
+        if (most > m) {  // (NaN: not taken, and s becomes NaN below)
+          m = most;
+          const float next = reference(fmaxf(m, -far), k2), d = c - next, f = ex2(d);
+          e2.x = (e2.x + s2.x * d) * f, e2.y = (e2.y + s2.y * d) * f;
+          s2.x *= f, s2.y *= f;
+          c = next;
+        }
+        const float2 kk = make_float2(k2, k2), cc = make_float2(-c, -c);
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          float f[N];
+          V8::unpack(q[u], f);
+#pragma unroll
+          for (int j = 0; j < N; j += 2) {
+            const float2 x = __ffma2_rn(make_float2(f[j], f[j + 1]), kk, cc);
+            const float2 p = make_float2(ex2(x.x), ex2(x.y));
+            s2 = __fadd2_rn(s2, p);
+            e2 = __ffma2_rn(p, x, e2);
           }
         }
       }
-      __syncthreads();
-      found = s_count;
+      const uint32_t buf = rows % B;
+      if (ok) ok = mbar_wait(&s_read[buf], ((rows / B) & 1) ^ 1);
+      s_part[buf].m[tid] = m;
+      s_part[buf].s[tid] = s2.x + s2.y;
+      s_part[buf].e[tid] = e2.x + e2.y;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&s_done[buf]);
     }
-    if (!odd && found <= kCap && found >= min(k, length)) {
-      // (the candidates' order in the list is not fixed, their ranks are)
-      for (uint32_t i = tid; i < found; i += THREADS) {
-        const uint64_t c = s_cand[i];
-        uint32_t above = 0;
-        for (uint32_t j = 0; j < found; ++j) above += s_cand[j] > c;
-        if (above < k) s_top[above] = c;
-      }
-    } else {
-      uint64_t last = ~0ull;
-      for (uint32_t r = 0; r < min(k, length); ++r) {
-        uint64_t best = 0;
-        auto see = [&](float z, uint32_t idx) {
-          const uint64_t c = entry_of(order_key(z), idx);
-          if (c < last && c > best) best = c;
-        };
-        for (uint32_t i = v0 + tid; i < v1; i += THREADS) {
-          float f[N];
-          V8::unpack(vec[i], f);
-#pragma unroll
-          for (int j = 0; j < N; ++j) see(f[j], cut.head + i * N + j);
+  } else if (warp == kReaders / 32) {
+    // ---------------- the ring's copies ----------------
+    if (lane == 0) {
+      uint32_t issued = 0;
+      for (int64_t t = first; ok && t < a.T; t += stride) {
+        const Share<T> h = share_of<T>(a, t, rank, C);
+        for (uint32_t v = h.v0; ok && v < h.v1; v += kStageVecs, ++issued) {
+          const uint32_t st = issued % kStages, n = min(h.v1 - v, (uint32_t)kStageVecs);
+          ok = mbar_wait(&s_free[st], ((issued / kStages) & 1) ^ 1);
+          if (!ok) break;
+          mbar_arrive_expect_tx(&s_full[st], n * 16);
+          bulk_load(&s_ring[st * kStageVecs], h.vec() + v, n * 16, &s_full[st]);
         }
-        if (tid < edges) see(edge, edge_idx);
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-          const uint64_t other = __shfl_xor_sync(0xFFFFFFFFu, best, o);
-          best = other > best ? other : best;
-        }
-        __syncthreads();  // (s_best of the round before has been read)
-        if (lane == 0) s_best[warp] = best;
-        __syncthreads();
-        best = s_best[0];
-#pragma unroll 1
-        for (int i = 1; i < WARPS; ++i) best = s_best[i] > best ? s_best[i] : best;
-        last = best;
-        if (tid == 0) s_top[r] = best;
       }
     }
-  }
-
-  if (C > 1) cluster_sync();
-  else __syncthreads();
-  if (rank == 0) {
-    Sum r = s_cta;
-    for (uint32_t c = 1; c < C; ++c) {
-      const Sum other{ld_cluster_f32(&s_cta.m, c), ld_cluster_f32(&s_cta.s, c), ld_cluster_f32(&s_cta.e, c)};
-      r = join(r, other, k2);
-    }
-    const bool empty = r.m == neg_inf && r.s == 0.0f;
-    const bool bad = r.s != r.s;
-    const float nan = __uint_as_float(0x7FFFFFFFu);
-    const float ln_s = logf(r.s);
-    if (tid == 0) {
-      *reinterpret_cast<float2*>(a.stats + 2 * t) = bad ? make_float2(nan, nan) : make_float2(r.m, r.s);
-      if (a.entropy) a.entropy[t] = bad ? nan : empty ? 0.0f : ln_s - kLn2 * (r.e / r.s);
-      if (a.targets) {
-        const int64_t at = a.targets[t];
-        float v = 0.0f;
-        if (at >= a.V || (bad && at >= 0)) v = nan;
-        else if (at >= 0) v = empty ? neg_inf : (V8::load(row + at) - r.m) * a.scale - ln_s;
-        a.logprob[t] = v;
+  } else {
+    // ---------------- joins and results ----------------
+    auto near = [&](float v) { return v > -0.5f * far && v <= 0.5f * far; };
+    Scratch<TOP>& x = s_scratch[warp - kReaders / 32 - 1];
+    uint32_t rows = warp - kReaders / 32 - 1;
+    for (int64_t t = first + rows * stride; t < a.T; t += J * stride, rows += J) {
+      const Share<T> h = share_of<T>(a, t, rank, C);
+      const uint32_t buf = rows % B;
+      const float edge = lane < h.edges ? V8::load(h.row + h.edge_index(lane)) : neg_inf;
+      // (the target's logit now: two loads that depend on each other)
+      const int64_t target = a.targets && rank == 0 ? a.targets[t] : -1;
+      const float z_target = target >= 0 && target < a.V ? V8::load(h.row + target) : 0.0f;
+      if (!mbar_wait_warp(&s_done[buf], (rows / B) & 1)) ok = false;
+      const Partials& part = s_part[buf];
+      float most = edge;
+#pragma unroll 2
+      for (int i = lane; i < kReaders; i += 32) most = fmaxf(most, part.m[i]);
+      Sum r;
+      r.m = warp_max(most);
+      const float c = reference(fmaxf(r.m, -far), k2);
+      r.s = 0.0f, r.e = 0.0f;
+      bool odd = false;
+#pragma unroll 2
+      for (int i = lane; i < kReaders; i += 32) {
+        const float s = part.s[i];
+        odd |= s != s;  // NaN hides in a thread's maximum
+        const float d = reference(fmaxf(part.m[i], -far), k2) - c, f = ex2(d);
+        r.s += s * f;
+        r.e += (part.e[i] + s * d) * f;
       }
-    }
-    if (TOP) {
-      const uint32_t k = a.top_k;
+      if (lane < h.edges) {
+        const float y = __fmaf_rn(max_nan(edge, -far), k2, -c), p = ex2(y);
+        odd |= edge != edge;
+        r.s += p;
+        r.e += p * y;
+      }
+      r.s = warp_sum(r.s), r.e = warp_sum(r.e);
+      odd = __any_sync(0xFFFFFFFFu, odd);
+      if (odd) r.s = __uint_as_float(0x7FFFFFFFu);
+      if constexpr (TOP) {
+        share_top<T>(h, part.m, edge, odd, a.top_k, x);
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&s_read[buf]);  // (the partials are not needed any more)
       if (C > 1) {
-        for (uint32_t i = tid; i < C * k; i += THREADS) s_cand[i] = ld_cluster_u64(&s_top[i % k], i / k);
-        __syncthreads();
-        for (uint32_t i = tid; i < C * k; i += THREADS) {
-          const uint64_t c = s_cand[i];
-          uint32_t above = 0;
-          for (uint32_t j = 0; j < C * k; ++j) above += s_cand[j] > c;
-          if (c != 0 && above < k) s_group[above] = i;  // (entries are distinct: one writer per rank)
+        const uint32_t to0 = rank * a.top_k;
+        if (rank != 0) {  // to rank 0
+          if (!mbar_wait_warp(&s_taken[buf], ((rows / B) & 1) ^ 1)) ok = false;
+          const uint32_t at = mapa_shared(smem_u32(&s_joined[buf][rank]), 0);
+          if (lane == 0) {
+            st_cluster_f32(at, r.m);
+            st_cluster_f32(at + 4, r.s);
+            st_cluster_f32(at + 8, r.e);
+          }
+          if constexpr (TOP) {
+            if (lane < a.top_k) st_cluster_u64(mapa_shared(smem_u32(&s_joined_top[buf][to0 + lane]), 0), x.top[lane]);
+          }
+          asm volatile("fence.acq_rel.cluster;" ::: "memory");
+          __syncwarp();
+          if (lane == 0) mbar_arrive_cluster(mapa_shared(smem_u32(&s_pushed[buf]), 0));
+          continue;
         }
-        __syncthreads();
+        if (lane == 0) s_joined[buf][0] = r;
+        if constexpr (TOP) {
+          if (lane < a.top_k) s_joined_top[buf][lane] = x.top[lane];
+        }
+        __syncwarp();
+        if (!__all_sync(0xFFFFFFFFu, mbar_wait_cluster(&s_pushed[buf], (rows / B) & 1))) ok = false;
+        most = s_joined[buf][0].m;
+        for (uint32_t i = 1; i < C; ++i) most = fmaxf(most, s_joined[buf][i].m);
+        const float to = reference(fmaxf(most, -far), k2);
+        r.m = most, r.s = 0.0f, r.e = 0.0f;
+        for (uint32_t i = 0; i < C; ++i) {
+          const Sum o = s_joined[buf][i];
+          const float d = reference(fmaxf(o.m, -far), k2) - to, f = ex2(d);
+          r.s += o.s * f;
+          r.e += (o.e + o.s * d) * f;
+        }
+        if constexpr (TOP) {
+          const uint32_t n = C * a.top_k;
+          for (uint32_t i = lane; i < n; i += 32) {
+            const uint64_t y = s_joined_top[buf][i];
+            uint32_t better = 0;
+            for (uint32_t j = 0; j < n; ++j) better += s_joined_top[buf][j] > y;
+            if (y != 0 && better < a.top_k) x.top[better] = y;
+          }
+        }
+        __syncwarp();
+        if (lane > 0 && lane < C) mbar_arrive_cluster(mapa_shared(smem_u32(&s_taken[buf]), lane));
       }
-      if (tid < k) {
-        const uint64_t c = C > 1 ? s_cand[s_group[tid]] : s_top[tid];
-        const float z = key_value(static_cast<uint32_t>(c >> 32));
-        a.top_index[t * k + tid] = static_cast<int64_t>(0xFFFFFFFFu - static_cast<uint32_t>(c));
-        a.top_logprob[t * k + tid] = bad ? nan : empty ? neg_inf : (z - r.m) * a.scale - ln_s;
+      most = r.m;
+      float S, E;  // relative to the maximum
+      const bool empty = most == neg_inf;
+      if (near(most)) {
+        const float f = __fmaf_rn(-most, k2, reference(most, k2)), up = ex2(f);
+        S = r.s * up;
+        E = __fadd_rn(r.e, __fmul_rn(f, r.s)) * up;  // (uncontracted: one token alone gives exactly 0)
+      } else if (empty) {
+        S = r.s != r.s ? r.s : 0.0f, E = 0.0f;
+      } else {  // a maximum far out: the whole row again, relative to it
+        S = 0.0f, E = 0.0f;
+        auto add = [&](float z) {
+          const float y = max_nan((z - most) * k2, kFloor), p = ex2(y);
+          S += p;
+          E += p * y;
+        };
+#pragma unroll 4
+        for (uint32_t i = lane; i < h.cut.vecs; i += 32) {
+          float f[N];
+          V8::unpack(h.vec()[i], f);
+#pragma unroll
+          for (int j = 0; j < N; ++j) add(f[j]);
+        }
+        if (lane < h.edges) add(edge);
+        S = warp_sum(S), E = warp_sum(E);
+      }
+      const bool bad = S != S, none = empty && !bad;
+      const float nan = __uint_as_float(0x7FFFFFFFu);
+      const float ln_s = logf(S);
+      if (lane == 0) {
+        *reinterpret_cast<float2*>(a.stats + 2 * t) = bad ? make_float2(nan, nan) : make_float2(most, S);
+        if (a.entropy) a.entropy[t] = bad ? nan : none ? 0.0f : ln_s - kLn2 * (E / S);
+        if (a.targets) {
+          float v = 0.0f;
+          if (target >= a.V || (bad && target >= 0)) v = nan;
+          else if (target >= 0) v = none ? neg_inf : (z_target - most) * a.scale - ln_s;
+          a.logprob[t] = v;
+        }
+      }
+      if constexpr (TOP) {
+        if (lane < a.top_k) {
+          const uint64_t y = x.top[lane];
+          const float z = key_value(static_cast<uint32_t>(y >> 32));
+          a.top_index[t * a.top_k + lane] = static_cast<int64_t>(0xFFFFFFFFu - static_cast<uint32_t>(y));
+          a.top_logprob[t * a.top_k + lane] = bad ? nan : none ? neg_inf : (z - most) * a.scale - ln_s;
+        }
+        __syncwarp();
       }
     }
   }
-  if (C > 1) cluster_sync();  // rank 0 has read this CTA's shared memory
+  if (!ok) drain_pause();  // a wait expired: let copies still in flight land first
+  if (C > 1) {
+    __syncwarp();
+    cluster_sync();  // nobody signals a CTA that has gone
+  }
 }
 
 // ---------------------------------------------------------------------------
-// Gradient: dz = e (A + B x2) with e = 2^x2, A = (-G - g_H (H - ln S)) scale / S, B = -g_H ln 2 scale / S,
+// Gradient: dz = 2^x (A + B x) with x = (z - m) k2, A = (-G - g_H (H - ln S)) scale / S, B = -g_H ln 2 scale / S,
 // plus the single entries' own gradients.  One CTA per chunk of a row.
 // ---------------------------------------------------------------------------
 constexpr int kBwdThreads = 256, kBwdVecs = 4;
 
 template <typename T, bool TOP>
-__global__ void __launch_bounds__(kBwdThreads) logprob_bwd_kernel(const LogprobBwdArgs a, uint32_t chunks) {
+__global__ void __launch_bounds__(kBwdThreads, 8) logprob_bwd_kernel(const LogprobBwdArgs a, uint32_t chunks,
+                                                                    const float far) {
   using V8 = Vec<T>;
   constexpr int N = V8::N;
   const int64_t t = blockIdx.x / chunks;
@@ -412,8 +706,10 @@ __global__ void __launch_bounds__(kBwdThreads) logprob_bwd_kernel(const LogprobB
   if (gh != 0.0f && s != 0.0f) c0 -= gh * (a.entropy[t] - logf(s));
   const float A = wrong ? nan : s == 0.0f ? 0.0f : c0 * inv, B = -gh * kLn2 * inv;
   const float k2 = a.scale * kLog2e;
+  // beside a maximum far out nothing may be clamped (NaN: everything is; banned tokens only: all zeros either way)
+  const bool near = m > -0.5f * far && m <= 0.5f * far;
   auto base = [&](float z) {
-    const float x = fmaxf((z - m) * k2, kFloor);
+    const float x = near ? (fmaxf(z, -far) - m) * k2 : fmaxf((z - m) * k2, kFloor);
     return ex2(x) * __fmaf_rn(B, x, A);
   };
   const float own_t = gt * a.scale;
@@ -445,7 +741,10 @@ __global__ void __launch_bounds__(kBwdThreads) logprob_bwd_kernel(const LogprobB
   if (wide) {
     const uint4* vec = reinterpret_cast<const uint4*>(row + cut.head);
     uint4* dst = reinterpret_cast<uint4*>(out + cut.head);
-    const uint32_t i0 = chunk * kVecs + tid;
+    const uint32_t i0 = chunk * kVecs + tid, low = V8::low_bits(-far);
+    const int64_t target_at = target - cut.head;
+    const uint32_t target_vec = target >= 0 && target_at >= 0 && target < a.V ? (uint32_t)(target_at / N) : 0xFFFFFFFFu;
+    const int target_in = (int)(target_at % N);
     uint4 q[kBwdVecs];
 #pragma unroll
     for (int u = 0; u < kBwdVecs; ++u)
@@ -455,14 +754,25 @@ __global__ void __launch_bounds__(kBwdThreads) logprob_bwd_kernel(const LogprobB
       const uint32_t i = i0 + u * kBwdThreads;
       if (i >= cut.vecs) break;
       float f[N], d[N];
-      V8::unpack(q[u], f);
+      if (near) {
+        q[u].x = V8::max1(q[u].x, low), q[u].y = V8::max1(q[u].y, low);
+        q[u].z = V8::max1(q[u].z, low), q[u].w = V8::max1(q[u].w, low);
+        V8::unpack(q[u], f);
 #pragma unroll
-      for (int j = 0; j < N; ++j) d[j] = base(f[j]);
-      if (!TOP) {
-        const int64_t at = target - cut.head - (int64_t)i * N;
+        for (int j = 0; j < N; j += 2) {
+          const float2 x = __fmul2_rn(__fadd2_rn(make_float2(f[j], f[j + 1]), make_float2(-m, -m)), make_float2(k2, k2));
+          const float2 y = __fmul2_rn(make_float2(ex2(x.x), ex2(x.y)), __ffma2_rn(make_float2(B, B), x, make_float2(A, A)));
+          d[j] = y.x, d[j + 1] = y.y;
+        }
+      } else {
+        V8::unpack(q[u], f);
+#pragma unroll
+        for (int j = 0; j < N; ++j) d[j] = base(f[j]);
+      }
+      if (!TOP && i == target_vec) {
 #pragma unroll
         for (int j = 0; j < N; ++j)
-          if (at == j && f[j] != neg_inf) d[j] += own_t;
+          if (j == target_in && V8::load(row + target) != neg_inf) d[j] += own_t;
       }
       dst[i] = V8::pack(d);
     }
@@ -489,11 +799,18 @@ __global__ void __launch_bounds__(kBwdThreads) logprob_bwd_kernel(const LogprobB
   }
 }
 
-template <typename T, int THREADS, bool TOP>
-static cudaError_t launch_fwd(const LogprobArgs& a, uint32_t cluster, cudaStream_t s) {
+template <typename T, bool TOP>
+static cudaError_t launch_fwd(const LogprobArgs& a, float far, uint32_t cluster, int num_sms, cudaStream_t s) {
+  auto kernel = logprob_kernel<T, TOP>;
+  static const cudaError_t attr_err =
+      cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
+  if (attr_err != cudaSuccess) return attr_err;
+  const int64_t slots = (int64_t)num_sms * per_sm_of(TOP);
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<uint32_t>(a.T) * cluster);
-  cfg.blockDim = dim3(THREADS);
+  const int64_t clusters = slots / cluster;
+  cfg.gridDim = dim3(static_cast<uint32_t>((a.T < clusters ? a.T : clusters) * cluster));
+  cfg.blockDim = dim3(threads_of(TOP));
+  cfg.dynamicSmemBytes = kSmemBytes;
   cfg.stream = s;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -502,18 +819,30 @@ static cudaError_t launch_fwd(const LogprobArgs& a, uint32_t cluster, cudaStream
   attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, logprob_kernel<T, THREADS, TOP>, a);
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, a, far);
   count_launch();
   return e;
 }
 
+// The power of two with far k2 in (2^29, 2^30]: its product with k2 is exact, x stays below 2^7 where the
+// reference is rounded (2^30 2^-24), and a logit clamped to -far beside a maximum above -far / 2 has 2^x = 0.
+static float far_of(float scale) { return ldexpf(1.0f, 30 - (ilogbf(scale * kLog2e) + 1)); }
+
 template <typename T>
 static cudaError_t launch_fwd_t(const LogprobArgs& a, int num_sms, cudaStream_t s) {
-  // Few rows: a cluster of up to 8 CTAs shares a row, while the CTAs of all rows fit the SMs about
-  // twice and each still has a vector or more per thread.
+  // The cluster size with the least work for the busiest CTA, rows / C times their number: one long row wants a
+  // large cluster, and so do 515 rows for 304 CTAs (two rows where one CTA takes a whole one, 1.75 in clusters of
+  // four); many rows want none, which has nothing to join.  A share is at least one stage of the ring.
+  const int64_t slots = (int64_t)num_sms * per_sm_of(a.top_k > 0);
   uint32_t cluster = 1;
-  while (cluster < 8 && a.T * cluster < num_sms && a.V / (cluster * 2) >= 256 * Vec<T>::N) cluster *= 2;
-  return a.top_k ? launch_fwd<T, 256, true>(a, cluster, s) : launch_fwd<T, 256, false>(a, cluster, s);
+  double least = 0;
+  for (uint32_t c = 1; c <= kMaxCluster && (c == 1 || a.V / c >= kStageVecs * Vec<T>::N); c *= 2) {
+    const int64_t clusters = slots / c;
+    const double work = (double)((a.T + clusters - 1) / clusters) / c;
+    if (c == 1 || work < 0.95 * least) cluster = c, least = work;
+  }
+  const float far = far_of(a.scale);
+  return a.top_k ? launch_fwd<T, true>(a, far, cluster, num_sms, s) : launch_fwd<T, false>(a, far, cluster, num_sms, s);
 }
 
 }  // namespace lp
@@ -528,8 +857,9 @@ static cudaError_t launch_bwd_t(const LogprobBwdArgs& a, cudaStream_t s) {
   const int64_t chunks = (a.V + per - 1) / per;
   if (a.T * chunks > INT32_MAX) return cudaErrorInvalidConfiguration;
   const dim3 grid(static_cast<uint32_t>(a.T * chunks));
-  if (a.top_k) lp::logprob_bwd_kernel<T, true><<<grid, lp::kBwdThreads, 0, s>>>(a, (uint32_t)chunks);
-  else lp::logprob_bwd_kernel<T, false><<<grid, lp::kBwdThreads, 0, s>>>(a, (uint32_t)chunks);
+  const float far = lp::far_of(a.scale);
+  if (a.top_k) lp::logprob_bwd_kernel<T, true><<<grid, lp::kBwdThreads, 0, s>>>(a, (uint32_t)chunks, far);
+  else lp::logprob_bwd_kernel<T, false><<<grid, lp::kBwdThreads, 0, s>>>(a, (uint32_t)chunks, far);
   const cudaError_t e = cudaGetLastError();
   count_launch();
   return e;
@@ -537,6 +867,15 @@ static cudaError_t launch_bwd_t(const LogprobBwdArgs& a, cudaStream_t s) {
 cudaError_t launch_token_logprobs_bwd(const LogprobBwdArgs& a, int num_sms, cudaStream_t s) {
   (void)num_sms;
   return a.f32 ? launch_bwd_t<float>(a, s) : launch_bwd_t<__nv_bfloat16>(a, s);
+}
+
+cudaError_t logprob_status_read_clear(unsigned int* out, cudaStream_t s) {
+  cudaError_t e = cudaStreamSynchronize(s);
+  if (e != cudaSuccess) return e;
+  e = cudaMemcpyFromSymbol(out, g_status, sizeof(unsigned int));
+  if (e != cudaSuccess) return e;
+  const unsigned int zero = 0;
+  return cudaMemcpyToSymbol(g_status, &zero, sizeof(unsigned int));
 }
 
 }  // namespace nvfp4

@@ -147,6 +147,43 @@ def test_many_equal_logits_give_the_lowest_indices(F, dtype):
 
 @pytest.mark.gpu
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("V", [900, 32000, 131072])
+def test_few_tokens_allowed(F, dtype, V):
+    # constrained decoding: all but a few tokens banned, by -inf and by the type's lowest value
+    z, _ = make(5, V, dtype, V)
+    for row, (allowed, fill) in enumerate([(1, -INF), (3, -INF), (40, -INF), (3, torch.finfo(dtype).min), (70, -1e30)]):
+        keep = torch.randperm(V, generator=torch.Generator().manual_seed(row))[:allowed].to(DEV)
+        kept = z[row, keep].clone()
+        z[row] = fill
+        z[row, keep] = kept
+    z[4, ::3] = -INF
+    for k in (1, 20, 32):
+        check_forward(F, z, torch.arange(5, device=DEV), 1.0, k)
+    check_backward(F, z, torch.arange(5, device=DEV), 1.0, 20, "lht")
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_extreme_logits_and_temperatures(F, dtype):
+    z = torch.zeros((5, 3000), dtype=dtype, device=DEV)
+    z[0] = torch.linspace(2e38, 3e38, 3000).to(dtype)
+    z[1] = torch.linspace(-3e38, -2e38, 3000).to(dtype)
+    z[2, 5:9] = 1e33
+    z[3] = -1e36
+    z[3, 77] = 1e36
+    z[4] = 1e29
+    targets = torch.tensor([2999, 2999, 6, 77, 3], device=DEV)
+    check_forward(F, z, targets, 1.0, 5)
+    check_backward(F, z, targets, 1.0, 5, "lht")
+    z = make(4, 3000, dtype, 2)[0]
+    z[1, :1500] = -INF
+    for temperature in (1e-20, 1e-3, 1e3, 1e20):
+        check_forward(F, z, targets[:4], temperature, 5)
+        check_backward(F, z, targets[:4], temperature, 0, "lh")
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
 def test_nan_and_infinity(F, dtype):
     V = 5000
     z, _ = make(4, V, dtype, 3)
