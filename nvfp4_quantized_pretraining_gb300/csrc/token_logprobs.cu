@@ -233,7 +233,7 @@ __device__ __forceinline__ void share_top(const Share<T> h, const float* maxima,
 
   uint32_t above = 0, equal = 0;  // entries in the lists
   // Fills the lists with the share's elements above tau and, with_equal, those equal to it; false if they do not fit
-  // (the lists then hold as many of them as do).
+  // (the lists then hold as many of the first ones as do).
   auto collect = [&](bool with_equal) {
     uint32_t strips = 0;
     const uint32_t bound = with_equal ? tau : tau + 1;
@@ -250,8 +250,8 @@ __device__ __forceinline__ void share_top(const Share<T> h, const float* maxima,
     const uint32_t per = (h.v1 - h.v0 + kReaders - 1) / kReaders;
     const uint32_t shift = per >= 32 ? 5 : per > 1 ? 32 - __clz(per - 1) : 0;  // 2^shift lanes take a strip's vectors
     uint32_t hits = 0;
-    for (uint32_t w0 = 0; w0 < per; w0 += 1u << shift) {
-      for (uint32_t q = lane >> shift; q - (lane >> shift) < strips; q += 4 * (32 >> shift)) {
+    for (uint32_t w0 = 0; w0 < per && hits <= kCap; w0 += 1u << shift) {
+      for (uint32_t q = lane >> shift; q - (lane >> shift) < strips && hits <= kCap; q += 4 * (32 >> shift)) {
         uint4 w[4];
         uint32_t at[4];
 #pragma unroll
@@ -830,17 +830,12 @@ static float far_of(float scale) { return ldexpf(1.0f, 30 - (ilogbf(scale * kLog
 
 template <typename T>
 static cudaError_t launch_fwd_t(const LogprobArgs& a, int num_sms, cudaStream_t s) {
-  // The cluster size with the least work for the busiest CTA, rows / C times their number: one long row wants a
-  // large cluster, and so do 515 rows for 304 CTAs (two rows where one CTA takes a whole one, 1.75 in clusters of
-  // four); many rows want none, which has nothing to join.  A share is at least one stage of the ring.
+  // Clusters only where whole rows leave CTAs without one, and then as large as all rows' CTAs fit at once (a share
+  // at least one stage of the ring): joining shares costs more than an uneven last round (515 x 50021 FP32, top 5:
+  // 25 us in single CTAs, 27, 46 and 74 in clusters of 2, 4 and 8; 64 x 131072 BF16, top 20: 35 and 21 in 1 and 4).
   const int64_t slots = (int64_t)num_sms * per_sm_of(a.top_k > 0);
   uint32_t cluster = 1;
-  double least = 0;
-  for (uint32_t c = 1; c <= kMaxCluster && (c == 1 || a.V / c >= kStageVecs * Vec<T>::N); c *= 2) {
-    const int64_t clusters = slots / c;
-    const double work = (double)((a.T + clusters - 1) / clusters) / c;
-    if (c == 1 || work < 0.95 * least) cluster = c, least = work;
-  }
+  while (cluster < kMaxCluster && a.T * cluster * 2 <= slots && a.V / (cluster * 2) >= kStageVecs * Vec<T>::N) cluster *= 2;
   const float far = far_of(a.scale);
   return a.top_k ? launch_fwd<T, true>(a, far, cluster, num_sms, s) : launch_fwd<T, false>(a, far, cluster, num_sms, s);
 }
