@@ -481,8 +481,8 @@ fp4_status fp4_token_logprobs_bwd(const void* logits, int dtype, int64_t T, int6
  *
  * grad_scale (optional, device): multiplies every gradient (a clipping coefficient);
  * if it is not finite the call leaves everything as it was.
- * Pointers are aligned to their elements; with all of them 16-byte aligned (codes
- * 8-byte) the kernel uses wide accesses.  A tensor with numel 0 is skipped; the others'
+ * Pointers are aligned to their elements; with all but the scales' 16-byte aligned the
+ * kernel uses wide accesses.  A tensor with numel 0 is skipped; the others'
  * buffers may not overlap.  grad_dtype: FP4_OUT_BF16 or FP4_OUT_F32 for all tensors.
  * lr, eps >= 0, 0 <= beta < 1, 1 <= step < 2^32.  n = 0 is a call without work. */
 typedef struct {

@@ -9,9 +9,12 @@
 //   size = lr / (1 - b1^t), root = 1 / sqrt(1 - b2^t)   (computed in FP64 on the host)
 // and with 8-bit states m and v are rounded after p has used them unrounded.
 //
-// The step is bound by memory: 30 bytes per element with FP32 states, FP32 gradients and a BF16 copy;
-// 16 with 8-bit states and BF16 gradients.  A thread owns 8 consecutive elements, so a block of 128 is
-// 16 lanes and its amax four shuffles; every stream moves in 8- or 16-byte accesses.
+// The step is bound by memory (30 bytes per element with FP32 states, FP32 gradients and a BF16 copy, 16 with 8-bit
+// states, BF16 gradients and a copy) and, with 8-bit states, nearly as much by issue slots: 6.8 TB/s leaves 87
+// instructions per element for two square roots' worth of exact arithmetic, two random numbers and two codes.  So the
+// inputs come through a ring of shared-memory stages by bulk copies (loads in flight without registers), arithmetic
+// goes in packed pairs, and a thread owns 8 consecutive elements: a block of 128 is 16 lanes, its amax four shuffles,
+// its random bits one generator call per moment.
 #include <cuda_bf16.h>
 
 #include "common.cuh"
@@ -40,16 +43,28 @@ struct Table {
   uint32_t first_chunk[CAP + 1];
 };
 
-__device__ __forceinline__ void load8(float (&x)[8], const float* p) {
-  const float4 a = *reinterpret_cast<const float4*>(p), b = *reinterpret_cast<const float4*>(p + 4);
-  x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w, x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
+// Pairs of FP32 operations, each rounded by itself.  Products that feed no sum are packed; a packed product and
+// sum were contracted into one rounding (seen as a last bit of the parameters), so sums take scalar products.
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) { return __fmul2_rn(a, b); }
+__device__ __forceinline__ float2 mul_each(float2 a, float b) { return make_float2(__fmul_rn(a.x, b), __fmul_rn(a.y, b)); }
+__device__ __forceinline__ float2 add_each(float2 a, float2 b) {
+  return make_float2(__fadd_rn(a.x, b.x), __fadd_rn(a.y, b.y));
 }
-__device__ __forceinline__ void store8(float* p, const float (&x)[8]) {
-  *reinterpret_cast<float4*>(p) = make_float4(x[0], x[1], x[2], x[3]);
-  *reinterpret_cast<float4*>(p + 4) = make_float4(x[4], x[5], x[6], x[7]);
+__device__ __forceinline__ void load8(float2 (&x)[4], const float* p) {
+  const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
+  x[0] = make_float2(a.x, a.y), x[1] = make_float2(a.z, a.w), x[2] = make_float2(b.x, b.y), x[3] = make_float2(b.z, b.w);
 }
-__device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
-  const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
+__device__ __forceinline__ void load8_bf16(float2 (&x)[4], const __nv_bfloat16* p) {
+  const uint4 q = *reinterpret_cast<const uint4*>(p);
+  x[0] = make_float2(bf16_lo(q.x), bf16_hi(q.x)), x[1] = make_float2(bf16_lo(q.y), bf16_hi(q.y));
+  x[2] = make_float2(bf16_lo(q.z), bf16_hi(q.z)), x[3] = make_float2(bf16_lo(q.w), bf16_hi(q.w));
+}
+__device__ __forceinline__ void store8(float* p, const float2 (&x)[4]) {
+  reinterpret_cast<float4*>(p)[0] = make_float4(x[0].x, x[0].y, x[1].x, x[1].y);
+  reinterpret_cast<float4*>(p)[1] = make_float4(x[2].x, x[2].y, x[3].x, x[3].y);
+}
+__device__ __forceinline__ uint32_t pack_bf16(float2 a) {
+  const __nv_bfloat162 v = __floats2bfloat162_rn(a.x, a.y);
   return *reinterpret_cast<const uint32_t*>(&v);
 }
 
@@ -91,11 +106,137 @@ __device__ __forceinline__ uint2 encode8(const float (&a)[8], const uint4& rnd, 
   return make_uint2(out[0], out[1]);
 }
 
+// The same for blocks whose values are all finite and whose scale leaves 2^-e * 2^-line a normal number (byte at most
+// kFastByte: amax up to 448 2^6, 57344 2^14), with the amax known: one product per value, and the codes of
+// four values gathered from the top bytes of (pattern + addend) << 4 or 3.
+template <int SHIFT>
+struct Fast {
+  static constexpr uint32_t kByte = SHIFT == 20 ? 133 : 141;
+  // 2^(127 - byte) 2^-120 or 2^-112
+  __device__ static __forceinline__ float factor(uint32_t byte) {
+    return __uint_as_float(((SHIFT == 20 ? 134u : 142u) - byte) << 23);
+  }
+};
+// Byte I of each of four words.
+template <int I>
+__device__ __forceinline__ uint32_t bytes(uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  return __byte_perm(__byte_perm(a, b, I | (4 + I) << 4), __byte_perm(c, d, I | (4 + I) << 4), 0x5410);
+}
+template <int SHIFT, bool FLOOR, bool SR>
+__device__ __forceinline__ uint2 encode8_fast(const float2 (&a)[4], const uint32_t (&w)[4], uint32_t byte) {
+  const float f = Fast<SHIFT>::factor(byte);
+  uint32_t t[8];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 y = mul2(a[i], make_float2(f, f));
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      const uint32_t bits = __float_as_uint(j ? y.y : y.x);
+      uint32_t v;  // (a sign bit stays where it is: the magnitude's sum has no carry that far)
+      if (SR) v = bits + (j ? w[i] >> 16 << (SHIFT - 16) : w[i] << 16 >> (32 - SHIFT));
+      else v = bits + (1u << (SHIFT - 1)) - 1u + ((bits >> SHIFT) & 1u);
+      if (FLOOR && (j ? a[i].y : a[i].x) > 0.0f) v = max(v, 1u << SHIFT);
+      t[2 * i + j] = v;
+    }
+  }
+  uint2 out;
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const uint32_t* q = t + 4 * h;
+    uint32_t codes = bytes<0>(q[0] >> SHIFT, q[1] >> SHIFT, q[2] >> SHIFT, q[3] >> SHIFT);
+    if (!FLOOR) codes = (codes & 0x7F7F7F7Fu) | (bytes<3>(q[0], q[1], q[2], q[3]) & 0x80808080u);  // the signs
+    (h ? out.y : out.x) = codes;
+  }
+  return out;
+}
+// The magnitude pattern of the largest of eight values; NaN if one is.
+__device__ __forceinline__ float max_nan_abs(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(fabsf(a)), "f"(fabsf(b)));
+  return r;
+}
+__device__ __forceinline__ uint32_t amax16(const float2 (&a)[4]) {
+  float m = max_nan_abs(max_nan_abs(max_nan_abs(a[0].x, a[0].y), max_nan_abs(a[1].x, a[1].y)),
+                        max_nan_abs(max_nan_abs(a[2].x, a[2].y), max_nan_abs(a[3].x, a[3].y)));
+#pragma unroll
+  for (int o = 1; o < 16; o <<= 1) m = max_nan_abs(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
+  return __float_as_uint(m);
+}
+
+// The random words of m and v for the group of eight elements j of a tensor with stream ids st, st + 1.  For j < 2^32
+// the two generators' first round and half of the second have the same products.
+struct RandomPair {
+  uint32_t m[4], v[4];
+};
+struct RandomBase {  // what does not depend on j: of a tensor
+  uint32_t hm, lm, hv, lv;  // round 2's product with word 0
+  uint32_t y1m, y1v;        // round 1's word 1
+};
+__device__ __forceinline__ RandomBase random_base(uint32_t st, const PhiloxKeys& k) {
+  RandomBase b;
+  const uint64_t pm = (uint64_t)0xCD9E8D57u * st, pv = (uint64_t)0xCD9E8D57u * (st + 1);
+  const uint64_t qm = (uint64_t)0xD2511F53u * ((uint32_t)(pm >> 32) ^ k.k0[0]);
+  const uint64_t qv = (uint64_t)0xD2511F53u * ((uint32_t)(pv >> 32) ^ k.k0[0]);
+  b.hm = (uint32_t)(qm >> 32), b.lm = (uint32_t)qm, b.hv = (uint32_t)(qv >> 32), b.lv = (uint32_t)qv;
+  b.y1m = (uint32_t)pm, b.y1v = (uint32_t)pv;
+  return b;
+}
+__device__ __forceinline__ void philox_tail(uint32_t (&o)[4], uint4 c, const PhiloxKeys& k) {
+#pragma unroll
+  for (int r = 2; r < 10; ++r) {
+    const uint64_t p0 = static_cast<uint64_t>(0xD2511F53u) * c.x;
+    const uint64_t p1 = static_cast<uint64_t>(0xCD9E8D57u) * c.z;
+    c = make_uint4(static_cast<uint32_t>(p1 >> 32) ^ c.y ^ k.k0[r], static_cast<uint32_t>(p1),
+                   static_cast<uint32_t>(p0 >> 32) ^ c.w ^ k.k1[r], static_cast<uint32_t>(p0));
+  }
+  o[0] = c.x, o[1] = c.y, o[2] = c.z, o[3] = c.w;
+}
+__device__ __forceinline__ RandomPair random_pair(int64_t group, uint32_t st, uint32_t step, const RandomBase& b,
+                                                  const PhiloxKeys& k) {
+  const uint32_t j = static_cast<uint32_t>(group), high = static_cast<uint32_t>(group >> 32);
+  if (high) {
+    const uint4 m = philox4x32_10(make_uint4(j, high, st, step), k), v = philox4x32_10(make_uint4(j, high, st + 1, step), k);
+    return RandomPair{{m.x, m.y, m.z, m.w}, {v.x, v.y, v.z, v.w}};
+  }
+  const uint64_t p = (uint64_t)0xD2511F53u * j;
+  const uint32_t z1 = (uint32_t)(p >> 32) ^ step ^ k.k1[0], w1 = (uint32_t)p;  // words 2 and 3 after round 1
+  const uint64_t q = (uint64_t)0xCD9E8D57u * z1;
+  const uint32_t h = (uint32_t)(q >> 32) ^ k.k0[1], l = (uint32_t)q;
+  RandomPair r;
+  philox_tail(r.m, make_uint4(h ^ b.y1m, l, b.hm ^ w1 ^ k.k1[1], b.lm), k);
+  philox_tail(r.v, make_uint4(h ^ b.y1v, l, b.hv ^ w1 ^ k.k1[1], b.lv), k);
+  return r;
+}
+
+// A stage of the ring: one whole chunk's parameters, gradients, moments and scales.
+template <bool GBF16, bool BITS8>
+struct Stage {
+  float p[kChunk];
+  uint8_t g[kChunk * (GBF16 ? 2 : 4)];
+  uint8_t m[kChunk * (BITS8 ? 1 : 4)], v[kChunk * (BITS8 ? 1 : 4)];
+  uint8_t m_scale[BITS8 ? kChunk / kFp8Block : 16], v_scale[BITS8 ? kChunk / kFp8Block : 16];
+};
+__host__ __device__ constexpr int stages_of(bool bits8) { return bits8 ? 3 : 2; }
+constexpr int kPerSm = 3;  // CTAs
+
 template <bool GBF16, bool BITS8, bool SR, int CAP>
-__global__ void __launch_bounds__(kThreads) adamw_kernel(const __grid_constant__ Table<CAP> tab,
-                                                         const __grid_constant__ Scalars k) {
+__global__ void __launch_bounds__(kThreads + 32, kPerSm)
+    adamw_kernel(const __grid_constant__ Table<CAP> tab, const __grid_constant__ Scalars k) {
+  using St = Stage<GBF16, BITS8>;
+  constexpr int kStages = stages_of(BITS8);
+  extern __shared__ __align__(16) uint8_t s_raw[];
+  St* ring = reinterpret_cast<St*>(s_raw);
+  __shared__ uint64_t s_full[kStages], s_free[kStages];
   const float gs = k.grad_scale ? *k.grad_scale : 1.0f;
   if (!(fabsf(gs) <= 3.402823466e38f)) return;  // the caller's signal that this step is not to be taken
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < kStages; ++i) {
+      mbar_init(&s_full[i], BITS8 ? 2 : 1);  // the copies, and the scales
+      mbar_init(&s_free[i], kThreads / 32);
+    }
+    fence_mbar_init();
+  }
+  __syncthreads();
   // this CTA's consecutive chunks, and the tensor of the first one
   const uint32_t c0 = static_cast<uint32_t>((uint64_t)k.chunks * blockIdx.x / gridDim.x);
   const uint32_t c1 = static_cast<uint32_t>((uint64_t)k.chunks * (blockIdx.x + 1) / gridDim.x);
@@ -105,135 +246,186 @@ __global__ void __launch_bounds__(kThreads) adamw_kernel(const __grid_constant__
     if (tab.first_chunk[mid] <= c0) lo = mid;
     else hi = mid;
   }
-  for (uint32_t c = c0; c < c1; ++c) {
-    while (tab.first_chunk[lo + 1] <= c) ++lo;
-    const AdamWEntry& t = tab.t[lo];
-    const int64_t e0 = (int64_t)(c - tab.first_chunk[lo]) * kChunk + threadIdx.x * 8;
-    const int64_t left = t.numel - e0;
-    const bool whole = left >= 8 && t.vector;
-    float p[8], g[8], m[8], v[8];
-    uint32_t mb = 0, vb = 0;
-    if (whole) {
-      load8(p, t.param + e0);
-      if (GBF16) {
-        const uint4 q = *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(t.grad) + e0);
-        g[0] = bf16_lo(q.x), g[1] = bf16_hi(q.x), g[2] = bf16_lo(q.y), g[3] = bf16_hi(q.y);
-        g[4] = bf16_lo(q.z), g[5] = bf16_hi(q.z), g[6] = bf16_lo(q.w), g[7] = bf16_hi(q.w);
-      } else {
-        load8(g, static_cast<const float*>(t.grad) + e0);
+  bool ok = true;
+  // whole chunks of tensors whose pointers allow it come through the ring, the others by loads of their own
+  auto in_ring = [&](const AdamWEntry& t, int64_t first) { return t.vector && t.numel - first >= kChunk; };
+
+  if (threadIdx.x >= kThreads) {
+    const uint32_t lane = threadIdx.x - kThreads;
+    uint32_t n = 0;
+    for (uint32_t c = c0; c < c1; ++c) {
+      while (tab.first_chunk[lo + 1] <= c) ++lo;
+      const AdamWEntry& t = tab.t[lo];
+      const int64_t first = (int64_t)(c - tab.first_chunk[lo]) * kChunk;
+      if (!in_ring(t, first)) continue;
+      St& st = ring[n % kStages];
+      uint64_t* bar = &s_full[n % kStages];
+      ok = mbar_wait_warp(&s_free[n % kStages], ((n / kStages) & 1) ^ 1);
+      if (!ok) break;
+      if (lane == 0) {
+        mbar_arrive_expect_tx(bar, sizeof(st.p) + sizeof(st.g) + sizeof(st.m) + sizeof(st.v));
+        bulk_load(st.p, t.param + first, sizeof(st.p), bar);
+        bulk_load(st.g, static_cast<const uint8_t*>(t.grad) + first * (GBF16 ? 2 : 4), sizeof(st.g), bar);
+        bulk_load(st.m, static_cast<const uint8_t*>(t.m) + first * (BITS8 ? 1 : 4), sizeof(st.m), bar);
+        bulk_load(st.v, static_cast<const uint8_t*>(t.v) + first * (BITS8 ? 1 : 4), sizeof(st.v), bar);
       }
-    } else {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const bool in = i < left;
-        p[i] = in ? t.param[e0 + i] : 0.0f;
-        if (GBF16) g[i] = in ? __bfloat162float(static_cast<const __nv_bfloat16*>(t.grad)[e0 + i]) : 0.0f;
-        else g[i] = in ? static_cast<const float*>(t.grad)[e0 + i] : 0.0f;
+      if (BITS8) {  // the scale bytes by loads: 16 of each, of any alignment
+        const uint8_t* from = lane < 16 ? t.m_scale : t.v_scale;
+        (lane < 16 ? st.m_scale : st.v_scale)[lane & 15] = from[first / kFp8Block + (lane & 15)];
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar);
       }
+      ++n;
     }
-    if (BITS8) {
-      uint2 mc = make_uint2(0, 0), vc = make_uint2(0, 0);
-      const uint8_t* mp = static_cast<const uint8_t*>(t.m) + e0;
-      const uint8_t* vp = static_cast<const uint8_t*>(t.v) + e0;
-      if (whole) {
-        mc = *reinterpret_cast<const uint2*>(mp);
-        vc = *reinterpret_cast<const uint2*>(vp);
+  } else {
+    RandomBase base{};
+    if (SR) base = random_base(2u * (k.first_tensor + lo), k.keys);
+    uint32_t used = 0;
+    for (uint32_t c = c0; c < c1; ++c) {
+      if (tab.first_chunk[lo + 1] <= c) {
+        while (tab.first_chunk[lo + 1] <= c) ++lo;
+        if (SR) base = random_base(2u * (k.first_tensor + lo), k.keys);
+      }
+      const AdamWEntry& t = tab.t[lo];
+      const int64_t first = (int64_t)(c - tab.first_chunk[lo]) * kChunk, e0 = first + threadIdx.x * 8;
+      const int64_t left = t.numel - e0;
+      const bool whole = left >= 8 && t.vector;
+
+      // ---- eight elements; those past the tensor are zeros
+      float2 p[4], g[4], m[4], v[4];
+      uint2 mc = make_uint2(0, 0), vc = mc;
+      uint32_t mb = 0, vb = 0;
+      if (in_ring(t, first)) {
+        const St& st = ring[used % kStages];
+        if (ok) ok = mbar_wait(&s_full[used % kStages], (used / kStages) & 1);
+        load8(p, st.p + threadIdx.x * 8);
+        if (GBF16) load8_bf16(g, reinterpret_cast<const __nv_bfloat16*>(st.g) + threadIdx.x * 8);
+        else load8(g, reinterpret_cast<const float*>(st.g) + threadIdx.x * 8);
+        if (BITS8) {
+          mc = reinterpret_cast<const uint2*>(st.m)[threadIdx.x], vc = reinterpret_cast<const uint2*>(st.v)[threadIdx.x];
+          mb = st.m_scale[threadIdx.x / 16], vb = st.v_scale[threadIdx.x / 16];
+        } else {
+          load8(m, reinterpret_cast<const float*>(st.m) + threadIdx.x * 8);
+          load8(v, reinterpret_cast<const float*>(st.v) + threadIdx.x * 8);
+        }
+        __syncwarp();
+        if ((threadIdx.x & 31) == 0) mbar_arrive(&s_free[used % kStages]);  // (the values are in registers)
+        ++used;
+      } else if (whole) {
+        load8(p, t.param + e0);
+        if (GBF16) load8_bf16(g, static_cast<const __nv_bfloat16*>(t.grad) + e0);
+        else load8(g, static_cast<const float*>(t.grad) + e0);
+        if (BITS8) {
+          mc = *reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(t.m) + e0);
+          vc = *reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(t.v) + e0);
+          mb = t.m_scale[e0 / kFp8Block], vb = t.v_scale[e0 / kFp8Block];
+        } else {
+          load8(m, static_cast<const float*>(t.m) + e0);
+          load8(v, static_cast<const float*>(t.v) + e0);
+        }
       } else {
+        float q[8], h[8], a[8], b[8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
+        for (int i = 0; i < 8; ++i) {
+          q[i] = h[i] = a[i] = b[i] = 0.0f;
           if (i < left) {
-            (i < 4 ? mc.x : mc.y) |= (uint32_t)mp[i] << (8 * (i & 3));
-            (i < 4 ? vc.x : vc.y) |= (uint32_t)vp[i] << (8 * (i & 3));
+            q[i] = t.param[e0 + i];
+            h[i] = GBF16 ? __bfloat162float(static_cast<const __nv_bfloat16*>(t.grad)[e0 + i])
+                         : static_cast<const float*>(t.grad)[e0 + i];
+            if (BITS8) {
+              (i < 4 ? mc.x : mc.y) |= (uint32_t)static_cast<const uint8_t*>(t.m)[e0 + i] << (8 * (i & 3));
+              (i < 4 ? vc.x : vc.y) |= (uint32_t)static_cast<const uint8_t*>(t.v)[e0 + i] << (8 * (i & 3));
+            } else {
+              a[i] = static_cast<const float*>(t.m)[e0 + i], b[i] = static_cast<const float*>(t.v)[e0 + i];
+            }
           }
+        }
+        if (BITS8 && left > 0) mb = t.m_scale[e0 / kFp8Block], vb = t.v_scale[e0 / kFp8Block];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          p[i] = make_float2(q[2 * i], q[2 * i + 1]), g[i] = make_float2(h[2 * i], h[2 * i + 1]);
+          m[i] = make_float2(a[2 * i], a[2 * i + 1]), v[i] = make_float2(b[2 * i], b[2 * i + 1]);
+        }
       }
-      if (left > 0) {
-        mb = t.m_scale[e0 / kFp8Block];
-        vb = t.v_scale[e0 / kFp8Block];
-      }
-      const float ms = fp8_scale_value(mb), vs = fp8_scale_value(vb);
+
+      // ---- the step
+      auto both = [](float a) { return make_float2(a, a); };
+      const float2 ms = both(fp8_scale_value(mb)), vs = both(fp8_scale_value(vb));
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const float2 a = e4m3x2_to_f32((i < 2 ? mc.x : mc.y) >> (16 * (i & 1)));
-        const float2 b = e5m2x2_to_f32((i < 2 ? vc.x : vc.y) >> (16 * (i & 1)));
-        m[2 * i] = __fmul_rn(a.x, ms), m[2 * i + 1] = __fmul_rn(a.y, ms);
-        v[2 * i] = __fmul_rn(b.x, vs), v[2 * i + 1] = __fmul_rn(b.y, vs);
-      }
-    } else if (whole) {
-      load8(m, static_cast<const float*>(t.m) + e0);
-      load8(v, static_cast<const float*>(t.v) + e0);
-    } else {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const bool in = i < left;
-        m[i] = in ? static_cast<const float*>(t.m)[e0 + i] : 0.0f;
-        v[i] = in ? static_cast<const float*>(t.v)[e0 + i] : 0.0f;
-      }
-    }
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      if (k.grad_scale) g[i] = __fmul_rn(g[i], gs);
-      m[i] = __fadd_rn(__fmul_rn(k.b1, m[i]), __fmul_rn(k.c1, g[i]));
-      v[i] = __fadd_rn(__fmul_rn(k.b2, v[i]), __fmul_rn(k.c2, __fmul_rn(g[i], g[i])));
-      const float d = __fadd_rn(__fmul_rn(__fsqrt_rn(v[i]), k.root), k.eps);
-      p[i] = __fsub_rn(__fmul_rn(p[i], t.keep), __fmul_rn(k.size, __fdiv_rn(m[i], d)));
-    }
-    if (whole) {
-      store8(t.param + e0, p);
-      if (t.model)
-        *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(t.model) + e0) = make_uint4(
-            pack_bf16(p[0], p[1]), pack_bf16(p[2], p[3]), pack_bf16(p[4], p[5]), pack_bf16(p[6], p[7]));
-    } else {
-#pragma unroll
-      for (int i = 0; i < 8; ++i)
-        if (i < left) {
-          t.param[e0 + i] = p[i];
-          if (t.model) static_cast<__nv_bfloat16*>(t.model)[e0 + i] = __float2bfloat16_rn(p[i]);
+        if (BITS8) {
+          m[i] = mul2(e4m3x2_to_f32((i < 2 ? mc.x : mc.y) >> (16 * (i & 1))), ms);
+          v[i] = mul2(e5m2x2_to_f32((i < 2 ? vc.x : vc.y) >> (16 * (i & 1))), vs);
         }
-    }
-    if (BITS8) {
-      uint4 rm = make_uint4(0, 0, 0, 0), rv = rm;
-      if (SR) {
-        const uint64_t j = static_cast<uint64_t>(e0) >> 3;
-        const uint32_t st = 2u * (k.first_tensor + lo);
-        rm = philox4x32_10(make_uint4((uint32_t)j, (uint32_t)(j >> 32), st, k.step), k.keys);
-        rv = philox4x32_10(make_uint4((uint32_t)j, (uint32_t)(j >> 32), st + 1u, k.step), k.keys);
+        if (k.grad_scale) g[i] = mul2(g[i], both(gs));
+        m[i] = add_each(mul_each(m[i], k.b1), mul_each(g[i], k.c1));
+        v[i] = add_each(mul_each(v[i], k.b2), mul_each(mul2(g[i], g[i]), k.c2));
+        const float2 d = add_each(mul_each(make_float2(__fsqrt_rn(v[i].x), __fsqrt_rn(v[i].y)), k.root), both(k.eps));
+        const float2 q = make_float2(__fdiv_rn(m[i].x, d.x), __fdiv_rn(m[i].y, d.y));
+        p[i] = add_each(mul_each(p[i], t.keep), mul_each(q, -k.size));
       }
-      if (left < 8) {  // a block's elements beyond the tensor count as zeros
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-          if (i >= left) m[i] = 0.0f, v[i] = 0.0f;
-      }
-      const uint2 mc = encode8<kTopE4M3, 20, 0x7Fu, false, SR>(m, rm, mb);
-      const uint2 vc = encode8<kTopE5M2, 21, 0x7Fu, true, SR>(v, rv, vb);
-      uint8_t* mp = static_cast<uint8_t*>(t.m) + e0;
-      uint8_t* vp = static_cast<uint8_t*>(t.v) + e0;
+
+      // ---- out
       if (whole) {
-        *reinterpret_cast<uint2*>(mp) = mc;
-        *reinterpret_cast<uint2*>(vp) = vc;
+        store8(t.param + e0, p);
+        if (t.model)
+          *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(t.model) + e0) =
+              make_uint4(pack_bf16(p[0]), pack_bf16(p[1]), pack_bf16(p[2]), pack_bf16(p[3]));
+        if (!BITS8) {
+          store8(static_cast<float*>(t.m) + e0, m);
+          store8(static_cast<float*>(t.v) + e0, v);
+        }
       } else {
 #pragma unroll
         for (int i = 0; i < 8; ++i)
           if (i < left) {
-            mp[i] = static_cast<uint8_t>((i < 4 ? mc.x : mc.y) >> (8 * (i & 3)));
-            vp[i] = static_cast<uint8_t>((i < 4 ? vc.x : vc.y) >> (8 * (i & 3)));
+            const float x = (i & 1) ? p[i >> 1].y : p[i >> 1].x;
+            t.param[e0 + i] = x;
+            if (t.model) static_cast<__nv_bfloat16*>(t.model)[e0 + i] = __float2bfloat16_rn(x);
+            if (!BITS8) {
+              static_cast<float*>(t.m)[e0 + i] = (i & 1) ? m[i >> 1].y : m[i >> 1].x;
+              static_cast<float*>(t.v)[e0 + i] = (i & 1) ? v[i >> 1].y : v[i >> 1].x;
+            }
           }
       }
-      if ((threadIdx.x & 15) == 0 && left > 0) {
-        t.m_scale[e0 / kFp8Block] = static_cast<uint8_t>(mb);
-        t.v_scale[e0 / kFp8Block] = static_cast<uint8_t>(vb);
-      }
-    } else if (whole) {
-      store8(static_cast<float*>(t.m) + e0, m);
-      store8(static_cast<float*>(t.v) + e0, v);
-    } else {
+      if (BITS8) {
+        RandomPair r{};
+        if (SR) r = random_pair(e0 >> 3, 2u * (k.first_tensor + lo), k.step, base, k.keys);
+        uint32_t mn = fp8_scale_byte(amax16(m), kTopE4M3), vn = fp8_scale_byte(amax16(v), kTopE5M2);
+        uint2 mo, vo;
+        // (NaN and Inf have exponent 255 and so a byte far above the limit)
+        if (__all_sync(0xFFFFFFFFu, mn <= Fast<20>::kByte && vn <= Fast<21>::kByte)) {
+          mo = encode8_fast<20, false, SR>(m, r.m, mn);
+          vo = encode8_fast<21, true, SR>(v, r.v, vn);
+        } else {
+          float m8[8], v8[8];
 #pragma unroll
-      for (int i = 0; i < 8; ++i)
-        if (i < left) {
-          static_cast<float*>(t.m)[e0 + i] = m[i];
-          static_cast<float*>(t.v)[e0 + i] = v[i];
+          for (int i = 0; i < 4; ++i)
+            m8[2 * i] = m[i].x, m8[2 * i + 1] = m[i].y, v8[2 * i] = v[i].x, v8[2 * i + 1] = v[i].y;
+          mo = encode8<kTopE4M3, 20, 0x7Fu, false, SR>(m8, make_uint4(r.m[0], r.m[1], r.m[2], r.m[3]), mn);
+          vo = encode8<kTopE5M2, 21, 0x7Fu, true, SR>(v8, make_uint4(r.v[0], r.v[1], r.v[2], r.v[3]), vn);
         }
+        uint8_t* mp = static_cast<uint8_t*>(t.m) + e0;
+        uint8_t* vp = static_cast<uint8_t*>(t.v) + e0;
+        if (whole) {
+          *reinterpret_cast<uint2*>(mp) = mo;
+          *reinterpret_cast<uint2*>(vp) = vo;
+        } else {
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            if (i < left) {
+              mp[i] = static_cast<uint8_t>((i < 4 ? mo.x : mo.y) >> (8 * (i & 3)));
+              vp[i] = static_cast<uint8_t>((i < 4 ? vo.x : vo.y) >> (8 * (i & 3)));
+            }
+        }
+        if ((threadIdx.x & 15) == 0 && left > 0) {
+          t.m_scale[e0 / kFp8Block] = static_cast<uint8_t>(mn);
+          t.v_scale[e0 / kFp8Block] = static_cast<uint8_t>(vn);
+        }
+      }
     }
   }
+  if (!ok) drain_pause();  // a wait expired: let copies still in flight land first
 }
 
 template <bool GBF16, bool BITS8, bool SR, int CAP>
@@ -248,9 +440,13 @@ static cudaError_t launch_table(const AdamWEntry* t, int n, Scalars k, int num_s
   tab.first_chunk[n] = chunks;
   k.count = static_cast<uint32_t>(n);
   k.chunks = chunks;
-  const uint32_t most = static_cast<uint32_t>(num_sms) * 32u;
+  constexpr int kSmem = stages_of(BITS8) * sizeof(Stage<GBF16, BITS8>);
+  static const cudaError_t attr_err = cudaFuncSetAttribute(adamw_kernel<GBF16, BITS8, SR, CAP>,
+                                                           cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+  if (attr_err != cudaSuccess) return attr_err;
+  const uint32_t most = static_cast<uint32_t>(num_sms * kPerSm);
   const uint32_t grid = chunks < most ? chunks : most;
-  adamw_kernel<GBF16, BITS8, SR, CAP><<<grid, kThreads, 0, s>>>(tab, k);
+  adamw_kernel<GBF16, BITS8, SR, CAP><<<grid, kThreads + 32, kSmem, s>>>(tab, k);
   const cudaError_t e = cudaGetLastError();
   count_launch();
   return e;
@@ -282,6 +478,15 @@ cudaError_t launch_adamw(const AdamWEntry* t, int n, int first_tensor, bool grad
                      : aw::launch_some<false, true, true>(t, n, k, num_sms, s);
   return grad_bf16 ? aw::launch_some<true, true, false>(t, n, k, num_sms, s)
                    : aw::launch_some<false, true, false>(t, n, k, num_sms, s);
+}
+
+cudaError_t adamw_status_read_clear(unsigned int* out, cudaStream_t s) {
+  cudaError_t e = cudaStreamSynchronize(s);
+  if (e != cudaSuccess) return e;
+  e = cudaMemcpyFromSymbol(out, g_status, sizeof(unsigned int));
+  if (e != cudaSuccess) return e;
+  const unsigned int zero = 0;
+  return cudaMemcpyToSymbol(g_status, &zero, sizeof(unsigned int));
 }
 
 }  // namespace nvfp4

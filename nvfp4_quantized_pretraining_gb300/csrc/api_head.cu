@@ -145,8 +145,7 @@ fp4_status fp4_adamw_step(const fp4_adamw_tensor* tensors, int n, int grad_dtype
     int64_t work = 0;
     for (int i = 0; i < count; ++i) {
       const fp4_adamw_tensor& t = tensors[first + i];
-      const uintptr_t sa = state_bits == 32 ? 16 : 8;
-      const bool vec = aligned16(t.param) && aligned16(t.grad) && aligned_to(t.m, sa) && aligned_to(t.v, sa) &&
+      const bool vec = aligned16(t.param) && aligned16(t.grad) && aligned16(t.m) && aligned16(t.v) &&
                        aligned16(t.model);
       e[i] = AdamWEntry{t.param, t.grad, t.m, t.v, t.m_scale, t.v_scale, t.model, t.numel,
                         static_cast<float>(1.0 - lr * t.weight_decay), vec ? 1u : 0u};

@@ -193,6 +193,7 @@ struct AdamWScalars {
 int adamw_capacity();
 cudaError_t launch_adamw(const AdamWEntry* t, int n, int first_tensor, bool grad_bf16, int bits, bool sr,
                          const AdamWScalars& a, int num_sms, cudaStream_t s);
+cudaError_t adamw_status_read_clear(unsigned int* out, cudaStream_t s);
 
 // Log probabilities of tokens (and their gradient); see the C header for the arguments.
 struct LogprobArgs {
