@@ -43,10 +43,9 @@ struct Table {
   uint32_t first_chunk[CAP + 1];
 };
 
-// Pairs of FP32 operations, each rounded by itself.  Products that feed no sum are packed; a packed product and
-// sum were contracted into one rounding (seen as a last bit of the parameters), so sums take scalar products.
+// Pairs of FP32 operations, each rounded by itself: packed products, scalar sums (a packed product and a packed sum
+// were contracted into one rounding, seen as a last bit of the parameters).
 __device__ __forceinline__ float2 mul2(float2 a, float2 b) { return __fmul2_rn(a, b); }
-__device__ __forceinline__ float2 mul_each(float2 a, float b) { return make_float2(__fmul_rn(a.x, b), __fmul_rn(a.y, b)); }
 __device__ __forceinline__ float2 add_each(float2 a, float2 b) {
   return make_float2(__fadd_rn(a.x, b.x), __fadd_rn(a.y, b.y));
 }
@@ -158,9 +157,8 @@ __device__ __forceinline__ float max_nan_abs(float a, float b) {
 __device__ __forceinline__ uint32_t amax16(const float2 (&a)[4]) {
   float m = max_nan_abs(max_nan_abs(max_nan_abs(a[0].x, a[0].y), max_nan_abs(a[1].x, a[1].y)),
                         max_nan_abs(max_nan_abs(a[2].x, a[2].y), max_nan_abs(a[3].x, a[3].y)));
-#pragma unroll
-  for (int o = 1; o < 16; o <<= 1) m = max_nan_abs(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
-  return __float_as_uint(m);
+  // (patterns of magnitudes order as they do, NaN above all)
+  return __reduce_max_sync(0xFFFFu << (threadIdx.x & 16), __float_as_uint(m));
 }
 
 // The random words of m and v for the group of eight elements j of a tensor with stream ids st, st + 1.  For j < 2^32
@@ -358,11 +356,11 @@ __global__ void __launch_bounds__(kThreads + 32, kPerSm)
           v[i] = mul2(e5m2x2_to_f32((i < 2 ? vc.x : vc.y) >> (16 * (i & 1))), vs);
         }
         if (k.grad_scale) g[i] = mul2(g[i], both(gs));
-        m[i] = add_each(mul_each(m[i], k.b1), mul_each(g[i], k.c1));
-        v[i] = add_each(mul_each(v[i], k.b2), mul_each(mul2(g[i], g[i]), k.c2));
-        const float2 d = add_each(mul_each(make_float2(__fsqrt_rn(v[i].x), __fsqrt_rn(v[i].y)), k.root), both(k.eps));
+        m[i] = add_each(mul2(m[i], both(k.b1)), mul2(g[i], both(k.c1)));
+        v[i] = add_each(mul2(v[i], both(k.b2)), mul2(mul2(g[i], g[i]), both(k.c2)));
+        const float2 d = add_each(mul2(make_float2(__fsqrt_rn(v[i].x), __fsqrt_rn(v[i].y)), both(k.root)), both(k.eps));
         const float2 q = make_float2(__fdiv_rn(m[i].x, d.x), __fdiv_rn(m[i].y, d.y));
-        p[i] = add_each(mul_each(p[i], t.keep), mul_each(q, -k.size));
+        p[i] = add_each(mul2(p[i], both(t.keep)), mul2(q, both(-k.size)));
       }
 
       // ---- out

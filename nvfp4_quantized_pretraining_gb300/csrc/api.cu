@@ -521,7 +521,7 @@ fp4_status fp4_linear_bwd(const void* dY, int64_t M, int64_t N, int64_t lddy, co
 fp4_status fp4_check_status(void* stream) {
   unsigned int v = 0;
   CUDA_TRY(gemm_status_read_clear(&v, static_cast<cudaStream_t>(stream)));
-  for (auto unit : {fp8_status_read_clear, logprob_status_read_clear, adamw_status_read_clear}) {
+  for (auto unit : {fp8_status_read_clear, fp8_quantize_status_read_clear, logprob_status_read_clear, adamw_status_read_clear}) {
     unsigned int u = 0;
     CUDA_TRY(unit(&u, static_cast<cudaStream_t>(stream)));
     v |= u;

@@ -62,7 +62,7 @@ static fp4_status quantize(const void* x, int64_t rows, int64_t cols, int64_t ld
   Fp8Out r{}, c{};
   if (row) r = out_of(row);
   if (col) c = out_of(col);
-  CUDA_TRY(launch_fp8_quantize(x, rows, cols, ld, square, row ? &r : nullptr, col ? &c : nullptr, s));
+  CUDA_TRY(launch_fp8_quantize(x, rows, cols, ld, square, row ? &r : nullptr, col ? &c : nullptr, sm_count(), s));
   return FP4_OK;
 }
 

@@ -2,10 +2,13 @@
 // transposed), or both from one read; or one scale per 128 x 128 block, shared by both forms (so that the
 // transposed weights are exactly the weights).
 //
-// A CTA takes a 128 x 128 tile.  Row form: 16 lanes hold a row's 128 elements, its amax is four shuffles of
-// packed BF16 magnitudes, each lane converts its 8.  Column form: the tile goes through shared memory, a thread
-// takes two adjacent columns and 32 rows (so shared reads are whole words without conflicts) and writes 2 x 32
-// consecutive codes.  Memory-bound: 2 bytes read, 1 written per form and element.
+// 128 x 128 tiles in shared memory.  Row form: 8 lanes hold a row's 128 elements (16 each), its amax is three shuffles
+// of packed BF16 magnitudes.  Column form: a thread takes two adjacent columns and 32 rows (whole words, no bank
+// conflicts) and writes 2 x 32 consecutive codes.
+//
+// Memory-bound (2 bytes read, 1 written per form and element), and close to bound by issue slots (both forms at
+// 6.8 TB/s leave 21 instructions per element): inputs whose rows start on 16 bytes come by TMA into a ring of tiles that
+// CTAs walk persistently, others by loads, a tile per CTA; both convert a tile with the same code.
 #include <cuda_bf16.h>
 
 #include "common.cuh"
@@ -27,121 +30,137 @@ __device__ __forceinline__ uint32_t finite_only(uint32_t w) {
   if ((w >> 16) >= 0x7F80u) w &= 0x0000FFFFu;
   return w;
 }
-// Two BF16 values to two codes (low element in the low byte): exact product, round to nearest even.  The largest
-// finite magnitude of the block lands at most on 448; what is not finite becomes NaN (0x7F).
-__device__ __forceinline__ uint32_t codes2(uint32_t w, float inv) {
-  uint16_t r;
-  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;"
-      : "=h"(r)
-      : "f"(__fmul_rn(bf16_hi(w), inv)), "f"(__fmul_rn(bf16_lo(w), inv)));
-  uint32_t c = r;
-  if ((w & 0x7FFFu) >= 0x7F80u) c |= 0x007Fu;
-  if ((w >> 16 & 0x7FFFu) >= 0x7F80u) c |= 0x7F00u;
-  return c;
+// Four finite values to four codes: exact products, round to nearest even.  The block's largest magnitude lands at
+// most on 448.
+__device__ __forceinline__ uint32_t codes4(float2 a, float2 b, float inv) {
+  const float2 x = __fmul2_rn(a, make_float2(inv, inv)), y = __fmul2_rn(b, make_float2(inv, inv));
+  uint32_t r;
+  asm("{\n .reg .b16 lo, hi;\n cvt.rn.satfinite.e4m3x2.f32 lo, %2, %1;\n cvt.rn.satfinite.e4m3x2.f32 hi, %4, %3;\n"
+      " mov.b32 %0, {lo, hi};\n}\n"
+      : "=r"(r)
+      : "f"(x.x), "f"(x.y), "f"(y.x), "f"(y.y));
+  return r;
+}
+__device__ __forceinline__ float2 both(uint32_t w) { return make_float2(bf16_lo(w), bf16_hi(w)); }
+// For blocks with Inf or NaN: 0x7F where a BF16 half of w0, w1 (four values, low first) is not finite.
+__device__ __forceinline__ uint32_t nan_codes4(uint32_t w0, uint32_t w1) {
+  uint32_t r = 0;
+  if ((w0 & 0x7FFFu) >= 0x7F80u) r |= 0x0000007Fu;
+  if ((w0 >> 16 & 0x7FFFu) >= 0x7F80u) r |= 0x00007F00u;
+  if ((w1 & 0x7FFFu) >= 0x7F80u) r |= 0x007F0000u;
+  if ((w1 >> 16 & 0x7FFFu) >= 0x7F80u) r |= 0x7F000000u;
+  return r;
 }
 
 __device__ __forceinline__ uint32_t larger_half(uint32_t m) { return max(m & 0xFFFFu, m >> 16); }
 
-template <bool ROW, bool COL, bool SQUARE>
-__global__ void __launch_bounds__(kThreads) quantize_kernel(const __nv_bfloat16* x, uint32_t rows, uint32_t cols,
-                                                            int64_t ld, bool wide, Fp8Out r, Fp8Out c) {
-  __shared__ uint4 s_tile[COL ? 128 * 16 : 1];  // [128 rows][16 x 8 elements]
-  __shared__ uint32_t s_max[COL && !SQUARE ? 4 * 64 : 8];
-  pdl_trigger();
-  pdl_wait();
-  const uint32_t kb = blockIdx.x, rb = blockIdx.y;
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const uint32_t col0 = kb * 128 + (lane & 15) * 8;
+struct Tensor {
+  uint32_t rows, cols, tiles_k, tiles_r;
+};
+__device__ __forceinline__ uint32_t largest(const uint4& v) {
+  return max_u16x2(max_u16x2(v.x & kAbs, v.y & kAbs), max_u16x2(v.z & kAbs, v.w & kAbs));
+}
+__device__ __forceinline__ uint32_t largest_finite(const uint4& v) {
+  return max_u16x2(max_u16x2(finite_only(v.x), finite_only(v.y)), max_u16x2(finite_only(v.z), finite_only(v.w)));
+}
+// The 256 converting threads' barrier.
+__device__ __forceinline__ void sync256() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
 
-  // the tile: pass i has rows 16 i + 2 warp + lane / 16; elements outside the tensor are zeros
-  uint4 q[8];
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const uint32_t row = rb * 128 + i * 16 + warp * 2 + (lane >> 4);
-    q[i] = make_uint4(0, 0, 0, 0);
-    if (row < rows) {
-      const __nv_bfloat16* p = x + row * ld + col0;
-      if (wide && col0 + 8 <= cols) {
-        q[i] = *reinterpret_cast<const uint4*>(p);
-      } else {
-        uint32_t w[4] = {0, 0, 0, 0};
-#pragma unroll
-        for (int j = 0; j < 8; ++j)
-          if (col0 + j < cols) w[j >> 1] |= (uint32_t)reinterpret_cast<const uint16_t*>(p)[j] << (16 * (j & 1));
-        q[i] = make_uint4(w[0], w[1], w[2], w[3]);
-      }
-    }
-    if (COL) s_tile[(i * 16 + warp * 2 + (lane >> 4)) * 16 + (lane & 15)] = q[i];
-  }
-  auto largest = [](const uint4& v) {
-    return max_u16x2(max_u16x2(v.x & kAbs, v.y & kAbs), max_u16x2(v.z & kAbs, v.w & kAbs));
-  };
-  auto largest_finite = [](const uint4& v) {
-    return max_u16x2(max_u16x2(finite_only(v.x), finite_only(v.y)), max_u16x2(finite_only(v.z), finite_only(v.w)));
-  };
-  uint32_t square = 0;  // SQUARE: the tile's scale byte
-  if (SQUARE) {
-    uint32_t m = 0;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) m = max_u16x2(m, largest_finite(q[i]));
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) m = max_u16x2(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
-    if (lane == 0) s_max[warp] = m;
-    __syncthreads();
-#pragma unroll
-    for (int i = 0; i < 8; ++i) m = max_u16x2(m, s_max[i]);
-    square = fp8_scale_byte(larger_half(m) << 16, kTopE4M3);
-  }
+// Tile (rb, kb) from shared memory ([128 rows][16 x 8 elements], zeros outside the tensor) to the outputs.  s_max: 256
+// words, another set for the tile after; `read` is called when the tile has been read.
+template <bool ROW, bool COL, bool SQUARE, typename Read>
+__device__ __forceinline__ void convert_tile(const uint4* tile, uint32_t* s_max, uint32_t rb, uint32_t kb,
+                                             const Tensor& t, const Fp8Out& r, const Fp8Out& c, Read read) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const uint32_t part = lane & 7;
   const uint32_t row_atoms = (r.cols + 511) / 512, col_atoms = (c.cols + 511) / 512;
+  // pass i: row 32 i + 4 warp + lane / 8, elements 8 part.. and 64 + 8 part..
+  uint4 q[4][2];
+  if (ROW || SQUARE) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint4* p = tile + (i * 32 + warp * 4 + (lane >> 3)) * 16 + part;
+      q[i][0] = p[0], q[i][1] = p[8];
+    }
+  }
+  uint32_t square = 0;  // SQUARE: the tile's scale byte
+  bool square_odd = false;
+  if (SQUARE) {
+    auto tile_max = [&](uint32_t* to, auto of) {
+      uint32_t m = 0;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) m = max_u16x2(m, max_u16x2(of(q[i][0]), of(q[i][1])));
+      m = __reduce_max_sync(0xFFFFFFFFu, larger_half(m));
+      if (lane == 0) to[warp] = m;
+      sync256();
+#pragma unroll
+      for (int i = 0; i < 8; ++i) m = max(m, to[i]);
+      return m;
+    };
+    uint32_t m = tile_max(s_max, [](const uint4& v) { return largest(v); });
+    square_odd = m >= 0x7F80u;
+    if (square_odd) m = tile_max(s_max + 8, [](const uint4& v) { return largest_finite(v); });
+    square = fp8_scale_byte(m << 16, kTopE4M3);
+  }
   if (ROW) {
-    uint8_t* codes = static_cast<uint8_t*>(r.codes);
+    uint8_t* codes = static_cast<uint8_t*>(r.codes) + (size_t)rb * 128 * r.pitch + kb * 128 + part * 8;
     uint8_t* scales = static_cast<uint8_t*>(r.scales);
-    const bool last = kb == gridDim.x - 1;
+    const bool last = kb == t.tiles_k - 1;
+    if (!COL) read();
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const uint32_t row = rb * 128 + i * 16 + warp * 2 + (lane >> 4);
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t in = i * 32 + warp * 4 + (lane >> 3), row = rb * 128 + in;
       uint32_t byte = square;
+      bool odd = square_odd;
       if (!SQUARE) {
-        uint32_t m = largest(q[i]);
+        uint32_t m = max_u16x2(largest(q[i][0]), largest(q[i][1]));
 #pragma unroll
-        for (int o = 1; o < 16; o <<= 1) m = max_u16x2(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
-        if (__any_sync(0xFFFFFFFFu, larger_half(m) >= 0x7F80u)) {
-          m = largest_finite(q[i]);
+        for (int o = 1; o < 8; o <<= 1) m = max_u16x2(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
+        uint32_t h = larger_half(m);
+        odd = __any_sync(0xFFFFFFFFu, h >= 0x7F80u);
+        if (odd) {
+          m = max_u16x2(largest_finite(q[i][0]), largest_finite(q[i][1]));
 #pragma unroll
-          for (int o = 1; o < 16; o <<= 1) m = max_u16x2(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
+          for (int o = 1; o < 8; o <<= 1) m = max_u16x2(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
+          h = larger_half(m);
         }
-        byte = fp8_scale_byte(larger_half(m) << 16, kTopE4M3);
+        byte = fp8_scale_byte(h << 16, kTopE4M3);
       }
       const float inv = fp8_scale_inverse(byte);
-      if (row < rows) {
-        const uint2 o = make_uint2(codes2(q[i].x, inv) | codes2(q[i].y, inv) << 16,
-                                   codes2(q[i].z, inv) | codes2(q[i].w, inv) << 16);
-        *reinterpret_cast<uint2*>(codes + (size_t)row * r.pitch + col0) = o;
+      if (row < t.rows) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const uint4& v = q[i][h];
+          uint2 o = make_uint2(codes4(both(v.x), both(v.y), inv), codes4(both(v.z), both(v.w), inv));
+          if (odd) o.x |= nan_codes4(v.x, v.y), o.y |= nan_codes4(v.z, v.w);
+          *reinterpret_cast<uint2*>(codes + (size_t)in * r.pitch + h * 64) = o;
+        }
       }
       // the scale, and zeros after the last block of the row's atom; rows past the tensor have scale 0
-      if ((lane & 15) == 0) scales[sf_offset(row, kb, row_atoms)] = static_cast<uint8_t>(row < rows ? byte : 0);
-      else if (last && (lane & 15) < 4 && (kb & 3) + (lane & 15) < 4)
-        scales[sf_offset(row, kb + (lane & 15), row_atoms)] = 0;
+      if (part == 0) scales[sf_offset(row, kb, row_atoms)] = static_cast<uint8_t>(row < t.rows ? byte : 0);
+      else if (last && part < 4 && (kb & 3) + part < 4) scales[sf_offset(row, kb + part, row_atoms)] = 0;
     }
   }
   if (COL) {
-    if (!SQUARE) __syncthreads();  // (SQUARE: the tile was complete before its amax)
-    const uint32_t* words = reinterpret_cast<const uint32_t*>(s_tile);  // [128][64] column pairs
+    const uint32_t* words = reinterpret_cast<const uint32_t*>(tile);  // [128][64] column pairs
     const uint32_t pair = tid & 63, group = tid >> 6;
     uint32_t w[32], b0 = square, b1 = square;
 #pragma unroll
     for (int i = 0; i < 32; ++i) w[i] = words[(group * 32 + i) * 64 + pair];
+    read();
+    bool odd = square_odd;
     if (!SQUARE) {
       uint32_t m = 0;
 #pragma unroll
       for (int i = 0; i < 32; ++i) m = max_u16x2(m, w[i] & kAbs);
-      if ((m & 0xFFFFu) >= 0x7F80u || (m >> 16) >= 0x7F80u) {
+      odd = larger_half(m) >= 0x7F80u;
+      if (odd) {
         m = 0;
 #pragma unroll
         for (int i = 0; i < 32; ++i) m = max_u16x2(m, finite_only(w[i]));
       }
       s_max[group * 64 + pair] = m;
-      __syncthreads();
+      sync256();
       m = max_u16x2(max_u16x2(s_max[pair], s_max[64 + pair]), max_u16x2(s_max[128 + pair], s_max[192 + pair]));
       b0 = fp8_scale_byte(m << 16, kTopE4M3);
       b1 = fp8_scale_byte(m & 0xFFFF0000u, kTopE4M3);
@@ -149,58 +168,160 @@ __global__ void __launch_bounds__(kThreads) quantize_kernel(const __nv_bfloat16*
     const float i0 = fp8_scale_inverse(b0), i1 = fp8_scale_inverse(b1);
     uint32_t o0[8], o1[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) o0[i] = o1[i] = 0;
-#pragma unroll
-    for (int i = 0; i < 32; i += 2) {
-      // rows i, i + 1 of each column as one packed pair
-      const uint32_t a = __byte_perm(w[i], w[i + 1], 0x5410), b = __byte_perm(w[i], w[i + 1], 0x7632);
-      o0[i >> 2] |= codes2(a, i0) << (8 * (i & 2));
-      o1[i >> 2] |= codes2(b, i1) << (8 * (i & 2));
+    for (int i = 0; i < 8; ++i) {
+      const uint32_t* v = w + 4 * i;  // four rows of the two columns
+      o0[i] = codes4(make_float2(bf16_lo(v[0]), bf16_lo(v[1])), make_float2(bf16_lo(v[2]), bf16_lo(v[3])), i0);
+      o1[i] = codes4(make_float2(bf16_hi(v[0]), bf16_hi(v[1])), make_float2(bf16_hi(v[2]), bf16_hi(v[3])), i1);
+      if (odd) {
+        o0[i] |= nan_codes4(__byte_perm(v[0], v[1], 0x5410), __byte_perm(v[2], v[3], 0x5410));
+        o1[i] |= nan_codes4(__byte_perm(v[0], v[1], 0x7632), __byte_perm(v[2], v[3], 0x7632));
+      }
     }
-    uint8_t* codes = static_cast<uint8_t*>(c.codes);
     uint8_t* scales = static_cast<uint8_t*>(c.scales);
     const uint32_t col = kb * 128 + pair * 2;
-    uint8_t* p = codes + (size_t)col * c.pitch + rb * 128 + group * 32;
-    if (col < cols) {
+    uint8_t* p = static_cast<uint8_t*>(c.codes) + (size_t)col * c.pitch + rb * 128 + group * 32;
+    if (col < t.cols) {
       reinterpret_cast<uint4*>(p)[0] = make_uint4(o0[0], o0[1], o0[2], o0[3]);
       reinterpret_cast<uint4*>(p)[1] = make_uint4(o0[4], o0[5], o0[6], o0[7]);
     }
-    if (col + 1 < cols) {
+    if (col + 1 < t.cols) {
       p += c.pitch;
       reinterpret_cast<uint4*>(p)[0] = make_uint4(o1[0], o1[1], o1[2], o1[3]);
       reinterpret_cast<uint4*>(p)[1] = make_uint4(o1[4], o1[5], o1[6], o1[7]);
     }
-    const bool last = rb == gridDim.y - 1;
     if (group == 0) {
-      scales[sf_offset(col, rb, col_atoms)] = static_cast<uint8_t>(col < cols ? b0 : 0);
-      scales[sf_offset(col + 1, rb, col_atoms)] = static_cast<uint8_t>(col + 1 < cols ? b1 : 0);
-    } else if (last && (rb & 3) + group < 4) {
+      scales[sf_offset(col, rb, col_atoms)] = static_cast<uint8_t>(col < t.cols ? b0 : 0);
+      scales[sf_offset(col + 1, rb, col_atoms)] = static_cast<uint8_t>(col + 1 < t.cols ? b1 : 0);
+    } else if (rb == t.tiles_r - 1 && (rb & 3) + group < 4) {
       scales[sf_offset(col, rb + group, col_atoms)] = 0;
       scales[sf_offset(col + 1, rb + group, col_atoms)] = 0;
     }
   }
 }
 
+constexpr int kTileBytes = 128 * 256;
+constexpr int kStages = 3, kPerSm = 2;
+constexpr int kSmemBytes = kStages * kTileBytes + 128;
+
+template <bool ROW, bool COL, bool SQUARE>
+__global__ void __launch_bounds__(kThreads + 32, kPerSm)
+    quantize_ring_kernel(const __grid_constant__ CUtensorMap map, const Tensor t, const Fp8Out r, const Fp8Out c) {
+  extern __shared__ uint8_t s_raw[];
+  uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(s_raw) + 127) & ~uintptr_t(127));
+  __shared__ uint64_t s_full[kStages], s_free[kStages];
+  __shared__ uint32_t s_max[2][256];
+  pdl_trigger();
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < kStages; ++i) {
+      mbar_init(&s_full[i], 1);
+      mbar_init(&s_free[i], kThreads / 32);
+    }
+    fence_mbar_init();
+    prefetch_tmap(&map);
+  }
+  __syncthreads();
+  pdl_wait();
+  const uint32_t tiles = t.tiles_k * t.tiles_r;
+  bool ok = true;
+  uint32_t n = 0;
+  if (threadIdx.x >= kThreads) {
+    if (threadIdx.x == kThreads) {
+      for (uint32_t i = blockIdx.x; ok && i < tiles; i += gridDim.x, ++n) {
+        const uint32_t st = n % kStages;
+        ok = mbar_wait(&s_free[st], ((n / kStages) & 1) ^ 1);
+        if (!ok) break;
+        mbar_arrive_expect_tx(&s_full[st], kTileBytes);
+        tma_load_2d(ring + st * kTileBytes, &map, &s_full[st], (int32_t)(i % t.tiles_k * 128), (int32_t)(i / t.tiles_k * 128));
+      }
+    }
+  } else {
+    for (uint32_t i = blockIdx.x; i < tiles; i += gridDim.x, ++n) {
+      const uint32_t st = n % kStages;
+      if (ok) ok = mbar_wait(&s_full[st], (n / kStages) & 1);
+      convert_tile<ROW, COL, SQUARE>(reinterpret_cast<const uint4*>(ring + st * kTileBytes), s_max[n & 1], i / t.tiles_k,
+                                     i % t.tiles_k, t, r, c, [&] {
+                                       __syncwarp();
+                                       if ((threadIdx.x & 31) == 0) mbar_arrive(&s_free[st]);
+                                     });
+    }
+  }
+  if (!ok) drain_pause();  // a wait expired: let copies still in flight land first
+}
+
+// Rows of any alignment: a tile per CTA, through registers.
+template <bool ROW, bool COL, bool SQUARE>
+__global__ void __launch_bounds__(kThreads) quantize_kernel(const __nv_bfloat16* x, int64_t ld, const Tensor t,
+                                                            const Fp8Out r, const Fp8Out c) {
+  __shared__ uint4 s_tile[128 * 16];
+  __shared__ uint32_t s_max[256];
+  pdl_trigger();
+  pdl_wait();
+  const uint32_t kb = blockIdx.x, rb = blockIdx.y, col = kb * 128 + (threadIdx.x & 63) * 2;
+  uint32_t* words = reinterpret_cast<uint32_t*>(s_tile);
+#pragma unroll 8
+  for (uint32_t i = threadIdx.x >> 6; i < 128; i += 4) {
+    const uint32_t row = rb * 128 + i;
+    const uint16_t* p = reinterpret_cast<const uint16_t*>(x) + (int64_t)row * ld + col;
+    uint32_t w = 0;
+    if (row < t.rows && col < t.cols) w = p[0];
+    if (row < t.rows && col + 1 < t.cols) w |= (uint32_t)p[1] << 16;
+    words[i * 64 + (threadIdx.x & 63)] = w;
+  }
+  __syncthreads();
+  convert_tile<ROW, COL, SQUARE>(s_tile, s_max, rb, kb, t, r, c, [] {});
+}
+
 }  // namespace fq
 
-cudaError_t launch_fp8_quantize(const void* x, int64_t rows, int64_t cols, int64_t ld, bool square, const Fp8Out* row,
-                                const Fp8Out* col, cudaStream_t s) {
-  const dim3 grid(static_cast<uint32_t>((cols + 127) / 128), static_cast<uint32_t>((rows + 127) / 128));
-  const bool wide = (reinterpret_cast<uintptr_t>(x) & 15u) == 0 && (ld % 8 == 0 || rows == 1);
-  const Fp8Out none{};
-  const Fp8Out r = row ? *row : none, c = col ? *col : none;
-  const __nv_bfloat16* p = static_cast<const __nv_bfloat16*>(x);
-  const uint32_t R = static_cast<uint32_t>(rows), C = static_cast<uint32_t>(cols);
-  auto go = [&](auto kernel) { return launch_pdl(kernel, grid, dim3(fq::kThreads), 0, s, p, R, C, ld, wide, r, c); };
+template <bool ROW, bool COL, bool SQUARE>
+static cudaError_t launch_one(const void* x, int64_t rows, int64_t cols, int64_t ld, const Fp8Out& r, const Fp8Out& c,
+                              int num_sms, cudaStream_t s) {
+  using namespace fq;
+  const Tensor t{static_cast<uint32_t>(rows), static_cast<uint32_t>(cols), static_cast<uint32_t>((cols + 127) / 128),
+                 static_cast<uint32_t>((rows + 127) / 128)};
+  const bool wide = (reinterpret_cast<uintptr_t>(x) & 15u) == 0 && ld % 8 == 0;
   cudaError_t e;
-  if (square)
-    e = row && col ? go(fq::quantize_kernel<true, true, true>)
-                   : row ? go(fq::quantize_kernel<true, false, true>) : go(fq::quantize_kernel<false, true, true>);
-  else
-    e = row && col ? go(fq::quantize_kernel<true, true, false>)
-                   : row ? go(fq::quantize_kernel<true, false, false>) : go(fq::quantize_kernel<false, true, false>);
+  if (wide) {
+    auto kernel = quantize_ring_kernel<ROW, COL, SQUARE>;
+    static const cudaError_t attr_err =
+        cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
+    if (attr_err != cudaSuccess) return attr_err;
+    CUtensorMap map;
+    if (!encode_tmap_2d(&map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, x, cols, rows, ld * 2, 128, 128,
+                        CU_TENSOR_MAP_SWIZZLE_NONE))
+      return cudaErrorInvalidValue;
+    const int64_t tiles = (int64_t)t.tiles_k * t.tiles_r, most = (int64_t)num_sms * kPerSm;
+    e = launch_pdl(kernel, dim3(static_cast<uint32_t>(tiles < most ? tiles : most)), dim3(kThreads + 32), kSmemBytes, s,
+                   map, t, r, c);
+  } else {
+    e = launch_pdl(quantize_kernel<ROW, COL, SQUARE>, dim3(t.tiles_k, t.tiles_r), dim3(kThreads), 0, s,
+                   static_cast<const __nv_bfloat16*>(x), ld, t, r, c);
+  }
   count_launch();
   return e;
+}
+
+cudaError_t launch_fp8_quantize(const void* x, int64_t rows, int64_t cols, int64_t ld, bool square, const Fp8Out* row,
+                                const Fp8Out* col, int num_sms, cudaStream_t s) {
+  const Fp8Out none{};
+  const Fp8Out r = row ? *row : none, c = col ? *col : none;
+  if (rows == 1) ld = (cols + 7) / 8 * 8;  // (one row: the pitch is not used)
+  if (square)
+    return row && col ? launch_one<true, true, true>(x, rows, cols, ld, r, c, num_sms, s)
+           : row      ? launch_one<true, false, true>(x, rows, cols, ld, r, c, num_sms, s)
+                      : launch_one<false, true, true>(x, rows, cols, ld, r, c, num_sms, s);
+  return row && col ? launch_one<true, true, false>(x, rows, cols, ld, r, c, num_sms, s)
+         : row      ? launch_one<true, false, false>(x, rows, cols, ld, r, c, num_sms, s)
+                    : launch_one<false, true, false>(x, rows, cols, ld, r, c, num_sms, s);
+}
+
+cudaError_t fp8_quantize_status_read_clear(unsigned int* out, cudaStream_t s) {
+  cudaError_t e = cudaStreamSynchronize(s);
+  if (e != cudaSuccess) return e;
+  e = cudaMemcpyFromSymbol(out, g_status, sizeof(unsigned int));
+  if (e != cudaSuccess) return e;
+  const unsigned int zero = 0;
+  return cudaMemcpyToSymbol(g_status, &zero, sizeof(unsigned int));
 }
 
 }  // namespace nvfp4

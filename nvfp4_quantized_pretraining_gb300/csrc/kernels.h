@@ -234,7 +234,8 @@ struct Fp8Out {
 };
 // x rows x cols BF16; square: one scale per 128 x 128 block, else per 1 x 128 block of each form.
 cudaError_t launch_fp8_quantize(const void* x, int64_t rows, int64_t cols, int64_t ld, bool square, const Fp8Out* row,
-                                const Fp8Out* col, cudaStream_t s);
+                                const Fp8Out* col, int num_sms, cudaStream_t s);
+cudaError_t fp8_quantize_status_read_clear(unsigned int* out, cudaStream_t s);
 // C (M x N, pitch ldc) = A B^T, A M x K, B N x K.
 struct Fp8GemmArgs {
   const void *a_codes, *a_scales, *b_codes, *b_scales;
