@@ -17,7 +17,7 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libnvfp4_gb300.so")
 SOURCES = ["quantize.cu", "gemm.cu", "branch.cu", "lora_grad.cu", "lora_cholqr.cu", "realign.cu", "newton_schulz.cu", "qadamw.cu",
-           "fp8_quantize.cu", "fp8_gemm.cu", "adamw.cu", "token_logprobs.cu", "peak.cu", "api.cu", "api_head.cu", "api_fp8.cu"]
+           "fp8_quantize.cu", "fp8_gemm.cu", "fp8_few.cu", "adamw.cu", "token_logprobs.cu", "peak.cu", "api.cu", "api_head.cu", "api_fp8.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ARCH + ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-I", INCLUDE]
 

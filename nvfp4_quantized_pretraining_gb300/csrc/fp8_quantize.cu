@@ -200,7 +200,7 @@ __device__ __forceinline__ void convert_tile(const uint4* tile, uint32_t* s_max,
 }
 
 constexpr int kTileBytes = 128 * 256;
-constexpr int kStages = 3, kPerSm = 2;
+constexpr int kStages = 2, kPerSm = 3;
 constexpr int kSmemBytes = kStages * kTileBytes + 128;
 
 template <bool ROW, bool COL, bool SQUARE>

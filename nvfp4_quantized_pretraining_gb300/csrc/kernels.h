@@ -245,6 +245,10 @@ struct Fp8GemmArgs {
   int64_t ldc;
 };
 cudaError_t launch_fp8_gemm(const Fp8GemmArgs& g, int num_sms, cudaStream_t s);
+// Y (T x N BF16, pitch ldy) = X W^T for at most kFp8FewTokens tokens, X quantized on the way.
+constexpr int64_t kFp8FewTokens = 32;
+cudaError_t launch_fp8_few(const void* x, int64_t T, int64_t K, int64_t ldx, const void* w_codes, const void* w_scales,
+                           int64_t N, void* y, int64_t ldy, int num_sms, cudaStream_t s);
 cudaError_t fp8_status_read_clear(unsigned int* out, cudaStream_t s);
 
 }  // namespace nvfp4
