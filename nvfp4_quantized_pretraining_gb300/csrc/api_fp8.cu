@@ -118,7 +118,7 @@ fp4_status fp4_fp8_linear_fwd(const void* X, int64_t M, int64_t K, int64_t ldx, 
   if ((st = check_shape(Wq, N, K, "Wq")) || (st = check_matrix(Y, M, N, ldy, 2, "Y"))) return st;
   if (xqT_saved && ((st = check_fp8(xqT_saved, "xqT_saved")) || (st = check_shape(xqT_saved, K, M, "xqT_saved")))) return st;
   if ((st = check_ws(ws, ws_bytes, fp4_fp8_linear_fwd_workspace(M, N, K)))) return st;
-  if (M <= kFp8FewTokens) {  // (the column form, if wanted, by a launch of its own)
+  if (fp8_few(M, N, K)) {  // (the column form, if wanted, by a launch of its own)
     if (xqT_saved && (st = quantize(X, M, K, ldx, false, nullptr, xqT_saved, s))) return st;
     CUDA_TRY(launch_fp8_few(X, M, K, ldx, Wq->codes, Wq->scales, N, Y, ldy, sm_count(), s));
     return FP4_OK;

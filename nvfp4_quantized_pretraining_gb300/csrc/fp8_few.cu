@@ -1,4 +1,4 @@
-// Y = X W^T for a few tokens (at most 32), the FP8 linear layer of generation: every weight is read for a handful of
+// Y = X W^T for a few tokens (at most 16), the FP8 linear layer of generation: every weight is read for a handful of
 // rows, so the call is bound by the weights' bytes and, below some ten megabytes, by latency.  One launch: a CTA takes
 // 16 R rows of W, its 8 warps a share of K each; a warp quantizes the tokens' block of 128 itself, in registers, in the
 // layout of the MMA's operand (no second kernel, no shared-memory staging, no scales in memory), multiplies with
@@ -203,9 +203,7 @@ cudaError_t launch_fp8_few(const void* x, int64_t T, int64_t K, int64_t ldx, con
                     static_cast<const uint8_t*>(w_scales), static_cast<__nv_bfloat16*>(y), ldy, fp8_pitch(K),
                     static_cast<uint32_t>(T), static_cast<uint32_t>(N), static_cast<uint32_t>(K)};
   const bool wide = (reinterpret_cast<uintptr_t>(x) & 15u) == 0 && (ldx % 8 == 0 || T == 1);
-  return T <= 8    ? few::launch_rows<1>(a, wide, num_sms, s)
-         : T <= 16 ? few::launch_rows<2>(a, wide, num_sms, s)
-                   : few::launch_rows<4>(a, wide, num_sms, s);
+  return T <= 8 ? few::launch_rows<1>(a, wide, num_sms, s) : few::launch_rows<2>(a, wide, num_sms, s);
 }
 
 }  // namespace nvfp4

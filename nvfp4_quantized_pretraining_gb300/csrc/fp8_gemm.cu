@@ -6,10 +6,17 @@
 // them are one 512-byte atom, moved to tensor memory by tcgen05.cp right before the MMAs that read it.
 // Accumulation is FP32 over the whole K and C is rounded once.
 //
-// A cluster of two CTAs computes a 256 x 256 tile with two-SM MMAs: CTA r stages A rows [128 r, +128) and B rows
-// [128 r, +128), receives C rows [128 r, +128); per SM 32 KB of operands feed 8.4 MFLOP per stage.  Warps: TMA
-// producer, MMA issuer (pair leader), eight epilogue warps.  Operands past M, N or K are zeros (TMA fill, code
-// padding), stores are clipped.  Every wait is bounded (FP4_ERR_TIMEOUT in the status word).
+// A CTA pair computes a tile of 256 rows of P times BN rows of Q with two-SM MMAs: CTA r stages P rows [128 r, +128)
+// and Q rows [BN/2 r, +BN/2) and receives tile rows [128 r, +128); with BN = 256, 32 KB of operands per SM feed 8.4
+// MFLOP a stage.  P is A and Q is B, except for few rows of A (at most 128): then P is B, so that the many rows take
+// the wide side, and tiles are stored transposed.
+//
+// Few tiles: a cluster of 2 S CTAs takes a tile, each pair a share of K; the pairs exchange their FP32 partial tiles
+// through distributed shared memory, each adds its share of the columns in the order of K and stores it (one launch, no
+// workspace, the same result every time).
+//
+// Warps: TMA producer, MMA issuer (pair leader), eight epilogue warps.  Operands past M, N or K are zeros (TMA fill,
+// code padding), stores are clipped.  Every wait is bounded (FP4_ERR_TIMEOUT in the status word).
 #include <cudaTypedefs.h>
 #include <cuda_bf16.h>
 
@@ -20,27 +27,35 @@ namespace nvfp4 {
 namespace f8 {
 
 constexpr int BK = 128;
-constexpr int STAGES = 5;
-constexpr int A_BYTES = 128 * BK, B_BYTES = 128 * BK;  // this CTA's rows of each operand
+constexpr int A_BYTES = 128 * BK;                      // this CTA's rows of P
 constexpr int SF_ATOM = 512;                           // 128 rows x 4 scale bytes: 512 elements of K
-constexpr int SF_BYTES = 3 * SF_ATOM;                  // this CTA's A rows, all 256 B rows
-constexpr int STAGE_BYTES = A_BYTES + B_BYTES + 2048;  // (a stage starts on a 1024-byte boundary)
 constexpr int EPI_WARPS = 8, FIRST_EPI_WARP = 2;
 constexpr int CHUNK_BYTES = 32 * 64;                   // 32 rows x 32 BF16 columns, 64-byte swizzled rows
 constexpr int OUT_BYTES = EPI_WARPS * 2 * CHUNK_BYTES;
 constexpr int kSfGroup = 4;                            // stages per scale word
 constexpr uint32_t TM_ACC = 0, TM_SF = 256, TM_SF_SLOT = 16, TM_COLS = 512;
 constexpr int NUM_THREADS = (FIRST_EPI_WARP + EPI_WARPS) * 32;
-constexpr int SMEM_BYTES = STAGES * STAGE_BYTES + OUT_BYTES + 1024 + 256;
-static_assert(STAGE_BYTES % 1024 == 0 && SMEM_BYTES <= 232448, "shared memory");
+template <int BN>
+struct Cfg {
+  static constexpr int B_BYTES = BN / 2 * BK;          // this CTA's rows of Q
+  static constexpr int SFB_ATOMS = (BN + 127) / 128;   // all rows of Q
+  static constexpr int SF_BYTES = (1 + SFB_ATOMS) * SF_ATOM;
+  static constexpr int STAGE_BYTES = A_BYTES + B_BYTES + 2048;  // (a stage starts on a 1024-byte boundary)
+  static constexpr int STAGES = BN == 256 ? 5 : BN == 128 ? 7 : 8;
+  static constexpr int SMEM_BYTES = STAGES * STAGE_BYTES + OUT_BYTES + 1024 + 256;
+  static_assert(STAGE_BYTES % 1024 == 0 && SMEM_BYTES <= 232448, "shared memory");
+  static constexpr int MAX_SPLIT = BN == 256 ? 2 : 4;
+  static_assert(STAGES * STAGE_BYTES >= 2 * (MAX_SPLIT - 1) * (BN / MAX_SPLIT) * 512, "a split tile's parts, sent and received");
+};
 
 struct Params {
-  uint32_t M, N, num_k, tiles_m, tiles_n;
-  uint32_t n_fastest;  // tile order: the larger operand is walked slowest
+  uint32_t P, Q, num_k, tiles_p, tiles_q;  // rows of the two sides
+  uint32_t q_fastest;                      // tile order: the larger operand is walked slowest
+  uint32_t split;                          // S: pairs that share a tile
   void* C;
   int64_t ldc;
   int c_f32, tma_store;
-  uint32_t vec;        // C rows allow 16-byte stores
+  uint32_t vec;                            // C rows allow 16-byte stores
 };
 
 // kind::mxf8f6f4: E4M3 x E4M3, UE8M0 scales, K-major operands; the scale byte's id is added per stage.
@@ -62,10 +77,74 @@ __device__ __forceinline__ void tc_cp_sf_pair(uint32_t taddr, uint64_t sdesc) {
   asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(sdesc) : "memory");
 }
 
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
+// 8 consecutive 32-bit columns of this warp's 32 TMEM lanes, complete on return.
+__device__ __forceinline__ void tmem_ld_32x32b_x8(uint32_t taddr, uint32_t (&r)[8]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];\n"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+      : "r"(taddr)
+      : "memory");
+}
+// 32 columns (col.., accumulators of this lane's row) of the tile to C.  SWAP: tile rows are C's columns, and the 32
+// lanes of a column store 32 neighbours.
+template <bool SWAP>
+__device__ __forceinline__ void store_direct(const Params& p, const uint32_t (&acc)[32], uint32_t row, uint32_t col) {
+  if (SWAP) {
+    if (row >= p.P) return;
+#pragma unroll
+    for (int i = 0; i < 32; ++i) {
+      if (col + i < p.Q) {
+        const float v = __uint_as_float(acc[i]);
+        const size_t at = (size_t)(col + i) * p.ldc + row;
+        if (p.c_f32) static_cast<float*>(p.C)[at] = v;
+        else static_cast<__nv_bfloat16*>(p.C)[at] = __float2bfloat16_rn(v);
+      }
+    }
+    return;
+  }
+  if (row >= p.P || col >= p.Q) return;
+  if (p.c_f32) {
+    float* dst = static_cast<float*>(p.C) + (size_t)row * p.ldc + col;
+    if (p.vec && col + 32 <= p.Q) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        reinterpret_cast<uint4*>(dst)[i] = make_uint4(acc[4 * i], acc[4 * i + 1], acc[4 * i + 2], acc[4 * i + 3]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 32; ++i)
+        if (col + i < p.Q) dst[i] = __uint_as_float(acc[i]);
+    }
+  } else {
+    __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(p.C) + (size_t)row * p.ldc + col;
+#pragma unroll
+    for (int i = 0; i < 32; ++i)
+      if (col + i < p.Q) dst[i] = __float2bfloat16_rn(__uint_as_float(acc[i]));
+  }
+}
+// FP32 accumulators to packed BF16, and to a 32 x 32 chunk in shared memory: row = lane, 64 bytes; 16-byte unit u at
+// u ^ ((row >> 1) & 3) (64-byte swizzle).
+__device__ __forceinline__ void convert(const uint32_t (&a)[32], uint32_t (&pk)[16]) {
+#pragma unroll
+  for (int e = 0; e < 16; ++e) {
+    const __nv_bfloat162 b = __floats2bfloat162_rn(__uint_as_float(a[2 * e]), __uint_as_float(a[2 * e + 1]));
+    pk[e] = *reinterpret_cast<const uint32_t*>(&b);
+  }
+}
+__device__ __forceinline__ void stage_chunk(uint8_t* chunk, const uint32_t (&pk)[16], int lane) {
+#pragma unroll
+  for (int u = 0; u < 4; ++u)
+    *reinterpret_cast<uint4*>(chunk + lane * 64 + ((u ^ ((lane >> 1) & 3)) << 4)) =
+        make_uint4(pk[4 * u], pk[4 * u + 1], pk[4 * u + 2], pk[4 * u + 3]);
+}
+
+template <int BN, bool SWAP>
+__global__ void __launch_bounds__(NUM_THREADS, 1)
     gemm_pair_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_constant__ CUtensorMap tmap_b,
                      const __grid_constant__ CUtensorMap tmap_sa, const __grid_constant__ CUtensorMap tmap_sb,
                      const __grid_constant__ CUtensorMap tmap_c, const Params p) {
+  using G = Cfg<BN>;
+  constexpr int STAGES = G::STAGES, STAGE_BYTES = G::STAGE_BYTES, B_BYTES = G::B_BYTES;
   pdl_trigger();
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -75,11 +154,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
   uint64_t* acc_full = empty + STAGES;                              // each CTA: accumulator complete
   uint64_t* acc_empty = acc_full + 1;                               // leader: both CTAs drained it
   uint64_t* done_bar = acc_empty + 1;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(done_bar + 1);
+  uint64_t* xchg = done_bar + 1;                                    // a split tile's parts have arrived
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(xchg + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const uint32_t rank = cluster_ctarank();
+  const uint32_t cta = cluster_ctarank(), rank = cta & 1, pair = cta >> 1;  // in the cluster; in the pair
   const bool leader = rank == 0;
   if (threadIdx.x == 0) {
     for (int s = 0; s < STAGES; ++s) {
@@ -89,6 +169,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
     mbar_init(acc_full, 1);
     mbar_init(acc_empty, 2 * EPI_WARPS);
     mbar_init(done_bar, 1);
+    mbar_init(xchg, 1);
     *abort_flag = 0;
     fence_mbar_init();
   }
@@ -106,23 +187,28 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
   const uint32_t tmem = *tmem_slot;
   pdl_wait();  // (the set-up above touches no global data)
 
-  const uint32_t cluster_id = blockIdx.x >> 1, num_clusters = gridDim.x >> 1;
-  const uint32_t num_tiles = p.tiles_m * p.tiles_n, num_k = p.num_k;
-  auto tile_at = [&](uint32_t t, uint32_t& mb, uint32_t& nb) {
-    mb = p.n_fastest ? t / p.tiles_n : t % p.tiles_m;
-    nb = p.n_fastest ? t % p.tiles_n : t / p.tiles_m;
+  const uint32_t S = p.split, cluster_id = blockIdx.x / (2 * S), num_clusters = gridDim.x / (2 * S);
+  const uint32_t num_tiles = p.tiles_p * p.tiles_q;
+  const uint32_t k0 = pair * p.num_k / S, k1 = (pair + 1) * p.num_k / S;  // this pair's stages of K
+  const uint16_t both = static_cast<uint16_t>(3u << (2 * pair)), own = static_cast<uint16_t>(1u << (2 * pair));
+  auto tile_at = [&](uint32_t t, uint32_t& pb, uint32_t& qb) {
+    pb = p.q_fastest ? t / p.tiles_q : t % p.tiles_p;
+    qb = p.q_fastest ? t % p.tiles_q : t / p.tiles_p;
   };
+  // warp w's part of the epilogue: TMEM lane quadrant w % 4 (32 of this CTA's rows), half the columns
+  const uint32_t quad = warp & 3, h = (uint32_t)(warp - FIRST_EPI_WARP) >> 2;
+  const uint32_t lane_off = (quad * 32) << 16;
 
   if (warp == 0) {
     if (lane == 0) {
       // ---------------- TMA producer (both CTAs; completion on the leader's barrier) ----------------
-      const uint32_t full0 = mapa_shared(smem_u32(&full[0]), 0);
+      const uint32_t full0 = mapa_shared(smem_u32(&full[0]), cta & ~1u);
       uint32_t stage = 0, phase = 0;
       bool ok = true;
       for (uint32_t t = cluster_id; ok && t < num_tiles; t += num_clusters) {
-        uint32_t mb, nb;
-        tile_at(t, mb, nb);
-        for (uint32_t it = 0; it < num_k; ++it) {
+        uint32_t pb, qb;
+        tile_at(t, pb, qb);
+        for (uint32_t it = k0; it < k1; ++it) {
           if (!mbar_wait(&empty[stage], phase ^ 1)) {
             ok = false;
             break;
@@ -131,14 +217,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
           uint8_t* sB = sA + A_BYTES;
           uint8_t* sS = sB + B_BYTES;
           const uint32_t full_l = full0 + stage * 8;
-          const bool sf = it % kSfGroup == 0;
-          if (leader) mbar_arrive_expect_tx(&full[stage], 2 * (A_BYTES + B_BYTES + (sf ? SF_BYTES : 0)));
-          tma_load_2d_pair(sA, &tmap_a, full_l, (int32_t)(it * BK), (int32_t)(mb * 256 + rank * 128));
-          tma_load_2d_pair(sB, &tmap_b, full_l, (int32_t)(it * BK), (int32_t)(nb * 256 + rank * 128));
+          const bool sf = it % kSfGroup == 0 || it == k0;
+          if (leader) mbar_arrive_expect_tx(&full[stage], 2 * (A_BYTES + B_BYTES + (sf ? G::SF_BYTES : 0)));
+          tma_load_2d_pair(sA, &tmap_a, full_l, (int32_t)(it * BK), (int32_t)(pb * 256 + rank * 128));
+          tma_load_2d_pair(sB, &tmap_b, full_l, (int32_t)(it * BK), (int32_t)(qb * BN + rank * (BN / 2)));
           if (sf) {
             const int32_t x = (int32_t)(it / kSfGroup * 64);  // 8-byte units
-            tma_load_2d_pair(sS, &tmap_sa, full_l, x, (int32_t)(mb * 2 + rank));
-            tma_load_2d_pair(sS + SF_ATOM, &tmap_sb, full_l, x, (int32_t)(nb * 2));
+            tma_load_2d_pair(sS, &tmap_sa, full_l, x, (int32_t)(pb * 2 + rank));
+            tma_load_2d_pair(sS + SF_ATOM, &tmap_sb, full_l, x, (int32_t)(qb * BN / 128));
           }
           if (++stage == STAGES) stage = 0, phase ^= 1;
         }
@@ -157,46 +243,43 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
       for (uint32_t t = cluster_id; ok && t < num_tiles; t += num_clusters, ++n) {
         if (*abort_flag || !mbar_wait(acc_empty, (n & 1) ^ 1)) { ok = false; break; }
         tc_fence_after();
-        for (uint32_t it = 0; it < num_k; ++it) {
+        for (uint32_t it = k0; it < k1; ++it) {
           if (!mbar_wait(&full[stage], phase)) {
             ok = false;
             break;
           }
           tc_fence_after();
-          if (it % kSfGroup == 0) {
+          if (it % kSfGroup == 0 || it == k0) {
             slot ^= 1;
             const uint32_t sf = tmem + TM_SF + slot * TM_SF_SLOT;
             const uint64_t sd = sdesc0 + stage * kStageD;
             tc_cp_sf_pair(sf, sd);
-            tc_cp_sf_pair(sf + 8, sd + (SF_ATOM >> 4));
-            tc_cp_sf_pair(sf + 12, sd + (2 * SF_ATOM >> 4));
+#pragma unroll
+            for (int i = 0; i < G::SFB_ATOMS; ++i) tc_cp_sf_pair(sf + 8 + 4 * i, sd + ((1 + i) * SF_ATOM >> 4));
           }
           const uint32_t sfa = tmem + TM_SF + slot * TM_SF_SLOT, sfb = sfa + 8;
-          const uint32_t idesc = idesc_mxf8(256, 256) | idesc_sf(it % kSfGroup);
+          const uint32_t idesc = idesc_mxf8(256, BN) | idesc_sf(it % kSfGroup);
           const uint64_t ad = adesc0 + stage * kStageD, bd = bdesc0 + stage * kStageD;
-          mma_mxf8_pair(tmem + TM_ACC, ad, bd, idesc, sfa, sfb, it != 0);
+          mma_mxf8_pair(tmem + TM_ACC, ad, bd, idesc, sfa, sfb, it != k0);
           mma_mxf8_pair(tmem + TM_ACC, ad + 2, bd + 2, idesc, sfa, sfb, 1);
           mma_mxf8_pair(tmem + TM_ACC, ad + 4, bd + 4, idesc, sfa, sfb, 1);
           mma_mxf8_pair(tmem + TM_ACC, ad + 6, bd + 6, idesc, sfa, sfb, 1);
-          tc_commit_pair_mc(&empty[stage], 3);
+          tc_commit_pair_mc(&empty[stage], both);
           if (++stage == STAGES) stage = 0, phase ^= 1;
         }
         if (!ok) break;
-        tc_commit_pair_mc(acc_full, 3);
+        tc_commit_pair_mc(acc_full, both);
       }
       if (!ok) *abort_flag = 1;
-      tc_commit_pair_mc(done_bar, 1);
+      tc_commit_pair_mc(done_bar, own);
       mbar_wait(done_bar, 0);
     }
   } else {
     // ---------------- epilogue (both CTAs) ----------------
-    // warp w reads TMEM lane quadrant w % 4 (32 of this CTA's rows) and 128 columns, in four chunks of 32
-    const uint32_t quad = warp & 3, h = (uint32_t)(warp - FIRST_EPI_WARP) >> 2;
-    const uint32_t lane_off = (quad * 32) << 16;
-    const uint32_t acc_empty0 = mapa_shared(smem_u32(acc_empty), 0);
+    const uint32_t acc_empty0 = mapa_shared(smem_u32(acc_empty), cta & ~1u);
     uint8_t* buf0 = s_out + (warp - FIRST_EPI_WARP) * 2 * CHUNK_BYTES;
     uint8_t* buf1 = buf0 + CHUNK_BYTES;
-    const uint32_t tacc = tmem + lane_off + TM_ACC + h * 128;
+    const uint32_t tacc = tmem + lane_off + TM_ACC + h * (BN / 2);
     auto release = [&] {  // every TMEM read of this warp is complete
       tc_fence_before();
       __syncwarp();
@@ -207,103 +290,170 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
     };
     uint32_t n = 0;
     for (uint32_t t = cluster_id; t < num_tiles; t += num_clusters, ++n) {
-      uint32_t mb, nb;
-      tile_at(t, mb, nb);
+      uint32_t pb, qb;
+      tile_at(t, pb, qb);
       if (*abort_flag || !mbar_wait_warp(acc_full, n & 1)) {
         *abort_flag = 1;
         break;
       }
       tc_fence_after();
-      const uint32_t row0 = mb * 256 + rank * 128 + quad * 32, col0 = nb * 256 + h * 128;
-      if (p.tma_store) {
-        auto convert = [&](const uint32_t (&a)[32], uint32_t (&pk)[16]) {
-#pragma unroll
-          for (int e = 0; e < 16; ++e) {
-            const __nv_bfloat162 b = __floats2bfloat162_rn(__uint_as_float(a[2 * e]), __uint_as_float(a[2 * e + 1]));
-            pk[e] = *reinterpret_cast<const uint32_t*>(&b);
+      if (S > 1) break;  // the partial tile is exchanged below
+      const uint32_t row0 = pb * 256 + rank * 128 + quad * 32, col0 = qb * BN + h * (BN / 2);
+      if constexpr (BN == 256 && !SWAP) {
+        if (p.tma_store) {
+          auto store = [&](const uint8_t* chunk, uint32_t col) {  // (clipped at the tensor's edges)
+            if (col < p.Q && row0 < p.P) tma_store_2d(&tmap_c, chunk, (int32_t)col, (int32_t)row0);
+          };
+          uint32_t ra[32], rb[32], pk[16], pk2[16], pk3[16];
+          if (lane == 0) bulk_wait_read<0>();  // the previous tile's stores have read both buffers
+          __syncwarp();
+          tmem_ld_32x32b_x32(tacc, ra);
+          tmem_ld_wait(ra);
+          tmem_ld_32x32b_x32(tacc + 32, rb);
+          convert(ra, pk);
+          stage_chunk(buf0, pk, lane);
+          tmem_ld_wait(rb);
+          tmem_ld_32x32b_x32(tacc + 64, ra);
+          convert(rb, pk);
+          stage_chunk(buf1, pk, lane);
+          tmem_ld_wait(ra);
+          tmem_ld_32x32b_x32(tacc + 96, rb);
+          convert(ra, pk2);
+          tmem_ld_wait(rb);
+          release();
+          convert(rb, pk3);
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) {
+            store(buf0, col0);
+            store(buf1, col0 + 32);
+            bulk_commit_group();
+            bulk_wait_read<0>();
           }
-        };
-        // row = lane, 64 bytes; 16-byte unit u lands at u ^ ((row >> 1) & 3) (64-byte swizzle)
-        auto stage_chunk = [&](uint8_t* chunk, const uint32_t (&pk)[16]) {
-#pragma unroll
-          for (int u = 0; u < 4; ++u)
-            *reinterpret_cast<uint4*>(chunk + lane * 64 + ((u ^ ((lane >> 1) & 3)) << 4)) =
-                make_uint4(pk[4 * u], pk[4 * u + 1], pk[4 * u + 2], pk[4 * u + 3]);
-        };
-        auto store = [&](const uint8_t* chunk, uint32_t col) {  // (clipped at the tensor's edges)
-          if (col < p.N && row0 < p.M) tma_store_2d(&tmap_c, chunk, (int32_t)col, (int32_t)row0);
-        };
-        uint32_t ra[32], rb[32], pk[16], pk2[16], pk3[16];
-        if (lane == 0) bulk_wait_read<0>();  // the previous tile's stores have read both buffers
-        __syncwarp();
-        tmem_ld_32x32b_x32(tacc, ra);
-        tmem_ld_wait(ra);
-        tmem_ld_32x32b_x32(tacc + 32, rb);
-        convert(ra, pk);
-        stage_chunk(buf0, pk);
-        tmem_ld_wait(rb);
-        tmem_ld_32x32b_x32(tacc + 64, ra);
-        convert(rb, pk);
-        stage_chunk(buf1, pk);
-        tmem_ld_wait(ra);
-        tmem_ld_32x32b_x32(tacc + 96, rb);
-        convert(ra, pk2);
-        tmem_ld_wait(rb);
-        release();
-        convert(rb, pk3);
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) {
-          store(buf0, col0);
-          store(buf1, col0 + 32);
-          bulk_commit_group();
-          bulk_wait_read<0>();
+          __syncwarp();
+          stage_chunk(buf0, pk2, lane);
+          stage_chunk(buf1, pk3, lane);
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) {
+            store(buf0, col0 + 64);
+            store(buf1, col0 + 96);
+            bulk_commit_group();
+          }
+          continue;
         }
-        __syncwarp();
-        stage_chunk(buf0, pk2);
-        stage_chunk(buf1, pk3);
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) {
-          store(buf0, col0 + 64);
-          store(buf1, col0 + 96);
-          bulk_commit_group();
-        }
-      } else {
-        const uint32_t row = row0 + lane;
+      }
 #pragma unroll 1
-        for (int j = 0; j < 4; ++j) {
-          uint32_t acc[32];
-          tmem_ld_32x32b_x32(tacc + j * 32, acc);
-          tmem_ld_wait(acc);
-          const uint32_t col = col0 + j * 32;
-          if (row < p.M && col < p.N) {
-            if (p.c_f32) {
-              float* dst = static_cast<float*>(p.C) + (size_t)row * p.ldc + col;
-              if (p.vec && col + 32 <= p.N) {
+      for (int j = 0; j < BN / 64; ++j) {
+        uint32_t acc[32];
+        tmem_ld_32x32b_x32(tacc + j * 32, acc);
+        tmem_ld_wait(acc);
+        store_direct<SWAP>(p, acc, row0 + lane, col0 + j * 32);
+      }
+      release();
+    }
+  }
+
+  if (S > 1) {
+    // ---------------- a split tile ----------------
+    // Pair i adds columns [i BN / S, +BN / S).  A CTA writes the other pairs' columns, [pair][column][128 rows], to its
+    // own shared memory and sends each pair's part by one bulk copy (stores to another CTA's shared memory one
+    // word a lane took 10 us for 32 KB); the parts that it receives follow, in the order of their pairs.
+    __syncwarp();
+    cluster_sync();  // every CTA's MMAs are done, its stages free
+    const uint32_t width = BN / S, log_width = __ffs(width) - 1;  // (powers of two)
+    const uint32_t part_bytes = width * 512, received = (S - 1) * part_bytes;
+    float* send = reinterpret_cast<float*>(smem);
+    const float* got = reinterpret_cast<const float*>(smem + received);
+    uint32_t pb, qb;
+    tile_at(cluster_id, pb, qb);
+    if (warp >= FIRST_EPI_WARP) {
+      const bool works = *abort_flag == 0;
+      tc_fence_after();
+      // (small loops here and below: straight-line code that a CTA runs once costs its instruction fetches, 15 us of
+      //  them when these were unrolled over 32 columns)
+#pragma unroll 1
+      for (uint32_t j = h * 8; j < BN - width; j += 16) {  // the others' columns, j and on without this pair's
+        uint32_t acc[8];
+        tmem_ld_32x32b_x8(tmem + lane_off + TM_ACC + j + (j >= pair * width ? width : 0), acc);
 #pragma unroll
-                for (int i = 0; i < 8; ++i)
-                  reinterpret_cast<uint4*>(dst)[i] = make_uint4(acc[4 * i], acc[4 * i + 1], acc[4 * i + 2], acc[4 * i + 3]);
-              } else {
+        for (int i = 0; i < 8; ++i) send[(j + i) * 128 + quad * 32 + lane] = __uint_as_float(acc[i]);
+      }
+      fence_proxy_async_smem();
+      asm volatile("bar.sync 1, 256;" ::: "memory");
+      if (warp == FIRST_EPI_WARP && lane == 0) {
+        mbar_arrive_expect_tx(xchg, received);
+        for (uint32_t i = 0; i < S; ++i) {
+          if (i == pair) continue;
+          const uint32_t there = i * 2 + rank, from = pair - (pair > i ? 1 : 0);  // my place among its parts
+          asm volatile(
+              "cp.async.bulk.shared::cluster.shared::cta.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+                  mapa_shared(smem_u32(smem) + received + from * part_bytes, there)),
+              "r"(smem_u32(smem) + (i - (i > pair ? 1 : 0)) * part_bytes), "r"(part_bytes),
+              "r"(mapa_shared(smem_u32(xchg), there))
+              : "memory");
+        }
+      }
+      __syncwarp();
+      if (!mbar_wait_warp(xchg, 0)) *abort_flag = 1;
+      if (works && *abort_flag == 0) {
+        const uint32_t row0 = pb * 256 + rank * 128 + quad * 32, col0 = qb * BN + pair * width;
+        uint8_t* buf = s_out + (warp - FIRST_EPI_WARP) * 2 * CHUNK_BYTES;
+        // units of 8 columns; with TMA stores, chunks of 32 of them (h's chunks), else every other unit
+        const bool chunks = !SWAP && p.tma_store && width >= 64;
+#pragma unroll 1
+        for (uint32_t n = 0; n < width / 16; ++n) {
+          const uint32_t in = chunks ? h * (width / 2) + n * 8 : (2 * n + h) * 8, col = col0 + in;
+          uint32_t own_part[8];
+          tmem_ld_32x32b_x8(tmem + lane_off + TM_ACC + pair * width + in, own_part);
+          float v[8];
+#pragma unroll 1
+          for (uint32_t s = 0; s < S; ++s) {  // in the order of K
+            const float* x = got + ((s - (s > pair ? 1 : 0)) * width + in) * 128 + quad * 32 + lane;
 #pragma unroll
-                for (int i = 0; i < 32; ++i)
-                  if (col + i < p.N) dst[i] = __uint_as_float(acc[i]);
+            for (int i = 0; i < 8; ++i) {
+              const float y = s == pair ? __uint_as_float(own_part[i]) : x[i * 128];
+              v[i] = s == 0 ? y : v[i] + y;
+            }
+          }
+          if (chunks) {
+            if ((n & 3) == 0) {
+              if (lane == 0) bulk_wait_read<0>();
+              __syncwarp();
+            }
+            uint4 o;
+            uint32_t* w = reinterpret_cast<uint32_t*>(&o);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const __nv_bfloat162 b = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
+              w[i] = *reinterpret_cast<const uint32_t*>(&b);
+            }
+            *reinterpret_cast<uint4*>(buf + lane * 64 + (((n & 3) ^ ((lane >> 1) & 3)) << 4)) = o;
+            if ((n & 3) == 3) {
+              fence_proxy_async_smem();
+              __syncwarp();
+              if (lane == 0) {
+                if (col - 24 < p.Q && row0 < p.P) tma_store_2d(&tmap_c, buf, (int32_t)(col - 24), (int32_t)row0);
+                bulk_commit_group();
               }
-            } else {
-              __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(p.C) + (size_t)row * p.ldc + col;
+            }
+          } else {
 #pragma unroll
-              for (int i = 0; i < 32; ++i)
-                if (col + i < p.N) dst[i] = __float2bfloat16_rn(__uint_as_float(acc[i]));
+            for (int i = 0; i < 8; ++i) {
+              const uint32_t m = SWAP ? col + i : row0 + lane, k = SWAP ? row0 + lane : col + i;  // C's row and column
+              if (row0 + lane < p.P && col + i < p.Q) {
+                if (p.c_f32) static_cast<float*>(p.C)[(size_t)m * p.ldc + k] = v[i];
+                else static_cast<__nv_bfloat16*>(p.C)[(size_t)m * p.ldc + k] = __float2bfloat16_rn(v[i]);
+              }
             }
           }
         }
-        release();
       }
+      tc_fence_before();
     }
-    if (lane == 0) bulk_wait_all();
     __syncwarp();
   }
-
+  if (lane == 0) bulk_wait_all();  // this thread's TMA stores
   __syncthreads();
   if (*abort_flag) {  // a wait expired: let copies still in flight land first
     if (threadIdx.x == 0) drain_pause();
@@ -318,47 +468,84 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
   cluster_sync();
 }
 
-}  // namespace f8
-
-cudaError_t launch_fp8_gemm(const Fp8GemmArgs& g, int num_sms, cudaStream_t s) {
-  using namespace f8;
-  static cudaError_t attr =
-      cudaFuncSetAttribute(gemm_pair_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_BYTES);
+struct Operand {
+  const void *codes, *scales;
+  int64_t rows;
+};
+template <int BN, bool SWAP>
+static cudaError_t launch(const Operand& P, const Operand& Q, const Fp8GemmArgs& g, int num_sms, cudaStream_t s) {
+  using G = Cfg<BN>;
+  auto kernel = gemm_pair_kernel<BN, SWAP>;
+  static const cudaError_t attr = [&] {
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, G::SMEM_BYTES);
+    return e != cudaSuccess ? e : cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+  }();
   if (attr != cudaSuccess) return attr;
   const uint64_t pitch = fp8_pitch(g.K), atoms = (g.K + 511) / 512;
   CUtensorMap ta, tb, tsa, tsb, tc;
   const auto u8 = CU_TENSOR_MAP_DATA_TYPE_UINT8, u64 = CU_TENSOR_MAP_DATA_TYPE_UINT64;
-  if (!encode_tmap_2d(&ta, u8, g.a_codes, pitch, g.M, pitch, BK, 128, CU_TENSOR_MAP_SWIZZLE_128B) ||
-      !encode_tmap_2d(&tb, u8, g.b_codes, pitch, g.N, pitch, BK, 128, CU_TENSOR_MAP_SWIZZLE_128B) ||
-      !encode_tmap_2d(&tsa, u64, g.a_scales, atoms * 64, (g.M + 127) / 128, atoms * 512, 64, 1, CU_TENSOR_MAP_SWIZZLE_NONE) ||
-      !encode_tmap_2d(&tsb, u64, g.b_scales, atoms * 64, (g.N + 127) / 128, atoms * 512, 64, 2, CU_TENSOR_MAP_SWIZZLE_NONE))
+  if (!encode_tmap_2d(&ta, u8, P.codes, pitch, P.rows, pitch, BK, 128, CU_TENSOR_MAP_SWIZZLE_128B) ||
+      !encode_tmap_2d(&tb, u8, Q.codes, pitch, Q.rows, pitch, BK, BN / 2, CU_TENSOR_MAP_SWIZZLE_128B) ||
+      !encode_tmap_2d(&tsa, u64, P.scales, atoms * 64, (P.rows + 127) / 128, atoms * 512, 64, 1,
+                      CU_TENSOR_MAP_SWIZZLE_NONE) ||
+      !encode_tmap_2d(&tsb, u64, Q.scales, atoms * 64, (Q.rows + 127) / 128, atoms * 512, 64, G::SFB_ATOMS,
+                      CU_TENSOR_MAP_SWIZZLE_NONE))
     return cudaErrorInvalidValue;
   Params p{};
-  p.M = (uint32_t)g.M;
-  p.N = (uint32_t)g.N;
+  p.P = (uint32_t)P.rows;
+  p.Q = (uint32_t)Q.rows;
   p.num_k = (uint32_t)(pitch / BK);
-  p.tiles_m = (p.M + 255) / 256;
-  p.tiles_n = (p.N + 255) / 256;
-  p.n_fastest = g.M > g.N;
+  p.tiles_p = (p.P + 255) / 256;
+  p.tiles_q = (p.Q + BN - 1) / BN;
+  p.q_fastest = P.rows > Q.rows;
   p.C = g.C;
   p.ldc = g.ldc;
   p.c_f32 = g.c_f32;
   const bool aligned = (reinterpret_cast<uintptr_t>(g.C) & 15u) == 0 && (g.ldc * (g.c_f32 ? 4 : 2)) % 16 == 0;
   p.vec = aligned;
-  p.tma_store = aligned && !g.c_f32;
+  p.tma_store = aligned && !g.c_f32 && !SWAP;
   if (p.tma_store) {
     if (!encode_tmap_2d(&tc, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, g.C, g.N, g.M, (uint64_t)g.ldc * 2, 32, 32,
-                CU_TENSOR_MAP_SWIZZLE_64B))
+                        CU_TENSOR_MAP_SWIZZLE_64B))
       return cudaErrorInvalidValue;
   } else {
     tc = ta;
   }
-  const uint32_t tiles = p.tiles_m * p.tiles_n, pairs = (uint32_t)num_sms / 2;
+  // Pairs left without a tile share the others' K, while a share keeps at least kMinShare stages: exchanging the
+  // partial tile takes as long as some 14 stages (11000 cycles of 770 with BN = 256, 6000 of 450 with 128).
+  constexpr uint32_t kMinShare = 10;
+  const uint32_t tiles = p.tiles_p * p.tiles_q, pairs = (uint32_t)num_sms / 2;
+  uint32_t S = 1;
+  while (S < G::MAX_SPLIT && tiles * S * 2 <= pairs && p.num_k >= 2 * S * kMinShare) S *= 2;
+  p.split = S;
   const uint32_t clusters = tiles < pairs ? tiles : pairs;
-  const cudaError_t e =
-      launch_pdl(gemm_pair_kernel, dim3(clusters * 2), dim3(NUM_THREADS), SMEM_BYTES, s, ta, tb, tsa, tsb, tc, p);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(clusters * 2 * S);
+  cfg.blockDim = dim3(NUM_THREADS);
+  cfg.dynamicSmemBytes = G::SMEM_BYTES;
+  cfg.stream = s;
+  cudaLaunchAttribute attrs[2];
+  attrs[0].id = cudaLaunchAttributeClusterDimension;
+  attrs[0].val.clusterDim.x = 2 * S;
+  attrs[0].val.clusterDim.y = 1;
+  attrs[0].val.clusterDim.z = 1;
+  attrs[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attrs[1].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attrs;
+  cfg.numAttrs = g_pdl_chain ? 2 : 1;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, ta, tb, tsa, tsb, tc, p);
+  g_pdl_chain = e == cudaSuccess;
   count_launch();
   return e;
+}
+
+}  // namespace f8
+
+cudaError_t launch_fp8_gemm(const Fp8GemmArgs& g, int num_sms, cudaStream_t s) {
+  const f8::Operand A{g.a_codes, g.a_scales, g.M}, B{g.b_codes, g.b_scales, g.N};
+  if (g.M <= 64) return f8::launch<64, true>(B, A, g, num_sms, s);
+  if (g.M <= 128) return f8::launch<128, true>(B, A, g, num_sms, s);
+  return f8::launch<256, false>(A, B, g, num_sms, s);
 }
 
 cudaError_t fp8_status_read_clear(unsigned int* out, cudaStream_t s) {

@@ -598,12 +598,18 @@ __global__ void __launch_bounds__(threads_of(TOP), per_sm_of(TOP)) logprob_kerne
           r.e += (o.e + o.s * d) * f;
         }
         if constexpr (TOP) {
-          const uint32_t n = C * a.top_k;
-          for (uint32_t i = lane; i < n; i += 32) {
-            const uint64_t y = s_joined_top[buf][i];
-            uint32_t better = 0;
-            for (uint32_t j = 0; j < n; ++j) better += s_joined_top[buf][j] > y;
-            if (y != 0 && better < a.top_k) x.top[better] = y;
+          // the shares' lists are in order: k rounds of the largest head
+          uint32_t at = 0;
+          uint64_t head = lane < C ? s_joined_top[buf][lane * a.top_k] : 0;
+          for (uint32_t i = 0; i < a.top_k; ++i) {
+            uint64_t best = head;
+#pragma unroll
+            for (int o = 1; o < kMaxCluster; o <<= 1) {
+              const uint64_t other = __shfl_xor_sync(0xFFFFFFFFu, best, o);
+              best = other > best ? other : best;
+            }
+            if (lane == 0) x.top[i] = best;
+            if (lane < C && head == best) head = ++at < a.top_k ? s_joined_top[buf][lane * a.top_k + at] : 0;
           }
         }
         __syncwarp();
