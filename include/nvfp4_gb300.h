@@ -398,7 +398,8 @@ fp4_status fp4_fp8_gemm(const fp4_fp8_tensor* A, const fp4_fp8_tensor* B, void* 
 /* Y (M x N BF16) = X W^T: X (M x K BF16, pitch ldx) quantized in blocks of 1 x 128, Wq N x K (blocks of
  * 128 x 128 or 1 x 128).  xqT_saved (K x M, caller-owned; NULL: not wanted) receives X's column form for
  * dW.  M = 0 without xqT_saved is a call without work.
- * ws: fp4_fp8_linear_fwd_workspace(M, N, K) bytes, 256-byte aligned, scratch. */
+ * ws: fp4_fp8_linear_fwd_workspace(M, N, K) bytes, 256-byte aligned, scratch; 0 bytes (ws may be NULL)
+ * for a few tokens, which take one launch that quantizes X on the way. */
 size_t fp4_fp8_linear_fwd_workspace(int64_t M, int64_t N, int64_t K);
 fp4_status fp4_fp8_linear_fwd(const void* X, int64_t M, int64_t K, int64_t ldx, const fp4_fp8_tensor* Wq, void* Y,
                               int64_t ldy, const fp4_fp8_tensor* xqT_saved, void* ws, size_t ws_bytes,

@@ -526,6 +526,7 @@ def fp4_qadamw_v_decode(q: NVFP4Tensor, mean: torch.Tensor, out: torch.Tensor | 
 
 
 FP8_BLOCK = 128  # elements that share a scale byte
+_BF16 = (torch.bfloat16,)
 
 
 class FP8Tensor:
@@ -572,6 +573,18 @@ def _out_2d(t, rows: int, cols: int, dtypes, device, name: str) -> torch.Tensor:
     return torch.empty((rows, -(-cols // unit) * unit), dtype=dtype, device=device)[:, :cols]
 
 
+def _matrix(x: torch.Tensor, name: str):
+    """(rows, columns, row pitch) of a BF16 matrix of any pitch; one row's pitch is its width.  (The small calls below
+    are bound by the host: sizes and strides are asked for once.)"""
+    if x.dtype != torch.bfloat16 or x.dim() != 2 or not x.is_cuda:
+        raise ValueError(f"{name} must be a 2-D CUDA bfloat16 tensor with unit column stride")
+    rows, cols = x.shape
+    s0, s1 = x.stride()
+    if s1 != 1 and cols > 1:
+        raise ValueError(f"{name} must be a 2-D CUDA bfloat16 tensor with unit column stride")
+    return rows, cols, s0 if rows > 1 else max(cols, 1)
+
+
 def _pitch(t: torch.Tensor) -> int:
     """Row pitch of a 2-D tensor; one row has its width."""
     return t.stride(0) if t.shape[0] > 1 else max(t.shape[1], 1)
@@ -579,32 +592,32 @@ def _pitch(t: torch.Tensor) -> int:
 
 def fp4_fp8_quantize(x: torch.Tensor, block_rows: int = 1, out: FP8Tensor | None = None, stream=None) -> FP8Tensor:
     """BF16 x to FP8, blocks of ``block_rows`` (1: activations, 128: weights) x 128."""
-    R, C, _ = _bf16_2d(x, "x")
+    R, C, ld = _matrix(x, "x")
     out = FP8Tensor.empty(R, C, x.device) if out is None else out
     _check_fp8(out, R, C, x.device, "out")
-    _check(lib().fp4_fp8_quantize(x.data_ptr(), R, C, _pitch(x), block_rows, out.c(), None, _stream(stream)))
+    _check(lib().fp4_fp8_quantize(x.data_ptr(), R, C, ld, block_rows, out.c(), None, _stream(stream)))
     return out
 
 
 def fp4_fp8_quantize_transposed(x: torch.Tensor, block_rows: int = 1, out: FP8Tensor | None = None,
                                 stream=None) -> FP8Tensor:
     """BF16 x (R x C) to the FP8 tensor of its transpose (C x R), blocks along x's rows."""
-    R, C, _ = _bf16_2d(x, "x")
+    R, C, ld = _matrix(x, "x")
     out = FP8Tensor.empty(C, R, x.device) if out is None else out
     _check_fp8(out, C, R, x.device, "out")
-    _check(lib().fp4_fp8_quantize(x.data_ptr(), R, C, _pitch(x), block_rows, None, out.c(), _stream(stream)))
+    _check(lib().fp4_fp8_quantize(x.data_ptr(), R, C, ld, block_rows, None, out.c(), _stream(stream)))
     return out
 
 
 def fp4_fp8_quantize_dual(x: torch.Tensor, block_rows: int = 1, out_row: FP8Tensor | None = None,
                           out_col: FP8Tensor | None = None, stream=None):
     """Both forms from one read of x."""
-    R, C, _ = _bf16_2d(x, "x")
+    R, C, ld = _matrix(x, "x")
     out_row = FP8Tensor.empty(R, C, x.device) if out_row is None else out_row
     out_col = FP8Tensor.empty(C, R, x.device) if out_col is None else out_col
     _check_fp8(out_row, R, C, x.device, "out_row")
     _check_fp8(out_col, C, R, x.device, "out_col")
-    _check(lib().fp4_fp8_quantize(x.data_ptr(), R, C, _pitch(x), block_rows, out_row.c(), out_col.c(),
+    _check(lib().fp4_fp8_quantize(x.data_ptr(), R, C, ld, block_rows, out_row.c(), out_col.c(),
                                   _stream(stream)))
     return out_row, out_col
 
@@ -633,33 +646,39 @@ def fp4_fp8_linear_fwd(X: torch.Tensor, Wq: FP8Tensor, Y=None, xqT_saved: FP8Ten
                        workspace=None, stream=None):
     """Y = X W^T (M x N BF16).  Returns (Y, xqT_saved); with ``save=False`` (inference) the column form of X for the
     weight gradient is not made and the second value is None."""
-    M, K, _ = _bf16_2d(X, "X")
+    M, K, ldx = _matrix(X, "X")
     dev, N = X.device, Wq.rows
     _check_fp8(Wq, N, K, dev, "Wq")
-    Y = _out_2d(Y, M, N, (torch.bfloat16,), dev, "Y")
+    Y = _out_2d(Y, M, N, _BF16, dev, "Y")
     if xqT_saved is None and save:
         xqT_saved = FP8Tensor.empty(K, M, dev)
     if xqT_saved is not None:
         _check_fp8(xqT_saved, K, M, dev, "xqT_saved")
+    L = lib()
+    ws = 0
     if workspace is None:
-        workspace = torch.empty(fp8_linear_fwd_workspace(M, N, K), dtype=torch.uint8, device=dev)
-    _check(lib().fp4_fp8_linear_fwd(X.data_ptr(), M, K, _pitch(X), Wq.c(), Y.data_ptr(), _pitch(Y),
-                                    None if xqT_saved is None else xqT_saved.c(), workspace.data_ptr(),
-                                    workspace.numel(), _stream(stream)))
+        ws = L.fp4_fp8_linear_fwd_workspace(M, N, K)  # 0 for a few tokens
+        if ws:
+            workspace = torch.empty(ws, dtype=torch.uint8, device=dev)
+    else:
+        ws = workspace.numel()
+    _check(L.fp4_fp8_linear_fwd(X.data_ptr(), M, K, ldx, Wq.c(), Y.data_ptr(), _pitch(Y),
+                                None if xqT_saved is None else xqT_saved.c(),
+                                None if workspace is None else workspace.data_ptr(), ws, _stream(stream)))
     return Y, xqT_saved
 
 
 def fp4_fp8_linear_bwd(dY: torch.Tensor, WqT: FP8Tensor | None, xqT_saved: FP8Tensor | None, dX=None, dW=None,
                        dw_dtype=torch.bfloat16, workspace=None, stream=None):
     """dX = dY W, dW = dY^T X.  Returns (dX, dW); without ``WqT`` or ``xqT_saved`` that gradient is not made (None)."""
-    M, N, _ = _bf16_2d(dY, "dY")
+    M, N, lddy = _matrix(dY, "dY")
     dev = dY.device
     if WqT is None and xqT_saved is None:
         raise ValueError("neither WqT nor xqT_saved is given")
     K = WqT.rows if WqT is not None else xqT_saved.rows
     if WqT is not None:
         _check_fp8(WqT, K, N, dev, "WqT")
-        dX = _out_2d(dX, M, K, (torch.bfloat16,), dev, "dX")
+        dX = _out_2d(dX, M, K, _BF16, dev, "dX")
     elif dX is not None:
         raise ValueError("dX needs WqT")
     if xqT_saved is not None:
@@ -671,7 +690,7 @@ def fp4_fp8_linear_bwd(dY: torch.Tensor, WqT: FP8Tensor | None, xqT_saved: FP8Te
         raise ValueError("dW needs xqT_saved")
     if workspace is None:
         workspace = torch.empty(fp8_linear_bwd_workspace(M, N, K), dtype=torch.uint8, device=dev)
-    _check(lib().fp4_fp8_linear_bwd(dY.data_ptr(), M, N, _pitch(dY), None if WqT is None else WqT.c(),
+    _check(lib().fp4_fp8_linear_bwd(dY.data_ptr(), M, N, lddy, None if WqT is None else WqT.c(),
                                     None if xqT_saved is None else xqT_saved.c(), _ptr(dX),
                                     0 if dX is None else _pitch(dX), _ptr(dW),
                                     OUT_F32 if dW is not None and dW.dtype == torch.float32 else OUT_BF16,
@@ -684,24 +703,29 @@ def fp4_fp8_linear_bwd(dY: torch.Tensor, WqT: FP8Tensor | None, xqT_saved: FP8Te
 class TokenLogprobs:
     """Result of ``fp4_token_logprobs`` for T rows: ``logprob`` float32 [T] (None without targets), ``entropy``
     float32 [T] (None if not wanted), ``stats`` float32 [T, 2] = (max logit, sum of exp((z - max) / temperature)),
-    ``top_logprob`` float32 and ``top_index`` int64 [T, top_k], and the ``temperature`` of the call."""
+    ``top_logprob`` float32 and ``top_index`` int64 [T, top_k] (None without top_k), and the ``temperature`` of the
+    call."""
     logprob: torch.Tensor | None
     entropy: torch.Tensor | None
     stats: torch.Tensor
-    top_logprob: torch.Tensor
-    top_index: torch.Tensor
+    top_logprob: torch.Tensor | None
+    top_index: torch.Tensor | None
     temperature: float
 
 
 def _logits_2d(x: torch.Tensor, name: str):
     """(dtype code, T, V, row pitch) of a matrix of logits; the pitch of fewer than two rows is not used."""
-    if x.dtype not in (torch.bfloat16, torch.float32) or x.dim() != 2 or not x.is_cuda or x.stride(1) != 1:
+    if x.dim() != 2 or not x.is_cuda or x.dtype not in _LOGIT_CODES:
         raise ValueError(f"{name} must be a 2-D CUDA bfloat16 or float32 tensor with unit column stride")
     T, V = x.shape
-    ld = x.stride(0) if T > 1 else max(V, 1)
-    if ld < V:
-        raise ValueError(f"{name}: rows overlap (row stride {ld} < {V})")
-    return OUT_F32 if x.dtype == torch.float32 else OUT_BF16, T, V, ld
+    s0, s1 = x.stride()
+    ld = s0 if T > 1 else max(V, 1)
+    if (s1 != 1 and V > 1) or ld < V:
+        raise ValueError(f"{name} must have unit column stride and rows that do not overlap (strides {s0}, {s1})")
+    return _LOGIT_CODES[x.dtype], T, V, ld
+
+
+_LOGIT_CODES = {torch.bfloat16: OUT_BF16, torch.float32: OUT_F32}
 
 
 def _check_vector(t, shape, dtype, device, name: str) -> None:
@@ -720,16 +744,16 @@ def fp4_token_logprobs(logits: torch.Tensor, targets: torch.Tensor | None = None
     dtype, T, V, ld = _logits_2d(logits, "logits")
     dev = logits.device
     _check_vector(targets, (T,), torch.int64, dev, "targets")
-    f32 = torch.float32
-    r = TokenLogprobs(torch.empty(T, dtype=f32, device=dev) if targets is not None else None,
-                      torch.empty(T, dtype=f32, device=dev) if entropy else None,
-                      torch.empty((T, 2), dtype=f32, device=dev),
-                      torch.empty((T, max(top_k, 0)), dtype=f32, device=dev),
-                      torch.empty((T, max(top_k, 0)), dtype=torch.int64, device=dev), float(temperature))
-    _check(lib().fp4_token_logprobs(logits.data_ptr(), dtype, T, V, ld, r.temperature, _ptr(targets), top_k,
-                                    _ptr(r.logprob), _ptr(r.entropy), r.stats.data_ptr(), r.top_logprob.data_ptr(),
-                                    r.top_index.data_ptr(), _stream(stream)))
-    return r
+    f32, some = torch.float32, top_k > 0
+    logprob = torch.empty(T, dtype=f32, device=dev) if targets is not None else None
+    H = torch.empty(T, dtype=f32, device=dev) if entropy else None
+    stats = torch.empty((T, 2), dtype=f32, device=dev)
+    top_logprob = torch.empty((T, top_k), dtype=f32, device=dev) if some else None
+    top_index = torch.empty((T, top_k), dtype=torch.int64, device=dev) if some else None
+    _check(lib().fp4_token_logprobs(logits.data_ptr(), dtype, T, V, ld, temperature, _ptr(targets), top_k,
+                                    _ptr(logprob), _ptr(H), stats.data_ptr(), _ptr(top_logprob), _ptr(top_index),
+                                    _stream(stream)))
+    return TokenLogprobs(logprob, H, stats, top_logprob, top_index, float(temperature))
 
 
 def fp4_token_logprobs_bwd(logits: torch.Tensor, saved: TokenLogprobs, targets: torch.Tensor | None = None,
@@ -737,7 +761,7 @@ def fp4_token_logprobs_bwd(logits: torch.Tensor, saved: TokenLogprobs, targets: 
     """Gradient of sum(g_logprob logprob) + sum(g_entropy entropy) + sum(g_top top_logprob) with respect to the
     logits, from the forward call's result.  Pass ``dlogits=logits`` to write over them."""
     dtype, T, V, ld = _logits_2d(logits, "logits")
-    dev, f32, k = logits.device, torch.float32, saved.top_index.shape[1]
+    dev, f32, k = logits.device, torch.float32, 0 if saved.top_index is None else saved.top_index.shape[1]
     _check_vector(targets, (T,), torch.int64, dev, "targets")
     _check_vector(saved.stats, (T, 2), f32, dev, "saved.stats")
     _check_vector(saved.entropy, (T,), f32, dev, "saved.entropy")
@@ -749,8 +773,8 @@ def fp4_token_logprobs_bwd(logits: torch.Tensor, saved: TokenLogprobs, targets: 
     ldd = dlogits.stride(0) if T > 1 else max(V, 1)
     _check(lib().fp4_token_logprobs_bwd(logits.data_ptr(), dtype, T, V, ld, saved.temperature, _ptr(targets),
                                         saved.stats.data_ptr(), _ptr(saved.entropy), _ptr(g_logprob),
-                                        _ptr(g_entropy), k, _ptr(saved.top_index) if k else None,
-                                        _ptr(g_top) if k else None, dlogits.data_ptr(), ldd, _stream(stream)))
+                                        _ptr(g_entropy), k, _ptr(saved.top_index), _ptr(g_top), dlogits.data_ptr(),
+                                        ldd, _stream(stream)))
     return dlogits
 
 

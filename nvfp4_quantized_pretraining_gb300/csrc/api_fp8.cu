@@ -100,7 +100,7 @@ fp4_status fp4_fp8_gemm(const fp4_fp8_tensor* A, const fp4_fp8_tensor* B, void* 
 }
 
 size_t fp4_fp8_linear_fwd_workspace(int64_t M, int64_t N, int64_t K) {
-  return M < 1 || N < 1 || K < 1 ? 0 : tensor_bytes(M, K);
+  return M < 1 || N < 1 || K < 1 || fp8_few(M, N, K) ? 0 : tensor_bytes(M, K);
 }
 size_t fp4_fp8_linear_bwd_workspace(int64_t M, int64_t N, int64_t K) {
   return M < 1 || N < 1 || K < 1 ? 0 : tensor_bytes(M, N) + tensor_bytes(N, M);
@@ -117,12 +117,12 @@ fp4_status fp4_fp8_linear_fwd(const void* X, int64_t M, int64_t K, int64_t ldx, 
   const int64_t N = Wq->rows;
   if ((st = check_shape(Wq, N, K, "Wq")) || (st = check_matrix(Y, M, N, ldy, 2, "Y"))) return st;
   if (xqT_saved && ((st = check_fp8(xqT_saved, "xqT_saved")) || (st = check_shape(xqT_saved, K, M, "xqT_saved")))) return st;
-  if ((st = check_ws(ws, ws_bytes, fp4_fp8_linear_fwd_workspace(M, N, K)))) return st;
   if (fp8_few(M, N, K)) {  // (the column form, if wanted, by a launch of its own)
     if (xqT_saved && (st = quantize(X, M, K, ldx, false, nullptr, xqT_saved, s))) return st;
     CUDA_TRY(launch_fp8_few(X, M, K, ldx, Wq->codes, Wq->scales, N, Y, ldy, sm_count(), s));
     return FP4_OK;
   }
+  if ((st = check_ws(ws, ws_bytes, fp4_fp8_linear_fwd_workspace(M, N, K)))) return st;
   uint8_t* at = static_cast<uint8_t*>(ws);
   const fp4_fp8_tensor xq = take(at, M, K);
   if ((st = quantize(X, M, K, ldx, false, &xq, xqT_saved, s))) return st;

@@ -344,7 +344,8 @@ def test_refusals(F):
     f = lambda *a: L.fp4_fp8_linear_fwd(*a, None)  # noqa: E731
     assert f(p, 4, 8, 8, t(16, 9), p, 16, None, p, 1 << 20) == bad
     assert f(p, 4, 8, 8, t(16, 8), p, 16, t(4, 8), p, 1 << 20) == bad
-    assert f(p, 4, 8, 8, t(16, 8), p, 16, None, p, 16) == ws and f(p, 4, 8, 8, t(16, 8), p, 16, None, p + 8, 1 << 20) == ws
+    assert f(p, 40, 8, 8, t(16, 8), p, 16, None, p, 16) == ws and f(p, 40, 8, 8, t(16, 8), p, 16, None, p + 8, 1 << 20) == ws
+    assert F.fp8_linear_fwd_workspace(1, 16, 8) == 0  # a few tokens need none
     assert f(p, -1, 8, 8, t(16, 8), p, 16, None, p, 1 << 20) == bad
     assert f(p, 0, 8, 8, t(16, 8), p, 16, None, None, 0) == F.FP4_OK
     b = lambda *a: L.fp4_fp8_linear_bwd(*a, None)  # noqa: E731

@@ -79,8 +79,9 @@ def check_forward(F, z, targets, temperature=1.0, top_k=0):
         near(r.stats[:, 1], w["S"], w["tS"] * w["S"], "sum")
         near(r.logprob, w["logprob"], d_ln + 2.0 ** -22 * np.abs(x_t), "logprob")
         near(r.entropy, w["H"], (2 + w["mean_x"]) * (w["tS"] + 2.0 ** -22) + 2.0 ** -23 * np.abs(w["ln_s"]), "entropy")
-        assert tuple(r.top_index.shape) == (T, top_k)
+        assert (r.top_index is None) == (top_k == 0)
         if top_k:
+            assert tuple(r.top_index.shape) == (T, top_k)
             assert np.array_equal(r.top_index.cpu().numpy(), w["order"])
             x_k = np.take_along_axis(w["x"], w["order"], 1)
             near(r.top_logprob, np.take_along_axis(w["lp"], w["order"], 1), d_ln[:, None] + 2.0 ** -22 * np.abs(x_k),
