@@ -370,7 +370,7 @@ fp4_status fp4_qadamw_v_decode(const fp4_tensor* in, const uint16_t* mean, float
  *           for 2^(b - 127) (UE8M0).  In the layout the tensor core reads: 128-row x 4-block atoms of
  *           512 bytes, ordered by 128-row block, then by group of 4 blocks; inside an atom byte
  *           (r % 32) * 16 + ((r % 128) / 32) * 4 + k % 4.  Padding bytes are zero.
- * Both device pointers, 16-byte aligned.  A block's scale is the least power of two (not below
+ * Device pointers, codes 32-byte and scales 16-byte aligned.  A block's scale is the least power of two (not below
  * 2^-127) with which its largest finite magnitude is at most 448; code = E4M3_rn(x / scale), exact
  * but for that one rounding.  Inf and NaN become NaN and take no part in the scale. */
 typedef struct {

@@ -11,8 +11,8 @@ constexpr int64_t kMaxRows = INT64_C(65535) * 128;  // a grid dimension of 128-r
 static fp4_status check_fp8(const fp4_fp8_tensor* t, const char* name) {
   if (!t) return fail(FP4_ERR_INVALID_ARG, "%s is NULL", name);
   if (!t->codes || !t->scales) return fail(FP4_ERR_INVALID_ARG, "%s has a NULL buffer", name);
-  if (!aligned16(t->codes) || !aligned16(t->scales))
-    return fail(FP4_ERR_MISALIGNED, "%s buffers must be 16-byte aligned", name);
+  if (!aligned_to(t->codes, 32) || !aligned16(t->scales))
+    return fail(FP4_ERR_MISALIGNED, "%s: codes must be 32-byte, scales 16-byte aligned", name);
   if (t->rows < 1 || t->cols < 1)
     return fail(FP4_ERR_INVALID_ARG, "%s is %lld x %lld", name, (long long)t->rows, (long long)t->cols);
   if (t->rows > kMaxRows || t->cols > kMaxRows || t->rows > (int64_t(1) << 38) / t->cols)

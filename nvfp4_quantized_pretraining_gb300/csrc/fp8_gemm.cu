@@ -72,6 +72,12 @@ __device__ __forceinline__ void mma_mxf8_pair(uint32_t d, uint64_t a, uint64_t b
       "l"(a), "l"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
       : "memory");
 }
+// True in one lane of a converged warp.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xFFFFFFFF;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(r));
+  return r != 0;
+}
 // 512 bytes (32 x 16) of each CTA's shared memory to 4 columns of its tensor memory, in every lane quadrant.
 __device__ __forceinline__ void tc_cp_sf_pair(uint32_t taddr, uint64_t sdesc) {
   asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(sdesc) : "memory");
@@ -122,6 +128,15 @@ __device__ __forceinline__ void store_direct(const Params& p, const uint32_t (&a
       if (col + i < p.Q) dst[i] = __float2bfloat16_rn(__uint_as_float(acc[i]));
   }
 }
+__device__ __forceinline__ uint4 pack8(const float (&v)[8]) {
+  uint32_t w[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const __nv_bfloat162 b = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
+    w[i] = *reinterpret_cast<const uint32_t*>(&b);
+  }
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
 // FP32 accumulators to packed BF16, and to a 32 x 32 chunk in shared memory: row = lane, 64 bytes; 16-byte unit u at
 // u ^ ((row >> 1) & 3) (64-byte swizzle).
 __device__ __forceinline__ void convert(const uint32_t (&a)[32], uint32_t (&pk)[16]) {
@@ -158,7 +173,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(xchg + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(0xFFFFFFFFu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   const uint32_t cta = cluster_ctarank(), rank = cta & 1, pair = cta >> 1;  // in the cluster; in the pair
   const bool leader = rank == 0;
   if (threadIdx.x == 0) {
@@ -199,25 +214,28 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
   const uint32_t quad = warp & 3, h = (uint32_t)(warp - FIRST_EPI_WARP) >> 2;
   const uint32_t lane_off = (quad * 32) << 16;
 
+  // The producer and the issuer keep their warps whole and elect a lane for each instruction: in a branch that only one
+  // lane takes, the operands of TMA and MMA instructions are not known to be uniform, and moving them took longer than
+  // the tensor core (344 ns a stage, whatever BN).
   if (warp == 0) {
-    if (lane == 0) {
-      // ---------------- TMA producer (both CTAs; completion on the leader's barrier) ----------------
-      const uint32_t full0 = mapa_shared(smem_u32(&full[0]), cta & ~1u);
-      uint32_t stage = 0, phase = 0;
-      bool ok = true;
-      for (uint32_t t = cluster_id; ok && t < num_tiles; t += num_clusters) {
-        uint32_t pb, qb;
-        tile_at(t, pb, qb);
-        for (uint32_t it = k0; it < k1; ++it) {
-          if (!mbar_wait(&empty[stage], phase ^ 1)) {
-            ok = false;
-            break;
-          }
-          uint8_t* sA = smem + stage * STAGE_BYTES;
-          uint8_t* sB = sA + A_BYTES;
-          uint8_t* sS = sB + B_BYTES;
-          const uint32_t full_l = full0 + stage * 8;
-          const bool sf = it % kSfGroup == 0 || it == k0;
+    // ---------------- TMA producer (both CTAs; completion on the leader's barrier) ----------------
+    const uint32_t full0 = mapa_shared(smem_u32(&full[0]), cta & ~1u);
+    uint32_t stage = 0, phase = 0;
+    bool ok = true;
+    for (uint32_t t = cluster_id; ok && t < num_tiles; t += num_clusters) {
+      uint32_t pb, qb;
+      tile_at(t, pb, qb);
+      for (uint32_t it = k0; it < k1; ++it) {
+        if (!mbar_wait_warp(&empty[stage], phase ^ 1)) {
+          ok = false;
+          break;
+        }
+        uint8_t* sA = smem + stage * STAGE_BYTES;
+        uint8_t* sB = sA + A_BYTES;
+        uint8_t* sS = sB + B_BYTES;
+        const uint32_t full_l = full0 + stage * 8;
+        const bool sf = it % kSfGroup == 0 || it == k0;
+        if (elect_one()) {
           if (leader) mbar_arrive_expect_tx(&full[stage], 2 * (A_BYTES + B_BYTES + (sf ? G::SF_BYTES : 0)));
           tma_load_2d_pair(sA, &tmap_a, full_l, (int32_t)(it * BK), (int32_t)(pb * 256 + rank * 128));
           tma_load_2d_pair(sB, &tmap_b, full_l, (int32_t)(it * BK), (int32_t)(qb * BN + rank * (BN / 2)));
@@ -226,13 +244,14 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
             tma_load_2d_pair(sS, &tmap_sa, full_l, x, (int32_t)(pb * 2 + rank));
             tma_load_2d_pair(sS + SF_ATOM, &tmap_sb, full_l, x, (int32_t)(qb * BN / 128));
           }
-          if (++stage == STAGES) stage = 0, phase ^= 1;
         }
+        __syncwarp();
+        if (++stage == STAGES) stage = 0, phase ^= 1;
       }
-      if (!ok) *abort_flag = 1;
     }
+    if (!ok) *abort_flag = 1;
   } else if (warp == 1) {
-    if (lane == 0 && leader) {
+    if (leader) {
       // ---------------- MMA issuer ----------------
       const uint64_t adesc0 = smem_desc(smem_u32(smem), 16, 1024, kSwizzle128B);
       const uint64_t bdesc0 = adesc0 + (A_BYTES >> 4);
@@ -241,38 +260,41 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       uint32_t stage = 0, phase = 0, slot = 0, n = 0;
       bool ok = true;
       for (uint32_t t = cluster_id; ok && t < num_tiles; t += num_clusters, ++n) {
-        if (*abort_flag || !mbar_wait(acc_empty, (n & 1) ^ 1)) { ok = false; break; }
+        if (*abort_flag || !mbar_wait_warp(acc_empty, (n & 1) ^ 1)) { ok = false; break; }
         tc_fence_after();
         for (uint32_t it = k0; it < k1; ++it) {
-          if (!mbar_wait(&full[stage], phase)) {
+          if (!mbar_wait_warp(&full[stage], phase)) {
             ok = false;
             break;
           }
           tc_fence_after();
-          if (it % kSfGroup == 0 || it == k0) {
-            slot ^= 1;
-            const uint32_t sf = tmem + TM_SF + slot * TM_SF_SLOT;
-            const uint64_t sd = sdesc0 + stage * kStageD;
-            tc_cp_sf_pair(sf, sd);
-#pragma unroll
-            for (int i = 0; i < G::SFB_ATOMS; ++i) tc_cp_sf_pair(sf + 8 + 4 * i, sd + ((1 + i) * SF_ATOM >> 4));
-          }
+          const bool sf_new = it % kSfGroup == 0 || it == k0;
+          if (sf_new) slot ^= 1;
           const uint32_t sfa = tmem + TM_SF + slot * TM_SF_SLOT, sfb = sfa + 8;
           const uint32_t idesc = idesc_mxf8(256, BN) | idesc_sf(it % kSfGroup);
           const uint64_t ad = adesc0 + stage * kStageD, bd = bdesc0 + stage * kStageD;
-          mma_mxf8_pair(tmem + TM_ACC, ad, bd, idesc, sfa, sfb, it != k0);
-          mma_mxf8_pair(tmem + TM_ACC, ad + 2, bd + 2, idesc, sfa, sfb, 1);
-          mma_mxf8_pair(tmem + TM_ACC, ad + 4, bd + 4, idesc, sfa, sfb, 1);
-          mma_mxf8_pair(tmem + TM_ACC, ad + 6, bd + 6, idesc, sfa, sfb, 1);
-          tc_commit_pair_mc(&empty[stage], both);
+          if (elect_one()) {
+            if (sf_new) {
+              const uint64_t sd = sdesc0 + stage * kStageD;
+              tc_cp_sf_pair(sfa, sd);
+#pragma unroll
+              for (int i = 0; i < G::SFB_ATOMS; ++i) tc_cp_sf_pair(sfb + 4 * i, sd + ((1 + i) * SF_ATOM >> 4));
+            }
+            mma_mxf8_pair(tmem + TM_ACC, ad, bd, idesc, sfa, sfb, it != k0);
+            mma_mxf8_pair(tmem + TM_ACC, ad + 2, bd + 2, idesc, sfa, sfb, 1);
+            mma_mxf8_pair(tmem + TM_ACC, ad + 4, bd + 4, idesc, sfa, sfb, 1);
+            mma_mxf8_pair(tmem + TM_ACC, ad + 6, bd + 6, idesc, sfa, sfb, 1);
+            tc_commit_pair_mc(&empty[stage], both);
+            if (it == k1 - 1) tc_commit_pair_mc(acc_full, both);
+          }
+          __syncwarp();
           if (++stage == STAGES) stage = 0, phase ^= 1;
         }
-        if (!ok) break;
-        tc_commit_pair_mc(acc_full, both);
       }
       if (!ok) *abort_flag = 1;
-      tc_commit_pair_mc(done_bar, own);
-      mbar_wait(done_bar, 0);
+      if (elect_one()) tc_commit_pair_mc(done_bar, own);
+      __syncwarp();
+      mbar_wait_warp(done_bar, 0);
     }
   } else {
     // ---------------- epilogue (both CTAs) ----------------
@@ -338,6 +360,32 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
           if (lane == 0) {
             store(buf0, col0 + 64);
             store(buf1, col0 + 96);
+            bulk_commit_group();
+          }
+          continue;
+        }
+      }
+      if constexpr (BN == 128 && !SWAP) {
+        if (p.tma_store) {
+          uint32_t ra[32], rb[32], pk[16];
+          if (lane == 0) bulk_wait_read<0>();  // the previous tile's stores have read both buffers
+          __syncwarp();
+          tmem_ld_32x32b_x32(tacc, ra);
+          tmem_ld_wait(ra);
+          tmem_ld_32x32b_x32(tacc + 32, rb);
+          convert(ra, pk);
+          stage_chunk(buf0, pk, lane);
+          tmem_ld_wait(rb);
+          release();
+          convert(rb, pk);
+          stage_chunk(buf1, pk, lane);
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) {
+            if (row0 < p.P) {
+              if (col0 < p.Q) tma_store_2d(&tmap_c, buf0, (int32_t)col0, (int32_t)row0);
+              if (col0 + 32 < p.Q) tma_store_2d(&tmap_c, buf1, (int32_t)(col0 + 32), (int32_t)row0);
+            }
             bulk_commit_group();
           }
           continue;
@@ -421,20 +469,24 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
               if (lane == 0) bulk_wait_read<0>();
               __syncwarp();
             }
-            uint4 o;
-            uint32_t* w = reinterpret_cast<uint32_t*>(&o);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const __nv_bfloat162 b = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
-              w[i] = *reinterpret_cast<const uint32_t*>(&b);
-            }
-            *reinterpret_cast<uint4*>(buf + lane * 64 + (((n & 3) ^ ((lane >> 1) & 3)) << 4)) = o;
+            *reinterpret_cast<uint4*>(buf + lane * 64 + (((n & 3) ^ ((lane >> 1) & 3)) << 4)) = pack8(v);
             if ((n & 3) == 3) {
               fence_proxy_async_smem();
               __syncwarp();
               if (lane == 0) {
                 if (col - 24 < p.Q && row0 < p.P) tma_store_2d(&tmap_c, buf, (int32_t)(col - 24), (int32_t)row0);
                 bulk_commit_group();
+              }
+            }
+          } else if (!SWAP && p.vec && col + 8 <= p.Q) {
+            if (row0 + lane < p.P) {
+              const size_t at = (size_t)(row0 + lane) * p.ldc + col;
+              if (p.c_f32) {
+                float4* dst = reinterpret_cast<float4*>(static_cast<float*>(p.C) + at);
+                dst[0] = make_float4(v[0], v[1], v[2], v[3]);
+                dst[1] = make_float4(v[4], v[5], v[6], v[7]);
+              } else {
+                *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.C) + at) = pack8(v);
               }
             }
           } else {
@@ -472,8 +524,32 @@ struct Operand {
   const void *codes, *scales;
   int64_t rows;
 };
+// The cycles that P x Q x K takes with tiles of 256 x BN and each tile's K shared by S pairs: rounds of tiles, or, split,
+// one round and the exchange of partial tiles.  Stage and fixed costs as measured (8192^3, and 256 x 8192 x 8192 by
+// phases); they serve to choose among tiles, nothing else.
+template <int BN>
+struct Plan {
+  static double cycles(int64_t P, int64_t Q, uint32_t num_k, uint32_t S, uint32_t pairs) {
+    const int64_t tiles = (P + 255) / 256 * ((Q + BN - 1) / BN);
+    constexpr double kStage = BN == 256 ? 770 : BN == 128 ? 420 : 320, kTile = BN == 256 ? 2500 : 1800;
+    constexpr double kExchange = BN == 256 ? 11000 : BN == 128 ? 6000 : 4000;
+    if (S == 1) return double((tiles + pairs - 1) / pairs) * (num_k * kStage + kTile);
+    if (tiles * S > pairs || S > Cfg<BN>::MAX_SPLIT) return 1e30;
+    return (num_k + S - 1) / S * kStage + kExchange + 700 * (S - 2);
+  }
+  static uint32_t split(int64_t P, int64_t Q, uint32_t num_k, uint32_t pairs, double& least) {
+    uint32_t best = 1;
+    least = cycles(P, Q, num_k, 1, pairs);
+    for (uint32_t S = 2; S <= 4 && S <= num_k; S *= 2) {
+      const double c = cycles(P, Q, num_k, S, pairs);
+      if (c < least) best = S, least = c;
+    }
+    return best;
+  }
+};
 template <int BN, bool SWAP>
-static cudaError_t launch(const Operand& P, const Operand& Q, const Fp8GemmArgs& g, int num_sms, cudaStream_t s) {
+static cudaError_t launch(const Operand& P, const Operand& Q, const Fp8GemmArgs& g, uint32_t split, int num_sms,
+                          cudaStream_t s) {
   using G = Cfg<BN>;
   auto kernel = gemm_pair_kernel<BN, SWAP>;
   static const cudaError_t attr = [&] {
@@ -511,12 +587,7 @@ static cudaError_t launch(const Operand& P, const Operand& Q, const Fp8GemmArgs&
   } else {
     tc = ta;
   }
-  // Pairs left without a tile share the others' K, while a share keeps at least kMinShare stages: exchanging the
-  // partial tile takes as long as some 14 stages (11000 cycles of 770 with BN = 256, 6000 of 450 with 128).
-  constexpr uint32_t kMinShare = 10;
-  const uint32_t tiles = p.tiles_p * p.tiles_q, pairs = (uint32_t)num_sms / 2;
-  uint32_t S = 1;
-  while (S < G::MAX_SPLIT && tiles * S * 2 <= pairs && p.num_k >= 2 * S * kMinShare) S *= 2;
+  const uint32_t tiles = p.tiles_p * p.tiles_q, pairs = (uint32_t)num_sms / 2, S = split;
   p.split = S;
   const uint32_t clusters = tiles < pairs ? tiles : pairs;
   cudaLaunchConfig_t cfg = {};
@@ -542,10 +613,14 @@ static cudaError_t launch(const Operand& P, const Operand& Q, const Fp8GemmArgs&
 }  // namespace f8
 
 cudaError_t launch_fp8_gemm(const Fp8GemmArgs& g, int num_sms, cudaStream_t s) {
-  const f8::Operand A{g.a_codes, g.a_scales, g.M}, B{g.b_codes, g.b_scales, g.N};
-  if (g.M <= 64) return f8::launch<64, true>(B, A, g, num_sms, s);
-  if (g.M <= 128) return f8::launch<128, true>(B, A, g, num_sms, s);
-  return f8::launch<256, false>(A, B, g, num_sms, s);
+  using namespace f8;
+  const Operand A{g.a_codes, g.a_scales, g.M}, B{g.b_codes, g.b_scales, g.N};
+  const uint32_t num_k = (uint32_t)(fp8_pitch(g.K) / BK), pairs = (uint32_t)num_sms / 2;
+  double c256, c128;
+  if (g.M <= 64) return launch<64, true>(B, A, g, Plan<64>::split(g.N, g.M, num_k, pairs, c128), num_sms, s);
+  if (g.M <= 128) return launch<128, true>(B, A, g, Plan<128>::split(g.N, g.M, num_k, pairs, c128), num_sms, s);
+  const uint32_t s256 = Plan<256>::split(g.M, g.N, num_k, pairs, c256), s128 = Plan<128>::split(g.M, g.N, num_k, pairs, c128);
+  return c128 < c256 ? launch<128, false>(A, B, g, s128, num_sms, s) : launch<256, false>(A, B, g, s256, num_sms, s);
 }
 
 cudaError_t fp8_status_read_clear(unsigned int* out, cudaStream_t s) {

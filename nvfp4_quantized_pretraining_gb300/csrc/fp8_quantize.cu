@@ -63,6 +63,13 @@ __device__ __forceinline__ uint32_t largest(const uint4& v) {
 __device__ __forceinline__ uint32_t largest_finite(const uint4& v) {
   return max_u16x2(max_u16x2(finite_only(v.x), finite_only(v.y)), max_u16x2(finite_only(v.z), finite_only(v.w)));
 }
+// One 32-byte store (two of 16 left half sectors for L2 to merge: the column form took 168 us instead of 144 at
+// 8192 x 32000).
+__device__ __forceinline__ void store32(uint8_t* p, const uint32_t (&v)[8]) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(v[0]), "r"(v[1]), "r"(v[2]),
+               "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+               : "memory");
+}
 // The 256 converting threads' barrier.
 __device__ __forceinline__ void sync256() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
 
@@ -181,13 +188,11 @@ __device__ __forceinline__ void convert_tile(const uint4* tile, uint32_t* s_max,
     const uint32_t col = kb * 128 + pair * 2;
     uint8_t* p = static_cast<uint8_t*>(c.codes) + (size_t)col * c.pitch + rb * 128 + group * 32;
     if (col < t.cols) {
-      reinterpret_cast<uint4*>(p)[0] = make_uint4(o0[0], o0[1], o0[2], o0[3]);
-      reinterpret_cast<uint4*>(p)[1] = make_uint4(o0[4], o0[5], o0[6], o0[7]);
+      store32(p, o0);
     }
     if (col + 1 < t.cols) {
       p += c.pitch;
-      reinterpret_cast<uint4*>(p)[0] = make_uint4(o1[0], o1[1], o1[2], o1[3]);
-      reinterpret_cast<uint4*>(p)[1] = make_uint4(o1[4], o1[5], o1[6], o1[7]);
+      store32(p, o1);
     }
     if (group == 0) {
       scales[sf_offset(col, rb, col_atoms)] = static_cast<uint8_t>(col < t.cols ? b0 : 0);

@@ -335,7 +335,7 @@ def test_refusals(F):
     assert q(p, 4, 8, 8, 64, t(4, 8), None) == bad
     assert q(p, 4, 8, 8, 1, None, None) == bad
     assert q(p, 4, 8, 8, 1, t(8, 4), None) == bad and q(p, 4, 8, 8, 1, None, t(4, 8)) == bad
-    assert q(p, 4, 8, 8, 1, t(4, 8, codes=p + 8), None) == mis and q(p, 4, 8, 8, 1, t(4, 8, scales=None), None) == bad
+    assert q(p, 4, 8, 8, 1, t(4, 8, codes=p + 16), None) == mis and q(p, 4, 8, 8, 1, t(4, 8, scales=None), None) == bad
     assert q(p, 1 << 24, 8, 8, 1, t(1 << 24, 8), None) == shape
     g = lambda *a: L.fp4_fp8_gemm(*a, None)  # noqa: E731
     assert g(None, t(4, 8), p, 0, 4) == bad and g(t(4, 8), t(4, 9), p, 0, 4) == bad

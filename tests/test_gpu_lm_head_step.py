@@ -1,0 +1,64 @@
+"""The example that runs the FP8 head, the log probabilities and the AdamW step together: one step against the same step in
+64 bits on the quantized operands, and a short training run."""
+import importlib.util
+import os
+
+import numpy as np
+import pytest
+import torch
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+DEV = "cuda"
+
+
+@pytest.fixture(scope="module")
+def X():
+    import __graft_entry__
+    __graft_entry__.build()
+    spec = importlib.util.spec_from_file_location("lm_head_step", os.path.join(ROOT, "examples", "lm_head_step.py"))
+    m = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(m)
+    return m
+
+
+@pytest.mark.gpu
+def test_one_step_against_64_bits(X):
+    # the operators round to E4M3 (2^-4 relative) once per operand and to BF16 (2^-9): an entry of a product of K
+    # such terms with independent errors is off by about 2^-4 of the norm of its terms, so 0.1 in relative norm bounds
+    # the logits and, with dlogits' own rounding beside it, both gradients
+    T, D, V = 300, 512, 1003
+    g = torch.Generator(device=DEV).manual_seed(3)
+    head = X.Head(V, D, g)
+    w = head.model.double().cpu().numpy()
+    hidden = torch.randn((T, D), device=DEV, generator=g).bfloat16()
+    targets = torch.randint(0, V, (T,), device=DEV, generator=g)
+    targets[::9] = -100
+    h, t = hidden.double().cpu().numpy(), targets.cpu().numpy()
+    z = h @ w.T
+    p = np.exp(z - z.max(1, keepdims=True))
+    p /= p.sum(1, keepdims=True)
+    valid = t >= 0
+    want_loss = -np.log(p[np.arange(T), np.maximum(t, 0)])[valid].mean()
+    d = p.copy()
+    d[np.arange(T), np.maximum(t, 0)] -= 1
+    d[~valid] = 0
+    d /= valid.sum()
+    want_dh, want_dw = d @ w, d.T @ h
+    before = head.master.clone()
+    loss, dh = head.train(hidden, targets, 1, 1e-2)
+    torch.cuda.synchronize()
+    X.F.fp4_check_status()
+    rel = lambda a, b: np.linalg.norm(a.double().cpu().numpy() - b) / np.linalg.norm(b)  # noqa: E731
+    assert abs(float(loss) - want_loss) < 0.02 * want_loss
+    assert rel(dh, want_dh) < 0.1 and rel(head.grad, want_dw) < 0.1
+    # the first step moves every weight with a gradient by about lr against its sign
+    moved = (head.master - before * (1 - 1e-2 * 0.01)).cpu().numpy()
+    big = np.abs(want_dw) > 0.2 * np.abs(want_dw).mean()
+    assert (np.sign(moved[big]) == -np.sign(want_dw[big])).mean() > 0.95
+    assert torch.equal(head.model, head.master.bfloat16())
+
+
+@pytest.mark.gpu
+def test_the_example_learns_and_answers(X):
+    losses, right = X.run(tokens=1024, width=512, vocab=2001, steps=12, log=lambda *a: None)
+    assert losses[-1] < 0.2 * losses[0] and right >= 14
