@@ -54,7 +54,7 @@ static fp4_fp8_tensor take(uint8_t*& at, int64_t rows, int64_t cols) {
 }
 static fp4_status gemm(const fp4_fp8_tensor& A, const fp4_fp8_tensor& B, void* C, int c_dtype, int64_t ldc, cudaStream_t s) {
   const Fp8GemmArgs g{A.codes, A.scales, B.codes, B.scales, A.rows, B.rows, A.cols, C, c_dtype == FP4_OUT_F32, ldc};
-  CUDA_TRY(launch_fp8_gemm(g, sm_count(), s));
+  CUDA_TRY(launch_fp8_gemm(g, s));
   return FP4_OK;
 }
 static fp4_status quantize(const void* x, int64_t rows, int64_t cols, int64_t ld, bool square, const fp4_fp8_tensor* row,

@@ -524,39 +524,68 @@ struct Operand {
   const void *codes, *scales;
   int64_t rows;
 };
-// The cycles that P x Q x K takes with tiles of 256 x BN and each tile's K shared by S pairs: rounds of tiles, or, split,
-// one round and the exchange of partial tiles.  Stage and fixed costs as measured (8192^3, and 256 x 8192 x 8192 by
-// phases); they serve to choose among tiles, nothing else.
-template <int BN>
+// What a kernel's launches need to know: how many clusters of 2 S CTAs the device holds at once (S = 1, 2, 4).
+struct Limits {
+  cudaError_t err;
+  uint32_t clusters[5];
+};
+template <int BN, bool SWAP>
+static const Limits& limits() {
+  static const Limits l = [] {
+    Limits m{};
+    auto kernel = gemm_pair_kernel<BN, SWAP>;
+    m.err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<BN>::SMEM_BYTES);
+    for (uint32_t S = 1; m.err == cudaSuccess && S <= 4; S *= 2) {
+      cudaLaunchConfig_t cfg = {};
+      cudaLaunchAttribute attr[1];
+      attr[0].id = cudaLaunchAttributeClusterDimension;
+      attr[0].val.clusterDim.x = 2 * S;
+      attr[0].val.clusterDim.y = 1;
+      attr[0].val.clusterDim.z = 1;
+      cfg.gridDim = dim3(2 * S);
+      cfg.blockDim = dim3(NUM_THREADS);
+      cfg.dynamicSmemBytes = Cfg<BN>::SMEM_BYTES;
+      cfg.attrs = attr;
+      cfg.numAttrs = 1;
+      int n = 0;
+      m.err = cudaOccupancyMaxActiveClusters(&n, kernel, &cfg);
+      m.clusters[S] = n > 0 ? n : 1;
+    }
+    return m;
+  }();
+  return l;
+}
+// The cycles of P x Q x K with tiles of 256 x BN and each tile's K shared by S pairs: rounds of tiles or, split, one
+// round and the exchange of partial tiles.  Costs as measured (211 ns a stage with BN = 64 and 128, 300 to 340 with 256
+// at 1.9 GHz; 256 x 2048 x 5632 in 17.4, 15.7 us with BN = 256, S = 1, 2 and 13.1, 11.6 with 128); they serve to choose
+// among tiles, nothing else.
+template <int BN, bool SWAP>
 struct Plan {
-  static double cycles(int64_t P, int64_t Q, uint32_t num_k, uint32_t S, uint32_t pairs) {
+  static double cycles(int64_t P, int64_t Q, uint32_t num_k, uint32_t S) {
     const int64_t tiles = (P + 255) / 256 * ((Q + BN - 1) / BN);
-    constexpr double kStage = BN == 256 ? 770 : BN == 128 ? 420 : 320, kTile = BN == 256 ? 2500 : 1800;
-    constexpr double kExchange = BN == 256 ? 11000 : BN == 128 ? 6000 : 4000;
-    if (S == 1) return double((tiles + pairs - 1) / pairs) * (num_k * kStage + kTile);
-    if (tiles * S > pairs || S > Cfg<BN>::MAX_SPLIT) return 1e30;
-    return (num_k + S - 1) / S * kStage + kExchange + 700 * (S - 2);
+    const uint32_t clusters = limits<BN, SWAP>().clusters[S];
+    constexpr double kStage = BN == 256 ? 600 : 400, kTile = BN == 256 ? 2500 : 1500;
+    constexpr double kExchange = BN == 256 ? 9000 : BN == 128 ? 6000 : 4000;
+    if (S == 1) return double((tiles + clusters - 1) / clusters) * (num_k * kStage + kTile);
+    if (tiles > clusters || S > Cfg<BN>::MAX_SPLIT || S > num_k) return 1e30;
+    return (num_k + S - 1) / S * kStage + kTile + kExchange + (S == 4 ? 700 : 0);
   }
-  static uint32_t split(int64_t P, int64_t Q, uint32_t num_k, uint32_t pairs, double& least) {
+  static uint32_t split(int64_t P, int64_t Q, uint32_t num_k, double& least) {
     uint32_t best = 1;
-    least = cycles(P, Q, num_k, 1, pairs);
-    for (uint32_t S = 2; S <= 4 && S <= num_k; S *= 2) {
-      const double c = cycles(P, Q, num_k, S, pairs);
+    least = cycles(P, Q, num_k, 1);
+    for (uint32_t S = 2; S <= 4; S *= 2) {
+      const double c = cycles(P, Q, num_k, S);
       if (c < least) best = S, least = c;
     }
     return best;
   }
 };
 template <int BN, bool SWAP>
-static cudaError_t launch(const Operand& P, const Operand& Q, const Fp8GemmArgs& g, uint32_t split, int num_sms,
-                          cudaStream_t s) {
+static cudaError_t launch(const Operand& P, const Operand& Q, const Fp8GemmArgs& g, uint32_t S, cudaStream_t s) {
   using G = Cfg<BN>;
   auto kernel = gemm_pair_kernel<BN, SWAP>;
-  static const cudaError_t attr = [&] {
-    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, G::SMEM_BYTES);
-    return e != cudaSuccess ? e : cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-  }();
-  if (attr != cudaSuccess) return attr;
+  const Limits& most = limits<BN, SWAP>();
+  if (most.err != cudaSuccess) return most.err;
   const uint64_t pitch = fp8_pitch(g.K), atoms = (g.K + 511) / 512;
   CUtensorMap ta, tb, tsa, tsb, tc;
   const auto u8 = CU_TENSOR_MAP_DATA_TYPE_UINT8, u64 = CU_TENSOR_MAP_DATA_TYPE_UINT64;
@@ -587,9 +616,9 @@ static cudaError_t launch(const Operand& P, const Operand& Q, const Fp8GemmArgs&
   } else {
     tc = ta;
   }
-  const uint32_t tiles = p.tiles_p * p.tiles_q, pairs = (uint32_t)num_sms / 2, S = split;
   p.split = S;
-  const uint32_t clusters = tiles < pairs ? tiles : pairs;
+  const uint32_t tiles = p.tiles_p * p.tiles_q;
+  const uint32_t clusters = tiles < most.clusters[S] ? tiles : most.clusters[S];
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(clusters * 2 * S);
   cfg.blockDim = dim3(NUM_THREADS);
@@ -612,15 +641,16 @@ static cudaError_t launch(const Operand& P, const Operand& Q, const Fp8GemmArgs&
 
 }  // namespace f8
 
-cudaError_t launch_fp8_gemm(const Fp8GemmArgs& g, int num_sms, cudaStream_t s) {
+cudaError_t launch_fp8_gemm(const Fp8GemmArgs& g, cudaStream_t s) {
   using namespace f8;
   const Operand A{g.a_codes, g.a_scales, g.M}, B{g.b_codes, g.b_scales, g.N};
-  const uint32_t num_k = (uint32_t)(fp8_pitch(g.K) / BK), pairs = (uint32_t)num_sms / 2;
+  const uint32_t num_k = (uint32_t)(fp8_pitch(g.K) / BK);
   double c256, c128;
-  if (g.M <= 64) return launch<64, true>(B, A, g, Plan<64>::split(g.N, g.M, num_k, pairs, c128), num_sms, s);
-  if (g.M <= 128) return launch<128, true>(B, A, g, Plan<128>::split(g.N, g.M, num_k, pairs, c128), num_sms, s);
-  const uint32_t s256 = Plan<256>::split(g.M, g.N, num_k, pairs, c256), s128 = Plan<128>::split(g.M, g.N, num_k, pairs, c128);
-  return c128 < c256 ? launch<128, false>(A, B, g, s128, num_sms, s) : launch<256, false>(A, B, g, s256, num_sms, s);
+  if (g.M <= 64) return launch<64, true>(B, A, g, Plan<64, true>::split(g.N, g.M, num_k, c128), s);
+  if (g.M <= 128) return launch<128, true>(B, A, g, Plan<128, true>::split(g.N, g.M, num_k, c128), s);
+  const uint32_t s256 = Plan<256, false>::split(g.M, g.N, num_k, c256);
+  const uint32_t s128 = Plan<128, false>::split(g.M, g.N, num_k, c128);
+  return c128 < c256 ? launch<128, false>(A, B, g, s128, s) : launch<256, false>(A, B, g, s256, s);
 }
 
 cudaError_t fp8_status_read_clear(unsigned int* out, cudaStream_t s) {

@@ -244,7 +244,7 @@ struct Fp8GemmArgs {
   int c_f32;
   int64_t ldc;
 };
-cudaError_t launch_fp8_gemm(const Fp8GemmArgs& g, int num_sms, cudaStream_t s);
+cudaError_t launch_fp8_gemm(const Fp8GemmArgs& g, cudaStream_t s);
 // Y (T x N BF16, pitch ldy) = X W^T for at most 16 tokens, X quantized on the way; fp8_few() says whether that beats a
 // quantizer and the GEMM: up to 8 tokens always (5632 x 2048: 5.0 against 10.4 us, 32000 x 2048: 14 against 19), to 16
 // while the weights are small (8.9 against 10.4 us, but 28 against 19).
