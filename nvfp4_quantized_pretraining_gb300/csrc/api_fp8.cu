@@ -52,9 +52,11 @@ static fp4_fp8_tensor take(uint8_t*& at, int64_t rows, int64_t cols) {
   at += tensor_bytes(rows, cols);
   return t;
 }
+static Fp8GemmArgs gemm_args(const fp4_fp8_tensor& A, const fp4_fp8_tensor& B, void* C, int c_dtype, int64_t ldc) {
+  return Fp8GemmArgs{A.codes, A.scales, B.codes, B.scales, A.rows, B.rows, A.cols, C, c_dtype == FP4_OUT_F32, ldc};
+}
 static fp4_status gemm(const fp4_fp8_tensor& A, const fp4_fp8_tensor& B, void* C, int c_dtype, int64_t ldc, cudaStream_t s) {
-  const Fp8GemmArgs g{A.codes, A.scales, B.codes, B.scales, A.rows, B.rows, A.cols, C, c_dtype == FP4_OUT_F32, ldc};
-  CUDA_TRY(launch_fp8_gemm(g, s));
+  CUDA_TRY(launch_fp8_gemm(gemm_args(A, B, C, c_dtype, ldc), s));
   return FP4_OK;
 }
 static fp4_status quantize(const void* x, int64_t rows, int64_t cols, int64_t ld, bool square, const fp4_fp8_tensor* row,
@@ -152,7 +154,11 @@ fp4_status fp4_fp8_linear_bwd(const void* dY, int64_t M, int64_t N, int64_t lddy
   uint8_t* at = static_cast<uint8_t*>(ws);
   const fp4_fp8_tensor dyq = take(at, M, N), dyqT = take(at, N, M);
   if ((st = quantize(dY, M, N, lddy, false, dX ? &dyq : nullptr, dW ? &dyqT : nullptr, s))) return st;
-  if (dX && (st = gemm(dyq, *WqT, dX, FP4_OUT_BF16, lddx, s))) return st;
+  if (dX && dW) {
+    CUDA_TRY(launch_fp8_gemm_two(gemm_args(dyq, *WqT, dX, FP4_OUT_BF16, lddx), gemm_args(dyqT, *xqT_saved, dW, dw_dtype, lddw), s));
+    return FP4_OK;
+  }
+  if (dX) return gemm(dyq, *WqT, dX, FP4_OUT_BF16, lddx, s);
   return dW ? gemm(dyqT, *xqT_saved, dW, dw_dtype, lddw, s) : FP4_OK;
 }
 

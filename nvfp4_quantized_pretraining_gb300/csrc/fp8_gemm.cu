@@ -48,15 +48,47 @@ struct Cfg {
   static_assert(STAGES * STAGE_BYTES >= 2 * (MAX_SPLIT - 1) * (BN / MAX_SPLIT) * 512, "a split tile's parts, sent and received");
 };
 
-struct Params {
+struct Problem {
   uint32_t P, Q, num_k, tiles_p, tiles_q;  // rows of the two sides
   uint32_t q_fastest;                      // tile order: the larger operand is walked slowest
-  uint32_t split;                          // S: pairs that share a tile
   void* C;
   int64_t ldc;
   int c_f32, tma_store;
   uint32_t vec;                            // C rows allow 16-byte stores
 };
+struct Maps {
+  CUtensorMap a, b, sa, sb, c;
+};
+struct Params {
+  Problem g[2];
+  Maps maps[2];
+  uint32_t split;   // S: pairs that share a tile (of the one problem)
+  uint32_t second;  // whether there are two problems
+  uint32_t lead;    // tiles of the second that the clusters with fewer of the first take ahead
+};
+
+// The i-th tile of cluster c of C.  Two problems: the first one's tiles go around the clusters; then the second one's,
+// with `lead` rounds first that leave out the clusters which had a tile more of the first.
+struct Tile {
+  uint32_t g, pb, qb;
+};
+__device__ __forceinline__ bool tile_of(const Params& p, uint32_t c, uint32_t C, uint32_t i, Tile& t) {
+  const uint32_t first = p.g[0].tiles_p * p.g[0].tiles_q;
+  uint32_t at = c + i * C;
+  t.g = 0;
+  if (at >= first) {
+    if (!p.second) return false;
+    const uint32_t rem = first % C, light = C - rem, had = first / C + (c < rem ? 1 : 0), j = i - had;
+    if (c < rem) at = p.lead * light + j * C + c;
+    else at = j < p.lead ? j * light + c - rem : p.lead * light + (j - p.lead) * C + c;
+    t.g = 1;
+    if (at >= p.g[1].tiles_p * p.g[1].tiles_q) return false;
+  }
+  const Problem& g = p.g[t.g];
+  t.pb = g.q_fastest ? at / g.tiles_q : at % g.tiles_p;
+  t.qb = g.q_fastest ? at % g.tiles_q : at / g.tiles_p;
+  return true;
+}
 
 // kind::mxf8f6f4: E4M3 x E4M3, UE8M0 scales, K-major operands; the scale byte's id is added per stage.
 __host__ __device__ constexpr uint32_t idesc_mxf8(uint32_t M, uint32_t N) {
@@ -95,7 +127,7 @@ __device__ __forceinline__ void tmem_ld_32x32b_x8(uint32_t taddr, uint32_t (&r)[
 // 32 columns (col.., accumulators of this lane's row) of the tile to C.  SWAP: tile rows are C's columns, and the 32
 // lanes of a column store 32 neighbours.
 template <bool SWAP>
-__device__ __forceinline__ void store_direct(const Params& p, const uint32_t (&acc)[32], uint32_t row, uint32_t col) {
+__device__ __forceinline__ void store_direct(const Problem& p, const uint32_t (&acc)[32], uint32_t row, uint32_t col) {
   if (SWAP) {
     if (row >= p.P) return;
 #pragma unroll
@@ -155,9 +187,7 @@ __device__ __forceinline__ void stage_chunk(uint8_t* chunk, const uint32_t (&pk)
 
 template <int BN, bool SWAP>
 __global__ void __launch_bounds__(NUM_THREADS, 1)
-    gemm_pair_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_constant__ CUtensorMap tmap_b,
-                     const __grid_constant__ CUtensorMap tmap_sa, const __grid_constant__ CUtensorMap tmap_sb,
-                     const __grid_constant__ CUtensorMap tmap_c, const Params p) {
+    gemm_pair_kernel(const __grid_constant__ Params p) {
   using G = Cfg<BN>;
   constexpr int STAGES = G::STAGES, STAGE_BYTES = G::STAGE_BYTES, B_BYTES = G::B_BYTES;
   pdl_trigger();
@@ -189,11 +219,13 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     fence_mbar_init();
   }
   if (warp == 0 && lane == 0) {
-    prefetch_tmap(&tmap_a);
-    prefetch_tmap(&tmap_b);
-    prefetch_tmap(&tmap_sa);
-    prefetch_tmap(&tmap_sb);
-    if (p.tma_store) prefetch_tmap(&tmap_c);
+    for (uint32_t i = 0; i <= p.second; ++i) {
+      prefetch_tmap(&p.maps[i].a);
+      prefetch_tmap(&p.maps[i].b);
+      prefetch_tmap(&p.maps[i].sa);
+      prefetch_tmap(&p.maps[i].sb);
+      if (p.g[i].tma_store) prefetch_tmap(&p.maps[i].c);
+    }
   }
   if (warp == 1) tmem_alloc_pair(tmem_slot, TM_COLS);
   tc_fence_before();
@@ -203,13 +235,9 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
   pdl_wait();  // (the set-up above touches no global data)
 
   const uint32_t S = p.split, cluster_id = blockIdx.x / (2 * S), num_clusters = gridDim.x / (2 * S);
-  const uint32_t num_tiles = p.tiles_p * p.tiles_q;
-  const uint32_t k0 = pair * p.num_k / S, k1 = (pair + 1) * p.num_k / S;  // this pair's stages of K
   const uint16_t both = static_cast<uint16_t>(3u << (2 * pair)), own = static_cast<uint16_t>(1u << (2 * pair));
-  auto tile_at = [&](uint32_t t, uint32_t& pb, uint32_t& qb) {
-    pb = p.q_fastest ? t / p.tiles_q : t % p.tiles_p;
-    qb = p.q_fastest ? t % p.tiles_q : t / p.tiles_p;
-  };
+  // this pair's stages of K
+  auto k_from = [&](const Problem& g, uint32_t i) { return i * g.num_k / S; };
   // warp w's part of the epilogue: TMEM lane quadrant w % 4 (32 of this CTA's rows), half the columns
   const uint32_t quad = warp & 3, h = (uint32_t)(warp - FIRST_EPI_WARP) >> 2;
   const uint32_t lane_off = (quad * 32) << 16;
@@ -222,9 +250,10 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     const uint32_t full0 = mapa_shared(smem_u32(&full[0]), cta & ~1u);
     uint32_t stage = 0, phase = 0;
     bool ok = true;
-    for (uint32_t t = cluster_id; ok && t < num_tiles; t += num_clusters) {
-      uint32_t pb, qb;
-      tile_at(t, pb, qb);
+    Tile t;
+    for (uint32_t i = 0; ok && tile_of(p, cluster_id, num_clusters, i, t); ++i) {
+      const uint32_t pb = t.pb, qb = t.qb, k0 = k_from(p.g[t.g], pair), k1 = k_from(p.g[t.g], pair + 1);
+      const Maps& map = p.maps[t.g];
       for (uint32_t it = k0; it < k1; ++it) {
         if (!mbar_wait_warp(&empty[stage], phase ^ 1)) {
           ok = false;
@@ -237,12 +266,12 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         const bool sf = it % kSfGroup == 0 || it == k0;
         if (elect_one()) {
           if (leader) mbar_arrive_expect_tx(&full[stage], 2 * (A_BYTES + B_BYTES + (sf ? G::SF_BYTES : 0)));
-          tma_load_2d_pair(sA, &tmap_a, full_l, (int32_t)(it * BK), (int32_t)(pb * 256 + rank * 128));
-          tma_load_2d_pair(sB, &tmap_b, full_l, (int32_t)(it * BK), (int32_t)(qb * BN + rank * (BN / 2)));
+          tma_load_2d_pair(sA, &map.a, full_l, (int32_t)(it * BK), (int32_t)(pb * 256 + rank * 128));
+          tma_load_2d_pair(sB, &map.b, full_l, (int32_t)(it * BK), (int32_t)(qb * BN + rank * (BN / 2)));
           if (sf) {
             const int32_t x = (int32_t)(it / kSfGroup * 64);  // 8-byte units
-            tma_load_2d_pair(sS, &tmap_sa, full_l, x, (int32_t)(pb * 2 + rank));
-            tma_load_2d_pair(sS + SF_ATOM, &tmap_sb, full_l, x, (int32_t)(qb * BN / 128));
+            tma_load_2d_pair(sS, &map.sa, full_l, x, (int32_t)(pb * 2 + rank));
+            tma_load_2d_pair(sS + SF_ATOM, &map.sb, full_l, x, (int32_t)(qb * BN / 128));
           }
         }
         __syncwarp();
@@ -259,7 +288,9 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       constexpr uint64_t kStageD = STAGE_BYTES >> 4;
       uint32_t stage = 0, phase = 0, slot = 0, n = 0;
       bool ok = true;
-      for (uint32_t t = cluster_id; ok && t < num_tiles; t += num_clusters, ++n) {
+      Tile t;
+      for (; ok && tile_of(p, cluster_id, num_clusters, n, t); ++n) {
+        const uint32_t k0 = k_from(p.g[t.g], pair), k1 = k_from(p.g[t.g], pair + 1);
         if (*abort_flag || !mbar_wait_warp(acc_empty, (n & 1) ^ 1)) { ok = false; break; }
         tc_fence_after();
         for (uint32_t it = k0; it < k1; ++it) {
@@ -310,10 +341,11 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         else mbar_arrive_cluster_relaxed(acc_empty0);
       }
     };
-    uint32_t n = 0;
-    for (uint32_t t = cluster_id; t < num_tiles; t += num_clusters, ++n) {
-      uint32_t pb, qb;
-      tile_at(t, pb, qb);
+    Tile t;
+    for (uint32_t n = 0; tile_of(p, cluster_id, num_clusters, n, t); ++n) {
+      const Problem& g = p.g[t.g];
+      const CUtensorMap& tmap_c = p.maps[t.g].c;
+      const uint32_t pb = t.pb, qb = t.qb;
       if (*abort_flag || !mbar_wait_warp(acc_full, n & 1)) {
         *abort_flag = 1;
         break;
@@ -322,9 +354,9 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       if (S > 1) break;  // the partial tile is exchanged below
       const uint32_t row0 = pb * 256 + rank * 128 + quad * 32, col0 = qb * BN + h * (BN / 2);
       if constexpr (BN == 256 && !SWAP) {
-        if (p.tma_store) {
+        if (g.tma_store) {
           auto store = [&](const uint8_t* chunk, uint32_t col) {  // (clipped at the tensor's edges)
-            if (col < p.Q && row0 < p.P) tma_store_2d(&tmap_c, chunk, (int32_t)col, (int32_t)row0);
+            if (col < g.Q && row0 < g.P) tma_store_2d(&tmap_c, chunk, (int32_t)col, (int32_t)row0);
           };
           uint32_t ra[32], rb[32], pk[16], pk2[16], pk3[16];
           if (lane == 0) bulk_wait_read<0>();  // the previous tile's stores have read both buffers
@@ -366,7 +398,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         }
       }
       if constexpr (BN == 128 && !SWAP) {
-        if (p.tma_store) {
+        if (g.tma_store) {
           uint32_t ra[32], rb[32], pk[16];
           if (lane == 0) bulk_wait_read<0>();  // the previous tile's stores have read both buffers
           __syncwarp();
@@ -382,9 +414,9 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
           fence_proxy_async_smem();
           __syncwarp();
           if (lane == 0) {
-            if (row0 < p.P) {
-              if (col0 < p.Q) tma_store_2d(&tmap_c, buf0, (int32_t)col0, (int32_t)row0);
-              if (col0 + 32 < p.Q) tma_store_2d(&tmap_c, buf1, (int32_t)(col0 + 32), (int32_t)row0);
+            if (row0 < g.P) {
+              if (col0 < g.Q) tma_store_2d(&tmap_c, buf0, (int32_t)col0, (int32_t)row0);
+              if (col0 + 32 < g.Q) tma_store_2d(&tmap_c, buf1, (int32_t)(col0 + 32), (int32_t)row0);
             }
             bulk_commit_group();
           }
@@ -396,7 +428,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         uint32_t acc[32];
         tmem_ld_32x32b_x32(tacc + j * 32, acc);
         tmem_ld_wait(acc);
-        store_direct<SWAP>(p, acc, row0 + lane, col0 + j * 32);
+        store_direct<SWAP>(g, acc, row0 + lane, col0 + j * 32);
       }
       release();
     }
@@ -413,8 +445,11 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     const uint32_t part_bytes = width * 512, received = (S - 1) * part_bytes;
     float* send = reinterpret_cast<float*>(smem);
     const float* got = reinterpret_cast<const float*>(smem + received);
-    uint32_t pb, qb;
-    tile_at(cluster_id, pb, qb);
+    const Problem& g = p.g[0];
+    const CUtensorMap& tmap_c = p.maps[0].c;
+    Tile t;
+    tile_of(p, cluster_id, num_clusters, 0, t);
+    const uint32_t pb = t.pb, qb = t.qb;
     if (warp >= FIRST_EPI_WARP) {
       const bool works = *abort_flag == 0;
       tc_fence_after();
@@ -448,7 +483,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         const uint32_t row0 = pb * 256 + rank * 128 + quad * 32, col0 = qb * BN + pair * width;
         uint8_t* buf = s_out + (warp - FIRST_EPI_WARP) * 2 * CHUNK_BYTES;
         // units of 8 columns; with TMA stores, chunks of 32 of them (h's chunks), else every other unit
-        const bool chunks = !SWAP && p.tma_store && width >= 64;
+        const bool chunks = !SWAP && g.tma_store && width >= 64;
 #pragma unroll 1
         for (uint32_t n = 0; n < width / 16; ++n) {
           const uint32_t in = chunks ? h * (width / 2) + n * 8 : (2 * n + h) * 8, col = col0 + in;
@@ -474,28 +509,28 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
               fence_proxy_async_smem();
               __syncwarp();
               if (lane == 0) {
-                if (col - 24 < p.Q && row0 < p.P) tma_store_2d(&tmap_c, buf, (int32_t)(col - 24), (int32_t)row0);
+                if (col - 24 < g.Q && row0 < g.P) tma_store_2d(&tmap_c, buf, (int32_t)(col - 24), (int32_t)row0);
                 bulk_commit_group();
               }
             }
-          } else if (!SWAP && p.vec && col + 8 <= p.Q) {
-            if (row0 + lane < p.P) {
-              const size_t at = (size_t)(row0 + lane) * p.ldc + col;
-              if (p.c_f32) {
-                float4* dst = reinterpret_cast<float4*>(static_cast<float*>(p.C) + at);
+          } else if (!SWAP && g.vec && col + 8 <= g.Q) {
+            if (row0 + lane < g.P) {
+              const size_t at = (size_t)(row0 + lane) * g.ldc + col;
+              if (g.c_f32) {
+                float4* dst = reinterpret_cast<float4*>(static_cast<float*>(g.C) + at);
                 dst[0] = make_float4(v[0], v[1], v[2], v[3]);
                 dst[1] = make_float4(v[4], v[5], v[6], v[7]);
               } else {
-                *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.C) + at) = pack8(v);
+                *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(g.C) + at) = pack8(v);
               }
             }
           } else {
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
               const uint32_t m = SWAP ? col + i : row0 + lane, k = SWAP ? row0 + lane : col + i;  // C's row and column
-              if (row0 + lane < p.P && col + i < p.Q) {
-                if (p.c_f32) static_cast<float*>(p.C)[(size_t)m * p.ldc + k] = v[i];
-                else static_cast<__nv_bfloat16*>(p.C)[(size_t)m * p.ldc + k] = __float2bfloat16_rn(v[i]);
+              if (row0 + lane < g.P && col + i < g.Q) {
+                if (g.c_f32) static_cast<float*>(g.C)[(size_t)m * g.ldc + k] = v[i];
+                else static_cast<__nv_bfloat16*>(g.C)[(size_t)m * g.ldc + k] = __float2bfloat16_rn(v[i]);
               }
             }
           }
@@ -564,12 +599,12 @@ struct Plan {
   static double cycles(int64_t P, int64_t Q, uint32_t num_k, uint32_t S) {
     const int64_t tiles = (P + 255) / 256 * ((Q + BN - 1) / BN);
     const uint32_t clusters = limits<BN, SWAP>().clusters[S];
-    constexpr double kStage = BN == 256 ? 600 : 400, kTile = BN == 256 ? 2500 : 1500;
     constexpr double kExchange = BN == 256 ? 9000 : BN == 128 ? 6000 : 4000;
-    if (S == 1) return double((tiles + clusters - 1) / clusters) * (num_k * kStage + kTile);
+    if (S == 1) return double((tiles + clusters - 1) / clusters) * tile(num_k);
     if (tiles > clusters || S > Cfg<BN>::MAX_SPLIT || S > num_k) return 1e30;
-    return (num_k + S - 1) / S * kStage + kTile + kExchange + (S == 4 ? 700 : 0);
+    return tile((num_k + S - 1) / S) + kExchange + (S == 4 ? 700 : 0);
   }
+  static double tile(uint32_t num_k) { return num_k * (BN == 256 ? 600.0 : 400.0) + (BN == 256 ? 2500.0 : 1500.0); }
   static uint32_t split(int64_t P, int64_t Q, uint32_t num_k, double& least) {
     uint32_t best = 1;
     least = cycles(P, Q, num_k, 1);
@@ -580,63 +615,82 @@ struct Plan {
     return best;
   }
 };
+// Problem i of a launch: C = A B^T with P = A and Q = B, or the other way around (SWAP).
 template <int BN, bool SWAP>
-static cudaError_t launch(const Operand& P, const Operand& Q, const Fp8GemmArgs& g, uint32_t S, cudaStream_t s) {
+static bool set_problem(Params& p, int i, const Operand& P, const Operand& Q, const Fp8GemmArgs& a) {
   using G = Cfg<BN>;
-  auto kernel = gemm_pair_kernel<BN, SWAP>;
+  const uint64_t pitch = fp8_pitch(a.K), atoms = (a.K + 511) / 512;
+  Maps& m = p.maps[i];
+  Problem& g = p.g[i];
+  const auto u8 = CU_TENSOR_MAP_DATA_TYPE_UINT8, u64 = CU_TENSOR_MAP_DATA_TYPE_UINT64;
+  if (!encode_tmap_2d(&m.a, u8, P.codes, pitch, P.rows, pitch, BK, 128, CU_TENSOR_MAP_SWIZZLE_128B) ||
+      !encode_tmap_2d(&m.b, u8, Q.codes, pitch, Q.rows, pitch, BK, BN / 2, CU_TENSOR_MAP_SWIZZLE_128B) ||
+      !encode_tmap_2d(&m.sa, u64, P.scales, atoms * 64, (P.rows + 127) / 128, atoms * 512, 64, 1,
+                      CU_TENSOR_MAP_SWIZZLE_NONE) ||
+      !encode_tmap_2d(&m.sb, u64, Q.scales, atoms * 64, (Q.rows + 127) / 128, atoms * 512, 64, G::SFB_ATOMS,
+                      CU_TENSOR_MAP_SWIZZLE_NONE))
+    return false;
+  g.P = (uint32_t)P.rows;
+  g.Q = (uint32_t)Q.rows;
+  g.num_k = (uint32_t)(pitch / BK);
+  g.tiles_p = (g.P + 255) / 256;
+  g.tiles_q = (g.Q + BN - 1) / BN;
+  g.q_fastest = P.rows > Q.rows;
+  g.C = a.C;
+  g.ldc = a.ldc;
+  g.c_f32 = a.c_f32;
+  const bool aligned = (reinterpret_cast<uintptr_t>(a.C) & 15u) == 0 && (a.ldc * (a.c_f32 ? 4 : 2)) % 16 == 0;
+  g.vec = aligned;
+  g.tma_store = aligned && !a.c_f32 && !SWAP;
+  return !g.tma_store || encode_tmap_2d(&m.c, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, a.C, a.N, a.M, (uint64_t)a.ldc * 2, 32, 32,
+                                        CU_TENSOR_MAP_SWIZZLE_64B);
+}
+template <int BN, bool SWAP>
+static cudaError_t launch(const Params& p, cudaStream_t s) {
+  using G = Cfg<BN>;
   const Limits& most = limits<BN, SWAP>();
   if (most.err != cudaSuccess) return most.err;
-  const uint64_t pitch = fp8_pitch(g.K), atoms = (g.K + 511) / 512;
-  CUtensorMap ta, tb, tsa, tsb, tc;
-  const auto u8 = CU_TENSOR_MAP_DATA_TYPE_UINT8, u64 = CU_TENSOR_MAP_DATA_TYPE_UINT64;
-  if (!encode_tmap_2d(&ta, u8, P.codes, pitch, P.rows, pitch, BK, 128, CU_TENSOR_MAP_SWIZZLE_128B) ||
-      !encode_tmap_2d(&tb, u8, Q.codes, pitch, Q.rows, pitch, BK, BN / 2, CU_TENSOR_MAP_SWIZZLE_128B) ||
-      !encode_tmap_2d(&tsa, u64, P.scales, atoms * 64, (P.rows + 127) / 128, atoms * 512, 64, 1,
-                      CU_TENSOR_MAP_SWIZZLE_NONE) ||
-      !encode_tmap_2d(&tsb, u64, Q.scales, atoms * 64, (Q.rows + 127) / 128, atoms * 512, 64, G::SFB_ATOMS,
-                      CU_TENSOR_MAP_SWIZZLE_NONE))
-    return cudaErrorInvalidValue;
-  Params p{};
-  p.P = (uint32_t)P.rows;
-  p.Q = (uint32_t)Q.rows;
-  p.num_k = (uint32_t)(pitch / BK);
-  p.tiles_p = (p.P + 255) / 256;
-  p.tiles_q = (p.Q + BN - 1) / BN;
-  p.q_fastest = P.rows > Q.rows;
-  p.C = g.C;
-  p.ldc = g.ldc;
-  p.c_f32 = g.c_f32;
-  const bool aligned = (reinterpret_cast<uintptr_t>(g.C) & 15u) == 0 && (g.ldc * (g.c_f32 ? 4 : 2)) % 16 == 0;
-  p.vec = aligned;
-  p.tma_store = aligned && !g.c_f32 && !SWAP;
-  if (p.tma_store) {
-    if (!encode_tmap_2d(&tc, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, g.C, g.N, g.M, (uint64_t)g.ldc * 2, 32, 32,
-                        CU_TENSOR_MAP_SWIZZLE_64B))
-      return cudaErrorInvalidValue;
-  } else {
-    tc = ta;
-  }
-  p.split = S;
-  const uint32_t tiles = p.tiles_p * p.tiles_q;
-  const uint32_t clusters = tiles < most.clusters[S] ? tiles : most.clusters[S];
+  const uint32_t tiles = p.g[0].tiles_p * p.g[0].tiles_q + (p.second ? p.g[1].tiles_p * p.g[1].tiles_q : 0);
+  const uint32_t clusters = tiles < most.clusters[p.split] ? tiles : most.clusters[p.split];
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(clusters * 2 * S);
+  cfg.gridDim = dim3(clusters * 2 * p.split);
   cfg.blockDim = dim3(NUM_THREADS);
   cfg.dynamicSmemBytes = G::SMEM_BYTES;
   cfg.stream = s;
   cudaLaunchAttribute attrs[2];
   attrs[0].id = cudaLaunchAttributeClusterDimension;
-  attrs[0].val.clusterDim.x = 2 * S;
+  attrs[0].val.clusterDim.x = 2 * p.split;
   attrs[0].val.clusterDim.y = 1;
   attrs[0].val.clusterDim.z = 1;
   attrs[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attrs[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attrs;
   cfg.numAttrs = g_pdl_chain ? 2 : 1;
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, ta, tb, tsa, tsb, tc, p);
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, gemm_pair_kernel<BN, SWAP>, p);
   g_pdl_chain = e == cudaSuccess;
   count_launch();
   return e;
+}
+template <int BN, bool SWAP>
+static cudaError_t launch_one(const Operand& P, const Operand& Q, const Fp8GemmArgs& a, uint32_t S, cudaStream_t s) {
+  Params p{};
+  p.split = S;
+  if (!set_problem<BN, SWAP>(p, 0, P, Q, a)) return cudaErrorInvalidValue;
+  return launch<BN, SWAP>(p, s);
+}
+// Two products in one launch: the second one's tiles fill the pairs that the first one's last round leaves idle.
+template <int BN>
+static cudaError_t launch_two(const Fp8GemmArgs& a, const Fp8GemmArgs& b, cudaStream_t s) {
+  Params p{};
+  p.split = 1;
+  p.second = 1;
+  if (!set_problem<BN, false>(p, 0, {a.a_codes, a.a_scales, a.M}, {a.b_codes, a.b_scales, a.N}, a) ||
+      !set_problem<BN, false>(p, 1, {b.a_codes, b.a_scales, b.M}, {b.b_codes, b.b_scales, b.N}, b))
+    return cudaErrorInvalidValue;
+  const uint32_t first = p.g[0].tiles_p * p.g[0].tiles_q, clusters = limits<BN, false>().clusters[1];
+  const double ratio = Plan<BN, false>::tile(p.g[0].num_k) / Plan<BN, false>::tile(p.g[1].num_k);
+  p.lead = first % clusters ? (uint32_t)(ratio + 0.5) : 0;
+  return launch<BN, false>(p, s);
 }
 
 }  // namespace f8
@@ -646,11 +700,39 @@ cudaError_t launch_fp8_gemm(const Fp8GemmArgs& g, cudaStream_t s) {
   const Operand A{g.a_codes, g.a_scales, g.M}, B{g.b_codes, g.b_scales, g.N};
   const uint32_t num_k = (uint32_t)(fp8_pitch(g.K) / BK);
   double c256, c128;
-  if (g.M <= 64) return launch<64, true>(B, A, g, Plan<64, true>::split(g.N, g.M, num_k, c128), s);
-  if (g.M <= 128) return launch<128, true>(B, A, g, Plan<128, true>::split(g.N, g.M, num_k, c128), s);
+  if (g.M <= 64) return launch_one<64, true>(B, A, g, Plan<64, true>::split(g.N, g.M, num_k, c128), s);
+  if (g.M <= 128) return launch_one<128, true>(B, A, g, Plan<128, true>::split(g.N, g.M, num_k, c128), s);
   const uint32_t s256 = Plan<256, false>::split(g.M, g.N, num_k, c256);
   const uint32_t s128 = Plan<128, false>::split(g.M, g.N, num_k, c128);
-  return c128 < c256 ? launch<128, false>(A, B, g, s128, s) : launch<256, false>(A, B, g, s256, s);
+  return c128 < c256 ? launch_one<128, false>(A, B, g, s128, s) : launch_one<256, false>(A, B, g, s256, s);
+}
+
+cudaError_t launch_fp8_gemm_two(const Fp8GemmArgs& a, const Fp8GemmArgs& b, cudaStream_t s) {
+  using namespace f8;
+  // few rows have kernels of their own; else one launch, with tiles of the width whose total is less
+  if (a.M <= 128 || b.M <= 128) {
+    const cudaError_t e = launch_fp8_gemm(a, s);
+    return e == cudaSuccess ? launch_fp8_gemm(b, s) : e;
+  }
+  auto total = [](const Fp8GemmArgs& g, int64_t bn, double tile) {
+    return double((g.M + 255) / 256 * ((g.N + bn - 1) / bn)) * tile;
+  };
+  auto stages = [](const Fp8GemmArgs& g) { return (uint32_t)(fp8_pitch(g.K) / BK); };
+  using P256 = Plan<256, false>;
+  using P128 = Plan<128, false>;
+  // (at least one tile's time: few long tiles take the narrow form)
+  auto cost = [&](double sum, double longest, uint32_t clusters) {
+    const double even = sum / clusters;
+    return even > longest ? even : longest;
+  };
+  const double t256 = cost(total(a, 256, P256::tile(stages(a))) + total(b, 256, P256::tile(stages(b))),
+                           P256::tile(stages(a) > stages(b) ? stages(a) : stages(b)), limits<256, false>().clusters[1]);
+  const double t128 = cost(total(a, 128, P128::tile(stages(a))) + total(b, 128, P128::tile(stages(b))),
+                           P128::tile(stages(a) > stages(b) ? stages(a) : stages(b)), limits<128, false>().clusters[1]);
+  // the longer tiles first: the shorter ones even out the end
+  const bool order = stages(a) >= stages(b);
+  const Fp8GemmArgs &x = order ? a : b, &y = order ? b : a;
+  return t128 < t256 ? launch_two<128>(x, y, s) : launch_two<256>(x, y, s);
 }
 
 cudaError_t fp8_status_read_clear(unsigned int* out, cudaStream_t s) {

@@ -245,6 +245,8 @@ struct Fp8GemmArgs {
   int64_t ldc;
 };
 cudaError_t launch_fp8_gemm(const Fp8GemmArgs& g, cudaStream_t s);
+// Two independent products, in one launch where that helps.
+cudaError_t launch_fp8_gemm_two(const Fp8GemmArgs& a, const Fp8GemmArgs& b, cudaStream_t s);
 // Y (T x N BF16, pitch ldy) = X W^T for at most 16 tokens, X quantized on the way; fp8_few() says whether that beats a
 // quantizer and the GEMM: up to 8 tokens always (5632 x 2048: 5.0 against 10.4 us, 32000 x 2048: 14 against 19), to 16
 // while the weights are small (8.9 against 10.4 us, but 28 against 19).

@@ -680,7 +680,7 @@ constexpr int kBwdThreads = 256, kBwdVecs = 4;
 
 template <typename T, bool TOP>
 __global__ void __launch_bounds__(kBwdThreads, 8) logprob_bwd_kernel(const LogprobBwdArgs a, uint32_t chunks,
-                                                                    const float far) {
+                                                                    const float far, const bool stream) {
   using V8 = Vec<T>;
   constexpr int N = V8::N;
   const int64_t t = blockIdx.x / chunks;
@@ -754,7 +754,7 @@ __global__ void __launch_bounds__(kBwdThreads, 8) logprob_bwd_kernel(const Logpr
     uint4 q[kBwdVecs];
 #pragma unroll
     for (int u = 0; u < kBwdVecs; ++u)
-      if (i0 + u * kBwdThreads < cut.vecs) q[u] = vec[i0 + u * kBwdThreads];
+      if (i0 + u * kBwdThreads < cut.vecs) q[u] = stream ? __ldcs(vec + i0 + u * kBwdThreads) : vec[i0 + u * kBwdThreads];
 #pragma unroll
     for (int u = 0; u < kBwdVecs; ++u) {
       const uint32_t i = i0 + u * kBwdThreads;
@@ -780,7 +780,8 @@ __global__ void __launch_bounds__(kBwdThreads, 8) logprob_bwd_kernel(const Logpr
         for (int j = 0; j < N; ++j)
           if (j == target_in && V8::load(row + target) != neg_inf) d[j] += own_t;
       }
-      dst[i] = V8::pack(d);
+      if (stream) __stcs(dst + i, V8::pack(d));
+      else dst[i] = V8::pack(d);
     }
     if (chunk == 0 && tid < cut.head + cut.tail) one(tid < cut.head ? tid : cut.vecs * N + tid);
   } else {
@@ -859,8 +860,11 @@ static cudaError_t launch_bwd_t(const LogprobBwdArgs& a, cudaStream_t s) {
   if (a.T * chunks > INT32_MAX) return cudaErrorInvalidConfiguration;
   const dim3 grid(static_cast<uint32_t>(a.T * chunks));
   const float far = lp::far_of(a.scale);
-  if (a.top_k) lp::logprob_bwd_kernel<T, true><<<grid, lp::kBwdThreads, 0, s>>>(a, (uint32_t)chunks, far);
-  else lp::logprob_bwd_kernel<T, false><<<grid, lp::kBwdThreads, 0, s>>>(a, (uint32_t)chunks, far);
+  // More than L2 holds (129 MB, for the logits and their gradient): neither is worth keeping there (8192 x 32000 BF16:
+  // 171 us with the default policy, 161 streaming); less is, for what reads the gradient next.
+  const bool stream = (double)a.T * a.V * sizeof(T) > 64e6;
+  if (a.top_k) lp::logprob_bwd_kernel<T, true><<<grid, lp::kBwdThreads, 0, s>>>(a, (uint32_t)chunks, far, stream);
+  else lp::logprob_bwd_kernel<T, false><<<grid, lp::kBwdThreads, 0, s>>>(a, (uint32_t)chunks, far, stream);
   const cudaError_t e = cudaGetLastError();
   count_launch();
   return e;
