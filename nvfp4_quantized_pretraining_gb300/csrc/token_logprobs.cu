@@ -138,16 +138,23 @@ __device__ __forceinline__ RowCut cut_row(const T* row, uint32_t V) {
 // results while the readers are at the next row.  (With loads into registers and the joins done by all warps between
 // barriers, 8192 x 32000 BF16 took 104 us, the loads idle during the joins.)
 //
-// A cluster of C CTAs takes a row, each CTA a consecutive share of the row's vectors (rank 0 also the edge
-// elements); shares are joined in rank 0.  Clusters walk the rows, as many as there are of them apart.
+// A cluster of C > 1 CTAs takes one row, each CTA a consecutive share of its vectors (rank 0 also the edge elements);
+// the shares are joined in rank 0.  Single CTAs walk the rows, as many as there are of them apart.
 constexpr int kReaders = 256;
-// One joining warp keeps up with the readers; four, each on every fourth row, where they find the top k.
-__host__ __device__ constexpr int joiners_of(bool top) { return top ? 4 : 1; }
-__host__ __device__ constexpr int buffers_of(bool top) { return top ? 4 : 2; }
-__host__ __device__ constexpr int per_sm_of(bool top) { return top ? 2 : 3; }  // CTAs
+// One joining warp keeps up with the readers; three, each on every third row, where they find the top k.
+__host__ __device__ constexpr int joiners_of(bool top) { return top ? 3 : 1; }
+__host__ __device__ constexpr int buffers_of(bool top) { return top ? 3 : 2; }
+constexpr int kPerSm = 3;  // CTAs
+// With the top k, the 56 registers a thread that three CTAs leave are split anew: 48 to the readers (two warpgroups), 72
+// to the copying and joining warps (one): 2 x 128 x 48 + 128 x 72 = 384 x 56.  (Both roles within 56 spilled, every
+// spilled word a miss in the little L1 left; two CTAs of 72 a thread took 112 us for 8192 x 32000 BF16, top 5, these 108.)
+constexpr int kReaderRegs = 48, kJoinerRegs = 72;
 __host__ __device__ constexpr int threads_of(bool top) { return kReaders + 32 + 32 * joiners_of(top); }
-constexpr int kStages = 3, kStageVecs = 1024;
-constexpr int kSmemBytes = kStages * kStageVecs * 16;
+constexpr int kStageVecs = 1024;
+// (two stages with the top k: three leave the joining warps' other reads next to no L1; 8192 x 32000 BF16, top 20:
+// 126 us with two, 164 with three)
+__host__ __device__ constexpr int stages_of(bool top) { return top ? 2 : 3; }
+__host__ __device__ constexpr int ring_bytes(bool top) { return stages_of(top) * kStageVecs * 16; }
 constexpr int kMaxCluster = 8;
 
 // What readers leave of a row: per thread the true maximum (-inf: only banned tokens), and the sums relative to
@@ -157,6 +164,7 @@ struct Partials {
 };
 template <bool TOP>
 struct Scratch {  // a joining warp's
+  uint4 in[4 * 32];
   uint4 hit[kCap];
   uint64_t above[kCap], equal[kCap / 2];
   uint64_t top[kMaxTop];
@@ -252,20 +260,24 @@ __device__ __forceinline__ void share_top(const Share<T> h, const float* maxima,
     uint32_t hits = 0;
     for (uint32_t w0 = 0; w0 < per && hits <= kCap; w0 += 1u << shift) {
       for (uint32_t q = lane >> shift; q - (lane >> shift) < strips && hits <= kCap; q += 4 * (32 >> shift)) {
-        uint4 w[4];
+        // (by asynchronous copies past L1: loads would each hold a line of the little L1 that the ring leaves)
         uint32_t at[4];
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
           const uint32_t p = q + u * (32 >> shift), v = w0 + (lane & ((1u << shift) - 1));
           at[u] = p < strips && v < per ? h.v0 + x.list[p] + v * kReaders : h.v1;
-          w[u] = at[u] < h.v1 ? vec[at[u]] : make_uint4(V8::kNone, V8::kNone, V8::kNone, V8::kNone);
+          if (at[u] < h.v1)
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(&x.in[u * 32 + lane])), "l"(vec + at[u])
+                         : "memory");
         }
+        asm volatile("cp.async.wait_all;" ::: "memory");
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
-          const float most = V8::widest(V8::max1(V8::max1(w[u].x, w[u].y), V8::max1(w[u].z, w[u].w)));
+          const uint4 w = x.in[u * 32 + lane];  // (its own copy; a lane without a vector has no use for what is there)
+          const float most = V8::widest(V8::max1(V8::max1(w.x, w.y), V8::max1(w.z, w.w)));
           const bool hit = at[u] < h.v1 && (with_equal ? most >= least : most > least);
           const uint32_t in = __ballot_sync(kAll, hit), to = hits + __popc(in & below);
-          if (hit && to < kCap) x.hit[to] = w[u], x.hit_at[to] = at[u];
+          if (hit && to < kCap) x.hit[to] = w, x.hit_at[to] = at[u];
           hits += __popc(in);
         }
       }
@@ -276,16 +288,18 @@ __device__ __forceinline__ void share_top(const Share<T> h, const float* maxima,
     const uint32_t listed = min(hits, (uint32_t)kCap);
     for (uint32_t i = 0; i < listed + 32; i += 32) {
       uint32_t over = 0, same = 0, first = 0;
-      float f[N];
       const bool last = i >= listed;
+      const T* hit = reinterpret_cast<const T*>(&x.hit[i + lane]);
       if (last) {
         first = h.edge_index(lane);
         over = lane < h.edges && edge_key > tau, same = lane < h.edges && edge_key == tau;
       } else if (i + lane < listed) {
-        V8::unpack(x.hit[i + lane], f);
         first = h.index(x.hit_at[i + lane], 0);
-#pragma unroll
-        for (int j = 0; j < N; ++j) over |= (f[j] > least) << j, same |= (f[j] == least) << j;
+#pragma unroll 2
+        for (int j = 0; j < N; ++j) {
+          const float z = V8::load(hit + j);
+          over |= (z > least ? 1u : 0u) << j, same |= (z == least ? 1u : 0u) << j;
+        }
       }
       if (!with_equal) same = 0;
       uint32_t n = __popc(over) | __popc(same) << 16, before = n;
@@ -297,16 +311,12 @@ __device__ __forceinline__ void share_top(const Share<T> h, const float* maxima,
       const uint32_t all = __shfl_sync(kAll, before, 31);
       before -= n;
       uint32_t to = above + (before & 0xFFFFu);
-      if (last) {
-        if (over && to < kCap) x.above[to] = entry_of(edge_key, first);
-      } else {
-#pragma unroll
-        for (int j = 0; j < N; ++j)
-          if ((over >> j & 1) && to < kCap) x.above[to++] = entry_of(order_key(f[j]), first + j);
+      for (; over && to < kCap; over &= over - 1) {
+        const uint32_t j = __ffs(over) - 1;
+        x.above[to++] = entry_of(last ? edge_key : order_key(V8::load(hit + j)), first + j);
       }
       to = equal + (before >> 16);
-      for (; same; same &= same - 1)
-        if (to < kCap / 2) x.equal[to++] = entry_of(tau, first + __ffs(same) - 1);
+      for (; same && to < kCap / 2; same &= same - 1) x.equal[to++] = entry_of(tau, first + __ffs(same) - 1);
       above += all & 0xFFFFu, equal += all >> 16;
     }
     __syncwarp();
@@ -413,17 +423,17 @@ __device__ __forceinline__ void share_top(const Share<T> h, const float* maxima,
 }
 
 template <typename T, bool TOP>
-__global__ void __launch_bounds__(threads_of(TOP), per_sm_of(TOP)) logprob_kernel(const LogprobArgs a, const float far) {
+__global__ void __launch_bounds__(threads_of(TOP), kPerSm) logprob_kernel(const LogprobArgs a, const float far) {
   using V8 = Vec<T>;
   constexpr int N = V8::N, U = kStageVecs / kReaders;
-  constexpr uint32_t B = buffers_of(TOP), J = joiners_of(TOP);
+  constexpr uint32_t B = buffers_of(TOP), J = joiners_of(TOP), kStages = stages_of(TOP);
   extern __shared__ uint4 s_ring[];  // [kStages][kStageVecs]
   __shared__ uint64_t s_full[kStages], s_free[kStages], s_done[B], s_read[B];
-  __shared__ uint64_t s_pushed[B], s_taken[B];  // rank 0: the other shares arrived; the others: rank 0 has used theirs
+  __shared__ uint64_t s_pushed;  // rank 0: the other shares have arrived
   __shared__ Partials s_part[B];
-  __shared__ Sum s_joined[B][kMaxCluster];
+  __shared__ Sum s_joined[kMaxCluster];
   __shared__ Scratch<TOP> s_scratch[joiners_of(TOP)];
-  __shared__ uint64_t s_joined_top[B][TOP ? kMaxCluster * kMaxTop : 1];
+  __shared__ uint64_t s_joined_top[TOP ? kMaxCluster * kMaxTop : 1];
   const uint32_t rank = cluster_ctarank(), C = cluster_size();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const float k2 = a.scale * kLog2e;
@@ -437,9 +447,8 @@ __global__ void __launch_bounds__(threads_of(TOP), per_sm_of(TOP)) logprob_kerne
     for (int i = 0; i < B; ++i) {
       mbar_init(&s_done[i], kReaders / 32);
       mbar_init(&s_read[i], 1);
-      mbar_init(&s_pushed[i], max(C, 2u) - 1);
-      mbar_init(&s_taken[i], 1);
     }
+    mbar_init(&s_pushed, max(C, 2u) - 1);
     fence_mbar_init();
   }
   if (C > 1) cluster_sync();  // (rank 0's barrier exists before anyone arrives on it)
@@ -448,6 +457,7 @@ __global__ void __launch_bounds__(threads_of(TOP), per_sm_of(TOP)) logprob_kerne
 
   if (warp < kReaders / 32) {
     // ---------------- readers ----------------
+    if (TOP) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kReaderRegs));
     uint32_t used = 0, rows = 0;
     const uint32_t low = V8::low_bits(-far);
     for (int64_t t = first; t < a.T; t += stride, ++rows) {
@@ -506,6 +516,7 @@ __global__ void __launch_bounds__(threads_of(TOP), per_sm_of(TOP)) logprob_kerne
     }
   } else if (warp == kReaders / 32) {
     // ---------------- the ring's copies ----------------
+    if (TOP) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kJoinerRegs));
     if (lane == 0) {
       uint32_t issued = 0;
       for (int64_t t = first; ok && t < a.T; t += stride) {
@@ -521,6 +532,7 @@ __global__ void __launch_bounds__(threads_of(TOP), per_sm_of(TOP)) logprob_kerne
     }
   } else {
     // ---------------- joins and results ----------------
+    if (TOP) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kJoinerRegs));
     auto near = [&](float v) { return v > -0.5f * far && v <= 0.5f * far; };
     Scratch<TOP>& x = s_scratch[warp - kReaders / 32 - 1];
     uint32_t rows = warp - kReaders / 32 - 1;
@@ -566,33 +578,32 @@ __global__ void __launch_bounds__(threads_of(TOP), per_sm_of(TOP)) logprob_kerne
       if (C > 1) {
         const uint32_t to0 = rank * a.top_k;
         if (rank != 0) {  // to rank 0
-          if (!mbar_wait_warp(&s_taken[buf], ((rows / B) & 1) ^ 1)) ok = false;
-          const uint32_t at = mapa_shared(smem_u32(&s_joined[buf][rank]), 0);
+          const uint32_t at = mapa_shared(smem_u32(&s_joined[rank]), 0);
           if (lane == 0) {
             st_cluster_f32(at, r.m);
             st_cluster_f32(at + 4, r.s);
             st_cluster_f32(at + 8, r.e);
           }
           if constexpr (TOP) {
-            if (lane < a.top_k) st_cluster_u64(mapa_shared(smem_u32(&s_joined_top[buf][to0 + lane]), 0), x.top[lane]);
+            if (lane < a.top_k) st_cluster_u64(mapa_shared(smem_u32(&s_joined_top[to0 + lane]), 0), x.top[lane]);
           }
           asm volatile("fence.acq_rel.cluster;" ::: "memory");
           __syncwarp();
-          if (lane == 0) mbar_arrive_cluster(mapa_shared(smem_u32(&s_pushed[buf]), 0));
+          if (lane == 0) mbar_arrive_cluster(mapa_shared(smem_u32(&s_pushed), 0));
           continue;
         }
-        if (lane == 0) s_joined[buf][0] = r;
+        if (lane == 0) s_joined[0] = r;
         if constexpr (TOP) {
-          if (lane < a.top_k) s_joined_top[buf][lane] = x.top[lane];
+          if (lane < a.top_k) s_joined_top[lane] = x.top[lane];
         }
         __syncwarp();
-        if (!__all_sync(0xFFFFFFFFu, mbar_wait_cluster(&s_pushed[buf], (rows / B) & 1))) ok = false;
-        most = s_joined[buf][0].m;
-        for (uint32_t i = 1; i < C; ++i) most = fmaxf(most, s_joined[buf][i].m);
+        if (!__all_sync(0xFFFFFFFFu, mbar_wait_cluster(&s_pushed, 0))) ok = false;
+        most = s_joined[0].m;
+        for (uint32_t i = 1; i < C; ++i) most = fmaxf(most, s_joined[i].m);
         const float to = reference(fmaxf(most, -far), k2);
         r.m = most, r.s = 0.0f, r.e = 0.0f;
         for (uint32_t i = 0; i < C; ++i) {
-          const Sum o = s_joined[buf][i];
+          const Sum o = s_joined[i];
           const float d = reference(fmaxf(o.m, -far), k2) - to, f = ex2(d);
           r.s += o.s * f;
           r.e += (o.e + o.s * d) * f;
@@ -600,7 +611,7 @@ __global__ void __launch_bounds__(threads_of(TOP), per_sm_of(TOP)) logprob_kerne
         if constexpr (TOP) {
           // the shares' lists are in order: k rounds of the largest head
           uint32_t at = 0;
-          uint64_t head = lane < C ? s_joined_top[buf][lane * a.top_k] : 0;
+          uint64_t head = lane < C ? s_joined_top[lane * a.top_k] : 0;
           for (uint32_t i = 0; i < a.top_k; ++i) {
             uint64_t best = head;
 #pragma unroll
@@ -609,11 +620,10 @@ __global__ void __launch_bounds__(threads_of(TOP), per_sm_of(TOP)) logprob_kerne
               best = other > best ? other : best;
             }
             if (lane == 0) x.top[i] = best;
-            if (lane < C && head == best) head = ++at < a.top_k ? s_joined_top[buf][lane * a.top_k + at] : 0;
+            if (lane < C && head == best) head = ++at < a.top_k ? s_joined_top[lane * a.top_k + at] : 0;
           }
         }
         __syncwarp();
-        if (lane > 0 && lane < C) mbar_arrive_cluster(mapa_shared(smem_u32(&s_taken[buf]), lane));
       }
       most = r.m;
       float S, E;  // relative to the maximum
@@ -810,14 +820,13 @@ template <typename T, bool TOP>
 static cudaError_t launch_fwd(const LogprobArgs& a, float far, uint32_t cluster, int num_sms, cudaStream_t s) {
   auto kernel = logprob_kernel<T, TOP>;
   static const cudaError_t attr_err =
-      cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
+      cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, ring_bytes(TOP));
   if (attr_err != cudaSuccess) return attr_err;
-  const int64_t slots = (int64_t)num_sms * per_sm_of(TOP);
+  const int64_t slots = (int64_t)num_sms * kPerSm;
   cudaLaunchConfig_t cfg = {};
-  const int64_t clusters = slots / cluster;
-  cfg.gridDim = dim3(static_cast<uint32_t>((a.T < clusters ? a.T : clusters) * cluster));
+  cfg.gridDim = dim3(static_cast<uint32_t>(cluster > 1 || a.T < slots ? a.T * cluster : slots));
   cfg.blockDim = dim3(threads_of(TOP));
-  cfg.dynamicSmemBytes = kSmemBytes;
+  cfg.dynamicSmemBytes = ring_bytes(TOP);
   cfg.stream = s;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -840,7 +849,7 @@ static cudaError_t launch_fwd_t(const LogprobArgs& a, int num_sms, cudaStream_t 
   // Clusters only where whole rows leave CTAs without one, and then as large as all rows' CTAs fit at once (a share
   // at least one stage of the ring): joining shares costs more than an uneven last round (515 x 50021 FP32, top 5:
   // 25 us in single CTAs, 27, 46 and 74 in clusters of 2, 4 and 8; 64 x 131072 BF16, top 20: 35 and 21 in 1 and 4).
-  const int64_t slots = (int64_t)num_sms * per_sm_of(a.top_k > 0);
+  const int64_t slots = (int64_t)num_sms * kPerSm;
   uint32_t cluster = 1;
   while (cluster < kMaxCluster && a.T * cluster * 2 <= slots && a.V / (cluster * 2) >= kStageVecs * Vec<T>::N) cluster *= 2;
   const float far = far_of(a.scale);
