@@ -11,10 +11,12 @@
 //
 // The step is bound by memory (30 bytes per element with FP32 states, FP32 gradients and a BF16 copy, 16 with 8-bit
 // states, BF16 gradients and a copy) and, with 8-bit states, nearly as much by issue slots: 6.8 TB/s leaves 87
-// instructions per element for two square roots' worth of exact arithmetic, two random numbers and two codes.  So the
+// instructions per element for a square root, a quotient, two random numbers and two codes; it takes 75.  So the
 // inputs come through a ring of shared-memory stages by bulk copies (loads in flight without registers), arithmetic
-// goes in packed pairs, and a thread owns 8 consecutive elements: a block of 128 is 16 lanes, its amax four shuffles,
-// its random bits one generator call per moment.
+// goes in packed pairs, the square root and the quotient with it, and a thread owns 8 consecutive elements: a block of
+// 128 is 16 lanes, its amax four shuffles, its random bits one generator call per moment.
+// 203M elements with 8-bit states: 578 us, 5.6 TB/s, 82% of the copy bandwidth (634 us with the compiler's square roots
+// and divisions, which are scalar and branch; 737 with loads into registers).
 #include <cuda_bf16.h>
 
 #include "common.cuh"
@@ -31,8 +33,12 @@ constexpr int kChunk = kThreads * 8;  // elements of one CTA step: 16 whole bloc
 // step with the caller's pointers).  Two capacities, so that a short list stays a small launch.
 constexpr int kCapSmall = 48, kCapLarge = 400;
 
+__device__ __forceinline__ float2 both(float a) { return make_float2(a, a); }
 struct Scalars {
-  float b1, c1, b2, c2, size, root, eps;
+  float2 b1, c1, b2, c2, size, minus_size, root, eps;  // (each twice: operands of packed instructions)
+  float2 one, scaled_root, up, minus_up, half, minus_half;  // 1, 2^-20 root, +-2^40, +-0.5
+  bool usual;                                               // constants that minus_quotient() takes
+  uint32_t up20, up21;                                      // 2^4, 2^3
   uint32_t step, first_tensor, count, chunks;
   const float* grad_scale;
   PhiloxKeys keys;
@@ -43,12 +49,11 @@ struct Table {
   uint32_t first_chunk[CAP + 1];
 };
 
-// Pairs of FP32 operations, each rounded by itself: packed products, scalar sums (a packed product and a packed sum
-// were contracted into one rounding, seen as a last bit of the parameters).
+// Pairs of FP32 operations, each rounded by itself.  A sum after a product is written fma2(product, one, b) with a
+// `one` that the compiler does not know: it merged packed products and packed sums into one rounding, seen as a last
+// bit of the parameters.
 __device__ __forceinline__ float2 mul2(float2 a, float2 b) { return __fmul2_rn(a, b); }
-__device__ __forceinline__ float2 add_each(float2 a, float2 b) {
-  return make_float2(__fadd_rn(a.x, b.x), __fadd_rn(a.y, b.y));
-}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) { return __ffma2_rn(a, b, c); }
 __device__ __forceinline__ void load8(float2 (&x)[4], const float* p) {
   const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
   x[0] = make_float2(a.x, a.y), x[1] = make_float2(a.z, a.w), x[2] = make_float2(b.x, b.y), x[3] = make_float2(b.z, b.w);
@@ -121,32 +126,56 @@ template <int I>
 __device__ __forceinline__ uint32_t bytes(uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
   return __byte_perm(__byte_perm(a, b, I | (4 + I) << 4), __byte_perm(c, d, I | (4 + I) << 4), 0x5410);
 }
+// up: 2^(24 - SHIFT), a variable so that the product stays a multiply-add (a shift would go to the busier pipe).
 template <int SHIFT, bool FLOOR, bool SR>
-__device__ __forceinline__ uint2 encode8_fast(const float2 (&a)[4], const uint32_t (&w)[4], uint32_t byte) {
+__device__ __forceinline__ uint2 encode8_fast(const float2 (&a)[4], const uint32_t (&w)[4], uint32_t byte, uint32_t up) {
   const float f = Fast<SHIFT>::factor(byte);
-  uint32_t t[8];
+  uint32_t t[8], sign[8];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const float2 y = mul2(a[i], make_float2(f, f));
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
       const uint32_t bits = __float_as_uint(j ? y.y : y.x);
-      uint32_t v;  // (a sign bit stays where it is: the magnitude's sum has no carry that far)
-      if (SR) v = bits + (j ? w[i] >> 16 << (SHIFT - 16) : w[i] << 16 >> (32 - SHIFT));
-      else v = bits + (1u << (SHIFT - 1)) - 1u + ((bits >> SHIFT) & 1u);
-      if (FLOOR && (j ? a[i].y : a[i].x) > 0.0f) v = max(v, 1u << SHIFT);
-      t[2 * i + j] = v;
+      uint32_t v;  // the code in the top byte, less its sign
+      if (SR) v = bits * up + __byte_perm(w[i], 0, j ? 0x4324 : 0x4104);
+      else v = (bits + (1u << (SHIFT - 1)) - 1u + ((bits >> SHIFT) & 1u)) * up;
+      if (FLOOR && (j ? a[i].y : a[i].x) > 0.0f) v = max(v, 1u << 24);
+      t[2 * i + j] = v, sign[2 * i + j] = bits;
     }
   }
   uint2 out;
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
-    const uint32_t* q = t + 4 * h;
-    uint32_t codes = bytes<0>(q[0] >> SHIFT, q[1] >> SHIFT, q[2] >> SHIFT, q[3] >> SHIFT);
-    if (!FLOOR) codes = (codes & 0x7F7F7F7Fu) | (bytes<3>(q[0], q[1], q[2], q[3]) & 0x80808080u);  // the signs
+    const uint32_t *q = t + 4 * h, *b = sign + 4 * h;
+    uint32_t codes = bytes<3>(q[0], q[1], q[2], q[3]);
+    if (!FLOOR) codes = (codes & 0x7F7F7F7Fu) | (bytes<3>(b[0], b[1], b[2], b[3]) & 0x80808080u);
     (h ? out.y : out.x) = codes;
   }
   return out;
+}
+// The quotient of the step for a pair, -m / (sqrt(v) root + eps), to the bit what the correctly rounded operations give,
+// in packed multiply-adds: Markstein's iterations ("Computation of elementary functions on the IBM RISC System/6000
+// processor", 1990), each with an exact remainder at its end.  For 0 <= v < 2^31, m of 0 or 2^-100 <= |m| < 2^16 and
+// constants with Scalars::usual: no intermediate value leaves the normal range, v below 2^-126 counts as
+// that (root sqrt(v) is no part of the rounded sum then), and v goes through the root times 2^40 to keep its remainder normal.
+__device__ __forceinline__ float2 minus_quotient(float2 m, float2 v, const Scalars& k) {
+  const float2 c = make_float2(fmaxf(v.x, 0x1p-126f), fmaxf(v.y, 0x1p-126f));
+  const float2 w = mul2(c, k.up), nw = mul2(c, k.minus_up);
+  float2 y;
+  asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(y.x) : "f"(w.x));
+  asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(y.y) : "f"(w.y));
+  float2 g = mul2(w, y), h = mul2(y, k.minus_half);  // sqrt w, -1 / (2 sqrt w)
+  const float2 r = fma2(g, h, k.half);
+  g = fma2(g, r, g), h = fma2(h, r, h);
+  g = fma2(fma2(g, g, nw), h, g);
+  const float2 d = fma2(mul2(g, k.scaled_root), k.one, k.eps);
+  float2 z;  // -1 / d
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(z.x) : "f"(-d.x));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(z.y) : "f"(-d.y));
+  z = fma2(fma2(d, z, k.one), z, z);
+  const float2 q = mul2(m, z);
+  return fma2(fma2(d, q, m), z, q);
 }
 // The magnitude pattern of the largest of eight values; NaN if one is.
 __device__ __forceinline__ float max_nan_abs(float a, float b) {
@@ -157,8 +186,12 @@ __device__ __forceinline__ float max_nan_abs(float a, float b) {
 __device__ __forceinline__ uint32_t amax16(const float2 (&a)[4]) {
   float m = max_nan_abs(max_nan_abs(max_nan_abs(a[0].x, a[0].y), max_nan_abs(a[1].x, a[1].y)),
                         max_nan_abs(max_nan_abs(a[2].x, a[2].y), max_nan_abs(a[3].x, a[3].y)));
-  // (patterns of magnitudes order as they do, NaN above all)
-  return __reduce_max_sync(0xFFFFu << (threadIdx.x & 16), __float_as_uint(m));
+  // (patterns of magnitudes order as they do, NaN above all; four shuffles, since a reduction of half a warp became
+  // a loop over the halves: 620 us instead of 599 for 203M elements)
+  uint32_t x = __float_as_uint(m);
+#pragma unroll
+  for (int o = 1; o < 16; o <<= 1) x = max(x, __shfl_xor_sync(0xFFFFFFFFu, x, o));
+  return x;
 }
 
 // The random words of m and v for the group of eight elements j of a tensor with stream ids st, st + 1.  For j < 2^32
@@ -278,10 +311,11 @@ __global__ void __launch_bounds__(kThreads + 32, kPerSm)
   } else {
     RandomBase base{};
     if (SR) base = random_base(2u * (k.first_tensor + lo), k.keys);
-    uint32_t used = 0;
+    uint32_t used = 0, next = tab.first_chunk[lo + 1];
     for (uint32_t c = c0; c < c1; ++c) {
-      if (tab.first_chunk[lo + 1] <= c) {
+      if (next <= c) {
         while (tab.first_chunk[lo + 1] <= c) ++lo;
+        next = tab.first_chunk[lo + 1];
         if (SR) base = random_base(2u * (k.first_tensor + lo), k.keys);
       }
       const AdamWEntry& t = tab.t[lo];
@@ -347,20 +381,55 @@ __global__ void __launch_bounds__(kThreads + 32, kPerSm)
       }
 
       // ---- the step
-      auto both = [](float a) { return make_float2(a, a); };
-      const float2 ms = both(fp8_scale_value(mb)), vs = both(fp8_scale_value(vb));
+          const float2 ms = both(fp8_scale_value(mb)), vs = both(fp8_scale_value(vb));
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         if (BITS8) {
           m[i] = mul2(e4m3x2_to_f32((i < 2 ? mc.x : mc.y) >> (16 * (i & 1))), ms);
           v[i] = mul2(e5m2x2_to_f32((i < 2 ? vc.x : vc.y) >> (16 * (i & 1))), vs);
         }
-        if (k.grad_scale) g[i] = mul2(g[i], both(gs));
-        m[i] = add_each(mul2(m[i], both(k.b1)), mul2(g[i], both(k.c1)));
-        v[i] = add_each(mul2(v[i], both(k.b2)), mul2(mul2(g[i], g[i]), both(k.c2)));
-        const float2 d = add_each(mul2(make_float2(__fsqrt_rn(v[i].x), __fsqrt_rn(v[i].y)), both(k.root)), both(k.eps));
-        const float2 q = make_float2(__fdiv_rn(m[i].x, d.x), __fdiv_rn(m[i].y, d.y));
-        p[i] = add_each(mul2(p[i], both(t.keep)), mul2(q, both(-k.size)));
+        g[i] = mul2(g[i], both(gs));  // (1 without a scale)
+        m[i] = fma2(mul2(m[i], k.b1), k.one, mul2(g[i], k.c1));
+        v[i] = fma2(mul2(v[i], k.b2), k.one, mul2(mul2(g[i], g[i]), k.c2));
+      }
+      uint32_t mn = 0, vn = 0;
+      bool usual = false;
+      if (BITS8) {
+        mn = fp8_scale_byte(amax16(m), kTopE4M3), vn = fp8_scale_byte(amax16(v), kTopE5M2);
+        uint32_t least = 0xFFFFFFFFu;  // (twice the pattern less 1: no sign, and 0 the largest)
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          least = min(min(least, 2u * __float_as_uint(m[i].x) - 1u), 2u * __float_as_uint(m[i].y) - 1u);
+        // (NaN and Inf have exponent 255 and so a byte far above the limit)
+        usual = __all_sync(0xFFFFFFFFu, mn <= Fast<20>::kByte && vn <= Fast<21>::kByte &&
+                                            least >= 2u * 0x0D800000u - 1u && k.usual);
+      }
+      RandomPair rnd{};
+      if (BITS8 && SR) rnd = random_pair(e0 >> 3, 2u * (k.first_tensor + lo), k.step, base, k.keys);
+      uint2 mo, vo;
+      if (BITS8 && usual) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float2 q = minus_quotient(m[i], v[i], k);
+          p[i] = fma2(mul2(p[i], both(t.keep)), k.one, mul2(q, k.size));
+        }
+        mo = encode8_fast<20, false, SR>(m, rnd.m, mn, k.up20);
+        vo = encode8_fast<21, true, SR>(v, rnd.v, vn, k.up21);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float2 d = fma2(mul2(make_float2(__fsqrt_rn(v[i].x), __fsqrt_rn(v[i].y)), k.root), k.one, k.eps);
+          const float2 q = make_float2(__fdiv_rn(m[i].x, d.x), __fdiv_rn(m[i].y, d.y));
+          p[i] = fma2(mul2(p[i], both(t.keep)), k.one, mul2(q, k.minus_size));
+        }
+        if (BITS8) {
+          float m8[8], v8[8];
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            m8[2 * i] = m[i].x, m8[2 * i + 1] = m[i].y, v8[2 * i] = v[i].x, v8[2 * i + 1] = v[i].y;
+          mo = encode8<kTopE4M3, 20, 0x7Fu, false, SR>(m8, make_uint4(rnd.m[0], rnd.m[1], rnd.m[2], rnd.m[3]), mn);
+          vo = encode8<kTopE5M2, 21, 0x7Fu, true, SR>(v8, make_uint4(rnd.v[0], rnd.v[1], rnd.v[2], rnd.v[3]), vn);
+        }
       }
 
       // ---- out
@@ -387,22 +456,6 @@ __global__ void __launch_bounds__(kThreads + 32, kPerSm)
           }
       }
       if (BITS8) {
-        RandomPair r{};
-        if (SR) r = random_pair(e0 >> 3, 2u * (k.first_tensor + lo), k.step, base, k.keys);
-        uint32_t mn = fp8_scale_byte(amax16(m), kTopE4M3), vn = fp8_scale_byte(amax16(v), kTopE5M2);
-        uint2 mo, vo;
-        // (NaN and Inf have exponent 255 and so a byte far above the limit)
-        if (__all_sync(0xFFFFFFFFu, mn <= Fast<20>::kByte && vn <= Fast<21>::kByte)) {
-          mo = encode8_fast<20, false, SR>(m, r.m, mn);
-          vo = encode8_fast<21, true, SR>(v, r.v, vn);
-        } else {
-          float m8[8], v8[8];
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-            m8[2 * i] = m[i].x, m8[2 * i + 1] = m[i].y, v8[2 * i] = v[i].x, v8[2 * i + 1] = v[i].y;
-          mo = encode8<kTopE4M3, 20, 0x7Fu, false, SR>(m8, make_uint4(r.m[0], r.m[1], r.m[2], r.m[3]), mn);
-          vo = encode8<kTopE5M2, 21, 0x7Fu, true, SR>(v8, make_uint4(r.v[0], r.v[1], r.v[2], r.v[3]), vn);
-        }
         uint8_t* mp = static_cast<uint8_t*>(t.m) + e0;
         uint8_t* vp = static_cast<uint8_t*>(t.v) + e0;
         if (whole) {
@@ -462,8 +515,14 @@ int adamw_capacity() { return aw::kCapLarge; }
 cudaError_t launch_adamw(const AdamWEntry* t, int n, int first_tensor, bool grad_bf16, int bits, bool sr,
                          const AdamWScalars& a, int num_sms, cudaStream_t s) {
   aw::Scalars k{};
-  k.b1 = a.b1, k.c1 = a.c1, k.b2 = a.b2, k.c2 = a.c2;
-  k.size = a.size, k.root = a.root, k.eps = a.eps;
+  auto both = [](float x) { return make_float2(x, x); };
+  k.b1 = both(a.b1), k.c1 = both(a.c1), k.b2 = both(a.b2), k.c2 = both(a.c2);
+  k.size = both(a.size), k.minus_size = both(-a.size), k.root = both(a.root), k.eps = both(a.eps);
+  k.up = both(0x1p40f), k.minus_up = both(-0x1p40f), k.half = both(0.5f), k.minus_half = both(-0.5f);
+  k.one = both(1.0f), k.scaled_root = both(a.root * 0x1p-20f);
+  // (2^-63 root, the most that v below 2^-126 adds to eps, rounds off; the divisor stays below 2^24)
+  k.usual = a.root <= 256.0f && a.eps <= 1.0f && a.root * 0x1p-63f <= a.eps * 0x1p-26f;
+  k.up20 = 16, k.up21 = 8;
   k.step = a.step;
   k.first_tensor = static_cast<uint32_t>(first_tensor);
   k.grad_scale = a.grad_scale;

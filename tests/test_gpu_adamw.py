@@ -228,6 +228,32 @@ def test_8bit_moments_near_64_bits(F, sr):
         assert (np.abs(val - want) <= step * (1.0 if sr else 0.5) * (1 + 1e-6) + bound).all()
 
 
+@pytest.mark.gpu
+@pytest.mark.parametrize("spread", [0, 12, 40])
+def test_8bit_update_is_the_correctly_rounded_quotient(F, spread):
+    # size = 1, root = 2, parameters +-0: the new parameter is the quotient m / (2 sqrt(v) + eps) itself, whose
+    # operations round to nearest, so it has to agree to the bit (zeros by their sign); moments over 2^+-spread
+    n, f = 1 << 20, np.float32
+    gen = torch.Generator(device=DEV).manual_seed(spread)
+    rnd = lambda: torch.rand(n, generator=gen, device=DEV)  # noqa: E731
+    wide = lambda k: torch.exp2((rnd() * 2 - 1) * k)  # noqa: E731
+    block = lambda lo, hi: (rnd()[:n // 128] * (hi - lo) + lo).to(torch.uint8)  # noqa: E731
+    for trial in range(8):
+        g = torch.randn(n, generator=gen, device=DEV) * wide(spread) * (rnd() > 0.1)
+        g[::7] *= -0.0
+        m8 = (torch.randn(n, generator=gen, device=DEV) * 60).clamp(-448, 448).to(KINDS[0])
+        v8 = (rnd() * 16 * wide(4)).to(KINDS[1])
+        ms, vs = block(110 - spread, 118 + spread / 2), block(110 - 2 * spread, 112 + spread / 2)
+        p = torch.where(rnd() < 0.5, -0.0, 0.0)
+        decoded = lambda c, s: c.float().cpu().numpy() * np.exp2(s.cpu().numpy().astype(f) - f(127)).repeat(128)  # noqa: E731
+        with np.errstate(all="ignore"):
+            m1 = f(0.5) * decoded(m8, ms) + f(0.5) * g.cpu().numpy()
+            v1 = f(0.75) * decoded(v8, vs) + f(0.25) * (g.cpu().numpy() * g.cpu().numpy())
+            want = p.cpu().numpy() - m1 / (np.sqrt(v1) * f(2) + f(EPS))
+        F.fp4_adamw_step(F.AdamWTensors([p], [g], [m8], [v8], [ms], [vs]), 1, 0.5, (0.5, 0.75), EPS, seed=trial)
+        assert np.array_equal(p.cpu().numpy().view(np.int32), want.view(np.int32)), trial
+
+
 def test_philox_of_this_file(F, oracle_mod):
     for low, stream, step, seed in ((0, 0, 1, 0), (77, 5, 300, (7 << 32) + 12345), (4_000_000_000, 9, 2, 1 << 63)):
         mine = [int(w[0]) for w in philox(np.array([low], np.uint64), stream, step, seed)]
