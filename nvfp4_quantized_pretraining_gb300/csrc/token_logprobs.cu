@@ -11,7 +11,7 @@
 //
 // Top k: a thread's maximum costs nothing extra.  The readers form 64 groups; the k-th largest group
 // maximum tau is a lower bound of the k-th largest logit (k groups hold an element that large), so only
-// readers whose maximum reaches tau have their vectors read again (from L2), and the elements >= tau, little
+// the quarters of readers' vectors whose maximum reaches tau are read again (from L2), and the elements >= tau, little
 // more than k of them, are ranked by counting.  Too many above tau: the k-th largest of those at hand is a
 // better bound.  Too many equal to it: an ordered scan takes the lowest indices.  NaN: k rounds of a maximum.
 //
@@ -63,6 +63,7 @@ struct Vec<float> {
     return __float_as_uint(max_nan(__uint_as_float(a), __uint_as_float(b)));
   }
   __device__ static __forceinline__ float widest(uint32_t w) { return __uint_as_float(w); }
+  __device__ static __forceinline__ uint16_t round_up(float v) { return __bfloat16_as_ushort(__float2bfloat16_ru(v)); }
   __device__ static __forceinline__ float load(const float* p) { return *p; }
   __device__ static __forceinline__ void store(float* p, float v) { *p = v; }
 };
@@ -88,6 +89,7 @@ struct Vec<__nv_bfloat16> {
     return r;
   }
   __device__ static __forceinline__ float widest(uint32_t w) { return max_nan(bf16_lo(w), bf16_hi(w)); }
+  __device__ static __forceinline__ uint16_t round_up(float v) { return __float_as_uint(v) >> 16; }  // (a BF16 value)
   __device__ static __forceinline__ float load(const __nv_bfloat16* p) { return __bfloat162float(*p); }
   __device__ static __forceinline__ void store(__nv_bfloat16* p, float v) { *p = __float2bfloat16_rn(v); }
 };
@@ -143,33 +145,44 @@ __device__ __forceinline__ RowCut cut_row(const T* row, uint32_t V) {
 constexpr int kReaders = 256;
 // One joining warp keeps up with the readers; three, each on every third row, where they find the top k.
 __host__ __device__ constexpr int joiners_of(bool top) { return top ? 3 : 1; }
-__host__ __device__ constexpr int buffers_of(bool top) { return top ? 3 : 2; }
+__host__ __device__ constexpr int buffers_of(bool top) { return top ? 4 : 2; }
 constexpr int kPerSm = 3;  // CTAs
 // With the top k, the 56 registers a thread that three CTAs leave are split anew: 48 to the readers (two warpgroups), 72
 // to the copying and joining warps (one): 2 x 128 x 48 + 128 x 72 = 384 x 56.  (Both roles within 56 spilled, every
-// spilled word a miss in the little L1 left; two CTAs of 72 a thread took 112 us for 8192 x 32000 BF16, top 5, these 108.)
+// spilled word a miss in the little L1 left; two CTAs of 72 a thread took 112 us for 8192 x 32000 BF16, top 5, when these took 108; now 104.)
 constexpr int kReaderRegs = 48, kJoinerRegs = 72;
 __host__ __device__ constexpr int threads_of(bool top) { return kReaders + 32 + 32 * joiners_of(top); }
 constexpr int kStageVecs = 1024;
-// (two stages with the top k: three leave the joining warps' other reads next to no L1; 8192 x 32000 BF16, top 20:
-// 126 us with two, 164 with three)
+// Maxima are kept per quarter of a reader's vectors too, for the top k to read again no more than those (456 x 131072
+// BF16, top 20: 30 us; 42 with whole readers' vectors read again).
+constexpr int kSegments = 4;
+// (two stages with the top k, whose lists take the rest of the shared memory)
 __host__ __device__ constexpr int stages_of(bool top) { return top ? 2 : 3; }
 __host__ __device__ constexpr int ring_bytes(bool top) { return stages_of(top) * kStageVecs * 16; }
 constexpr int kMaxCluster = 8;
+constexpr int kItems = 256;  // segments that are read again, at a time
+constexpr int kBatch = 4;    // vectors of a lane that are read again at once
 
 // What readers leave of a row: per thread the true maximum (-inf: only banned tokens), and the sums relative to
 // reference(max(maximum, -far)).
+template <bool TOP>
 struct Partials {
   float m[kReaders], s[kReaders], e[kReaders];
+  uint16_t segment[TOP ? kSegments * kReaders : 1];  // per segment and thread: the maximum, as BF16 rounded up
 };
+// A share's stages in kSegments runs of `stages` each (the last ones may be empty).
+__device__ __forceinline__ uint32_t segment_stages(uint32_t vecs) {
+  return ((vecs + kStageVecs - 1) / kStageVecs + kSegments - 1) / kSegments;
+}
 template <bool TOP>
 struct Scratch {  // a joining warp's
-  uint4 in[4 * 32];
+  uint4 in[kBatch * 32];
   uint4 hit[kCap];
   uint64_t above[kCap], equal[kCap / 2];
   uint64_t top[kMaxTop];
   uint32_t hit_at[kCap];
   uint8_t list[kReaders];
+  uint16_t item[kItems];
 };
 template <>
 struct Scratch<false> {};
@@ -215,7 +228,7 @@ __device__ __forceinline__ Share<T> share_of(const LogprobArgs& a, int64_t t, ui
 // The top k of a share by one warp, into x.top (0: nothing left).  maxima: the readers' (shared memory).
 
 template <typename T>
-__device__ __forceinline__ void share_top(const Share<T> h, const float* maxima, float edge, bool odd, uint32_t k,
+__device__ __forceinline__ void share_top(const Share<T> h, const Partials<true>& part, float edge, bool odd, uint32_t k,
                                        Scratch<true>& x) {
   using V8 = Vec<T>;
   constexpr int N = V8::N;
@@ -227,10 +240,10 @@ __device__ __forceinline__ void share_top(const Share<T> h, const float* maxima,
   const uint32_t edge_key = order_key(edge);
   x.top[lane] = 0;
   // the groups: readers lane, + 32, + 64, + 96, and the same from lane + 128
-  auto key = [&](int i) { return order_key(maxima[lane + 32 * i]); };
+  auto key = [&](int i) { return order_key(part.m[lane + 32 * i]); };
   const uint32_t g0 = max(max(key(0), key(1)), max(key(2), key(3))), g1 = max(max(key(4), key(5)), max(key(6), key(7)));
   uint32_t better0 = 0, better1 = 0;
-#pragma unroll
+#pragma unroll 4
   for (int j = 0; j < 32; ++j) {
     const uint32_t o0 = __shfl_sync(kAll, g0, j), o1 = __shfl_sync(kAll, g1, j);
     better0 += (o0 > g0 || (o0 == g0 && j < lane)) + (o1 > g0);
@@ -245,7 +258,7 @@ __device__ __forceinline__ void share_top(const Share<T> h, const float* maxima,
   auto collect = [&](bool with_equal) {
     uint32_t strips = 0;
     const uint32_t bound = with_equal ? tau : tau + 1;
-#pragma unroll
+#pragma unroll 2
     for (int i = 0; i < 8; ++i) {
       const bool is = key(i) >= bound;
       const uint32_t in = __ballot_sync(kAll, is);
@@ -255,38 +268,66 @@ __device__ __forceinline__ void share_top(const Share<T> h, const float* maxima,
     __syncwarp();
     // vectors with such an element
     const float least = key_value(tau);
-    const uint32_t per = (h.v1 - h.v0 + kReaders - 1) / kReaders;
-    const uint32_t shift = per >= 32 ? 5 : per > 1 ? 32 - __clz(per - 1) : 0;  // 2^shift lanes take a strip's vectors
+    const uint32_t stages = segment_stages(h.v1 - h.v0), per = stages * (kStageVecs / kReaders);
+    // (lane by lane over items x per; 32 lanes on is `step` items and `over_by` vectors on.  Small loops here and below:
+    // for a few rows, straight-line code costs its instruction fetches.)
+    const uint32_t step = 32 / max(per, 1u), over_by = 32 - step * per;
     uint32_t hits = 0;
-    for (uint32_t w0 = 0; w0 < per && hits <= kCap; w0 += 1u << shift) {
-      for (uint32_t q = lane >> shift; q - (lane >> shift) < strips && hits <= kCap; q += 4 * (32 >> shift)) {
+    for (uint32_t p0 = 0; p0 < strips && hits <= kCap; p0 += kItems / kSegments) {
+      uint32_t items = 0;  // segments of threads that hold such an element, up to kItems at a time
+      for (uint32_t i = p0 * kSegments + lane; i - lane < min(p0 * kSegments + kItems, strips * kSegments); i += 32) {
+        const uint32_t g = i % kSegments, who = i < strips * kSegments ? x.list[i / kSegments] : 0;
+        const bool is = i < strips * kSegments && g * stages * kStageVecs < h.v1 - h.v0 &&
+                        order_key(__uint_as_float((uint32_t)part.segment[g * kReaders + who] << 16)) >= bound;
+        const uint32_t in = __ballot_sync(kAll, is);
+        if (is) x.item[items + __popc(in & below)] = static_cast<uint16_t>(g * kReaders + who);
+        items += __popc(in);
+      }
+      __syncwarp();
+      const uint32_t total = items * per;
+      struct At {
+        uint32_t p, v;
+      } next = {lane / max(per, 1u), 0};
+      next.v = lane - next.p * per;
+      auto vector_at = [&](const At& i) {
+        if (i.p >= items) return h.v1;
+        const uint32_t item = x.item[i.p];
+        return h.v0 + item / kReaders * per * kReaders + item % kReaders + i.v * kReaders;
+      };
+      auto advance = [&](At& i) {
+        i.p += step, i.v += over_by;
+        if (i.v >= per) i.v -= per, ++i.p;
+      };
+      for (uint32_t i = 0; i < total && hits <= kCap; i += kBatch * 32) {
+        const uint32_t n = min((uint32_t)kBatch, (total - i + 31) / 32);
+        At same = next;
         // (by asynchronous copies past L1: loads would each hold a line of the little L1 that the ring leaves)
-        uint32_t at[4];
-#pragma unroll
-        for (int u = 0; u < 4; ++u) {
-          const uint32_t p = q + u * (32 >> shift), v = w0 + (lane & ((1u << shift) - 1));
-          at[u] = p < strips && v < per ? h.v0 + x.list[p] + v * kReaders : h.v1;
-          if (at[u] < h.v1)
-            asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(&x.in[u * 32 + lane])), "l"(vec + at[u])
+#pragma unroll 1
+        for (uint32_t u = 0; u < n; ++u, advance(next)) {
+          const uint32_t at = vector_at(next);
+          if (at < h.v1)
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(&x.in[u * 32 + lane])), "l"(vec + at)
                          : "memory");
         }
         asm volatile("cp.async.wait_all;" ::: "memory");
-#pragma unroll
-        for (int u = 0; u < 4; ++u) {
+#pragma unroll 1
+        for (uint32_t u = 0; u < n; ++u, advance(same)) {
+          const uint32_t at = vector_at(same);
           const uint4 w = x.in[u * 32 + lane];  // (its own copy; a lane without a vector has no use for what is there)
           const float most = V8::widest(V8::max1(V8::max1(w.x, w.y), V8::max1(w.z, w.w)));
-          const bool hit = at[u] < h.v1 && (with_equal ? most >= least : most > least);
+          const bool hit = at < h.v1 && (with_equal ? most >= least : most > least);
           const uint32_t in = __ballot_sync(kAll, hit), to = hits + __popc(in & below);
-          if (hit && to < kCap) x.hit[to] = w, x.hit_at[to] = at[u];
+          if (hit && to < kCap) x.hit[to] = w, x.hit_at[to] = at;
           hits += __popc(in);
         }
       }
+      __syncwarp();  // (the items have been read)
     }
     __syncwarp();
-    // their elements; the edge elements as one more round
+    // their elements; the edge elements, if there are any, as one more round
     above = 0, equal = 0;
     const uint32_t listed = min(hits, (uint32_t)kCap);
-    for (uint32_t i = 0; i < listed + 32; i += 32) {
+    for (uint32_t i = 0; i < listed + (h.edges ? 32 : 0); i += 32) {
       uint32_t over = 0, same = 0, first = 0;
       const bool last = i >= listed;
       const T* hit = reinterpret_cast<const T*>(&x.hit[i + lane]);
@@ -430,10 +471,13 @@ __global__ void __launch_bounds__(threads_of(TOP), kPerSm) logprob_kernel(const 
   extern __shared__ uint4 s_ring[];  // [kStages][kStageVecs]
   __shared__ uint64_t s_full[kStages], s_free[kStages], s_done[B], s_read[B];
   __shared__ uint64_t s_pushed;  // rank 0: the other shares have arrived
-  __shared__ Partials s_part[B];
+  __shared__ Partials<TOP> s_part[B];
   __shared__ Sum s_joined[kMaxCluster];
   __shared__ Scratch<TOP> s_scratch[joiners_of(TOP)];
-  __shared__ uint64_t s_joined_top[TOP ? kMaxCluster * kMaxTop : 1];
+  // (the shares' entries, in rank 0: a cluster has one row, so the second joining warp's vectors are free)
+  static_assert(sizeof(Scratch<true>::in) >= kMaxCluster * kMaxTop * 8);
+  uint64_t* s_joined_top = nullptr;
+  if constexpr (TOP) s_joined_top = reinterpret_cast<uint64_t*>(s_scratch[1].in);
   const uint32_t rank = cluster_ctarank(), C = cluster_size();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const float k2 = a.scale * kLog2e;
@@ -464,6 +508,13 @@ __global__ void __launch_bounds__(threads_of(TOP), kPerSm) logprob_kernel(const 
       const Share<T> h = share_of<T>(a, t, rank, C);
       float m = neg_inf, c = reference(-far, k2);
       float2 s2 = make_float2(0.0f, 0.0f), e2 = make_float2(0.0f, 0.0f);
+      const uint32_t buf = rows % B;
+      float segment_most = neg_inf;
+      uint32_t left = 0, slot = tid;
+      if (TOP) {
+        left = segment_stages(h.v1 - h.v0);
+        if (ok) ok = mbar_wait(&s_read[buf], ((rows / B) & 1) ^ 1);
+      }
       // (a thread that has met nothing above -far counts its elements as 2^0 of that reference: the first real
       //  maximum, here or in the join, multiplies them by 2^-2^29 = 0)
 #pragma unroll 1
@@ -485,6 +536,11 @@ __global__ void __launch_bounds__(threads_of(TOP), kPerSm) logprob_kernel(const 
         __syncwarp();
         if (lane == 0) mbar_arrive(&s_free[st]);  // (the values are in registers)
         const float most = V8::widest(top);
+        if (TOP) {
+          segment_most = fmaxf(segment_most, most);
+          s_part[buf].segment[slot] = V8::round_up(segment_most);
+          if (--left == 0) left = segment_stages(h.v1 - h.v0), slot += kReaders, segment_most = neg_inf;
+        }
         if (most > m) {  // (NaN: not taken, and s becomes NaN below)
           m = most;
           const float next = reference(fmaxf(m, -far), k2), d = c - next, f = ex2(d);
@@ -506,8 +562,7 @@ __global__ void __launch_bounds__(threads_of(TOP), kPerSm) logprob_kernel(const 
           }
         }
       }
-      const uint32_t buf = rows % B;
-      if (ok) ok = mbar_wait(&s_read[buf], ((rows / B) & 1) ^ 1);
+      if (!TOP && ok) ok = mbar_wait(&s_read[buf], ((rows / B) & 1) ^ 1);
       s_part[buf].m[tid] = m;
       s_part[buf].s[tid] = s2.x + s2.y;
       s_part[buf].e[tid] = e2.x + e2.y;
@@ -544,7 +599,7 @@ __global__ void __launch_bounds__(threads_of(TOP), kPerSm) logprob_kernel(const 
       const int64_t target = a.targets && rank == 0 ? a.targets[t] : -1;
       const float z_target = target >= 0 && target < a.V ? V8::load(h.row + target) : 0.0f;
       if (!mbar_wait_warp(&s_done[buf], (rows / B) & 1)) ok = false;
-      const Partials& part = s_part[buf];
+      const Partials<TOP>& part = s_part[buf];
       float most = edge;
 #pragma unroll 2
       for (int i = lane; i < kReaders; i += 32) most = fmaxf(most, part.m[i]);
@@ -571,7 +626,7 @@ __global__ void __launch_bounds__(threads_of(TOP), kPerSm) logprob_kernel(const 
       odd = __any_sync(0xFFFFFFFFu, odd);
       if (odd) r.s = __uint_as_float(0x7FFFFFFFu);
       if constexpr (TOP) {
-        share_top<T>(h, part.m, edge, odd, a.top_k, x);
+        share_top<T>(h, part, edge, odd, a.top_k, x);
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(&s_read[buf]);  // (the partials are not needed any more)
@@ -609,19 +664,21 @@ __global__ void __launch_bounds__(threads_of(TOP), kPerSm) logprob_kernel(const 
           r.e += (o.e + o.s * d) * f;
         }
         if constexpr (TOP) {
-          // the shares' lists are in order: k rounds of the largest head
-          uint32_t at = 0;
-          uint64_t head = lane < C ? s_joined_top[lane * a.top_k] : 0;
-          for (uint32_t i = 0; i < a.top_k; ++i) {
-            uint64_t best = head;
+          // the shares' lists are in order: each in turn, reversed, against the entries so far; the larger ones of
+          // 32 pairs are the largest 32 of both, bitonic, and five exchanges sort them
+          uint64_t mine = lane < a.top_k ? s_joined_top[lane] : 0;
+#pragma unroll 1
+          for (uint32_t c = 1; c < C; ++c) {
+            const uint32_t from = 31 - lane;
+            const uint64_t other = from < a.top_k ? s_joined_top[c * a.top_k + from] : 0;
+            mine = other > mine ? other : mine;
 #pragma unroll
-            for (int o = 1; o < kMaxCluster; o <<= 1) {
-              const uint64_t other = __shfl_xor_sync(0xFFFFFFFFu, best, o);
-              best = other > best ? other : best;
+            for (int o = 16; o > 0; o >>= 1) {
+              const uint64_t y = __shfl_xor_sync(0xFFFFFFFFu, mine, o);
+              if ((lane & o) == 0 ? y > mine : y < mine) mine = y;
             }
-            if (lane == 0) x.top[i] = best;
-            if (lane < C && head == best) head = ++at < a.top_k ? s_joined_top[lane * a.top_k + at] : 0;
           }
+          if (lane < a.top_k) x.top[lane] = mine;
         }
         __syncwarp();
       }
