@@ -149,7 +149,8 @@ __host__ __device__ constexpr int buffers_of(bool top) { return top ? 4 : 2; }
 constexpr int kPerSm = 3;  // CTAs
 // With the top k, the 56 registers a thread that three CTAs leave are split anew: 48 to the readers (two warpgroups), 72
 // to the copying and joining warps (one): 2 x 128 x 48 + 128 x 72 = 384 x 56.  (Both roles within 56 spilled, every
-// spilled word a miss in the little L1 left; two CTAs of 72 a thread took 112 us for 8192 x 32000 BF16, top 5, when these took 108; now 104.)
+// spilled word a miss in the little L1 left; two CTAs of 72 a thread took 112 us for 8192 x 32000 BF16, top 5, when
+// these took 108; with the second reads as they are now, 104.)
 constexpr int kReaderRegs = 48, kJoinerRegs = 72;
 __host__ __device__ constexpr int threads_of(bool top) { return kReaders + 32 + 32 * joiners_of(top); }
 constexpr int kStageVecs = 1024;
