@@ -1,9 +1,14 @@
 // Y = X W^T for a few tokens (at most 16), the FP8 linear layer of generation: every weight is read for a handful of
-// rows, so the call is bound by the weights' bytes and, below some ten megabytes, by latency.  One launch: a CTA takes
-// 16 R rows of W, its 8 warps a share of K each; a warp quantizes the tokens' block of 128 itself, in registers, in the
-// layout of the MMA's operand (no second kernel, no shared-memory staging, no scales in memory), multiplies with
-// mma.sync m16n8k32 (E4M3, FP32 accumulation; at this width the tensor pipe is idle anyway) and applies the two
-// power-of-two scales per block of 128.  Shares are added in shared memory in a fixed order, and Y is rounded once.
+// rows, so the call is bound by the weights' bytes and, below some ten megabytes, by latency.  One launch, a CTA per SM:
+// its 16 warps share K by blocks of 128 and walk the rows of W, 16 at a time.  Each warp first starts its first weights on
+// their way, then quantizes the tokens' blocks that it multiplies by, once, into shared memory in the layout of the MMA's
+// operand (no second kernel, no scales in global memory).  Weights come by asynchronous copies into a ring of the warp's
+// own (loads into registers waited for the newest as well as the oldest: 32000 x 2048 in 17.8 us instead of 14.7), are
+// multiplied with mma.sync m16n8k32 (E4M3, FP32 accumulation; at this width the tensor pipe is idle anyway) and take the
+// two power-of-two scales per block of 128.  The warps' shares are added in shared memory in a fixed order, four groups
+// of rows at a time (a barrier for each: 16.2 us), and Y is rounded once.
+// One token, weights not in L2: 32000 x 2048 in 14.7 us, 4.5 TB/s; 2048 x 5632 in 7.9 us; 5632 x 2048 in 6.2 us, of which
+// about 3 are an empty call's.
 //
 // K is permuted the same way in both operands so that a lane's 16 bytes of a row are 16 consecutive codes: of 64
 // elements of K, lane q of a quad holds k = 16 q .. 16 q + 15, words 0 and 1 for one MMA, 2 and 3 for the next.
@@ -17,7 +22,8 @@
 namespace nvfp4 {
 namespace few {
 
-constexpr int kWarps = 8, kThreads = kWarps * 32;
+constexpr int kWarps = 16, kThreads = kWarps * 32, kAhead = 3;
+constexpr int kBlockBytes = 64 * 16 + 32;  // eight tokens' codes of a block of 128, and their scales
 
 struct Args {
   const __nv_bfloat16* x;
@@ -62,52 +68,67 @@ __device__ __forceinline__ uint32_t codes4(uint32_t w0, uint32_t w1, float inv) 
 }
 __device__ __forceinline__ bool odd_half(uint32_t h) { return (h & 0x7FFFu) >= 0x7F80u; }
 
-template <int NT, int R, bool WIDE>
-__global__ void __launch_bounds__(kThreads) few_kernel(const Args a) {
-  __shared__ float s_sum[kWarps][NT * 8][R * 16 + 1];
+// What a warp multiplies at a time, 16 rows x 128 of the weights, lane by lane: rows g and 8 + g, elements 16 q.. and
+// 64 + 16 q..; and the rows' words of scales.
+struct Item {
+  uint4 w[2][2][32];
+  uint32_t scale[16];
+};
+__device__ __forceinline__ void copy16(void* to, const void* from) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(to)), "l"(from) : "memory");
+}
+__device__ __forceinline__ void copy4(void* to, const void* from) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(to)), "l"(from) : "memory");
+}
+
+template <int NT, bool WIDE>
+__global__ void __launch_bounds__(kThreads, 1) few_kernel(const Args a) {
+  extern __shared__ uint4 s_raw[];  // the warps' rings; codes [KB][NT][2][32], lane by lane; their scales [KB][NT * 8]
+  constexpr uint32_t kHeld = 4 / NT;  // groups of rows whose shares wait to be added
+  __shared__ float s_sum[kHeld][kWarps][NT * 8][17];
   pdl_trigger();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, q = lane & 3;
-  const uint32_t n0 = blockIdx.x * (16 * R), KB = (a.K + 127) / 128, atoms = (KB + 3) / 4;
-  float sum[R][NT][4];
-#pragma unroll
-  for (int r = 0; r < R; ++r)
-#pragma unroll
-    for (int t = 0; t < NT; ++t)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) sum[r][t][i] = 0.0f;
-  const uint8_t* rows[2 * R];
-  uint32_t row[2 * R];
-#pragma unroll
-  for (int i = 0; i < 2 * R; ++i) {
-    row[i] = min(n0 + i * 8 + g, a.N - 1);  // (a row past the tensor: the last one again, its results are not stored)
-    rows[i] = a.w + (size_t)row[i] * a.pitch + q * 16;
-  }
+  const uint32_t KB = (a.K + 127) / 128, atoms = (KB + 3) / 4, groups = (a.N + 15) / 16;
+  Item* ring = reinterpret_cast<Item*>(s_raw) + warp * kAhead;
+  uint4* s_codes = reinterpret_cast<uint4*>(reinterpret_cast<Item*>(s_raw) + kWarps * kAhead);
+  float* s_scale = reinterpret_cast<float*>(s_codes + KB * NT * 64);
   pdl_wait();
-  for (uint32_t kb = warp; kb < KB; kb += kWarps) {
-    uint4 w[2 * R][2];
-    uint32_t ws[2 * R];
+  // ---- the first weights, on their way while the tokens are quantized
+  struct Walk {
+    uint32_t group, kb;
+  } load = {blockIdx.x, (uint32_t)warp}, use = load;
+  auto step = [&](Walk& i) {
+    i.kb += kWarps;
+    if (i.kb >= KB) i.kb = warp, i.group += gridDim.x;
+  };
+  auto fetch = [&](Item& it) {
+    if (load.group < groups && load.kb < KB) {
 #pragma unroll
-    for (int i = 0; i < 2 * R; ++i) {
-      w[i][0] = *reinterpret_cast<const uint4*>(rows[i] + kb * 128);
-      w[i][1] = *reinterpret_cast<const uint4*>(rows[i] + kb * 128 + 64);
-      ws[i] = a.w_scales[sf_offset(row[i], kb, atoms)];
+      for (int i = 0; i < 2; ++i) {
+        const uint32_t row = min(load.group * 16 + i * 8 + g, a.N - 1);  // (past the tensor: the last row, not stored)
+        const uint8_t* p = a.w + (size_t)row * a.pitch + load.kb * 128 + q * 16;
+        copy16(&it.w[i][0][lane], p);
+        copy16(&it.w[i][1][lane], p + 64);
+        if (q == i) copy4(&it.scale[i * 8 + g], a.w_scales + sf_offset(row, load.kb & ~3u, atoms));
+      }
     }
-    // the tokens' block: lane holds token 8 t + g's elements 16 q.. and 64 + 16 q..
-    uint32_t x[NT][2][8];
+    asm volatile("cp.async.commit_group;" ::: "memory");
+    step(load);
+  };
 #pragma unroll
-    for (int t = 0; t < NT; ++t)
+  for (int u = 0; u < kAhead; ++u) fetch(ring[u]);
+  // ---- the tokens' blocks that this warp multiplies by: token 8 t + g's elements 16 q.. and 64 + 16 q..
+  for (uint32_t kb = warp; kb < KB; kb += kWarps) {
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+      uint32_t x[2][8], m = 0;
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         const uint32_t k = kb * 128 + h * 64 + q * 16, token = t * 8 + g;
-        load16<WIDE>(x[t][h], a.x + (int64_t)token * a.ldx + k, token < a.T ? (int)a.K - (int)k : 0);
+        load16<WIDE>(x[h], a.x + (int64_t)token * a.ldx + k, token < a.T ? (int)a.K - (int)k : 0);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) m = __vmaxu2(m, x[h][i] & 0x7FFF7FFFu);
       }
-#pragma unroll
-    for (int t = 0; t < NT; ++t) {
-      uint32_t m = 0;
-#pragma unroll
-      for (int h = 0; h < 2; ++h)
-#pragma unroll
-        for (int i = 0; i < 8; ++i) m = __vmaxu2(m, x[t][h][i] & 0x7FFF7FFFu);
       uint32_t most = max(m & 0xFFFFu, m >> 16);
       most = max(most, __shfl_xor_sync(0xFFFFFFFFu, most, 1));
       most = max(most, __shfl_xor_sync(0xFFFFFFFFu, most, 2));
@@ -118,7 +139,7 @@ __global__ void __launch_bounds__(kThreads) few_kernel(const Args a) {
         for (int h = 0; h < 2; ++h)
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
-            const uint32_t lo = x[t][h][i] & 0x7FFFu, hi = x[t][h][i] >> 16 & 0x7FFFu;
+            const uint32_t lo = x[h][i] & 0x7FFFu, hi = x[h][i] >> 16 & 0x7FFFu;
             most = max(most, max(lo < 0x7F80u ? lo : 0u, hi < 0x7F80u ? hi : 0u));
           }
         most = max(most, __shfl_xor_sync(0xFFFFFFFFu, most, 1));
@@ -126,73 +147,105 @@ __global__ void __launch_bounds__(kThreads) few_kernel(const Args a) {
       }
       const uint32_t byte = fp8_scale_byte(most << 16, kTopE4M3);
       const float inv = fp8_scale_inverse(byte);
-      uint32_t b[2][4];
 #pragma unroll
-      for (int h = 0; h < 2; ++h)
+      for (int h = 0; h < 2; ++h) {
+        uint32_t b[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const uint32_t w0 = x[t][h][2 * i], w1 = x[t][h][2 * i + 1];
-          b[h][i] = codes4(w0, w1, inv);
+          const uint32_t w0 = x[h][2 * i], w1 = x[h][2 * i + 1];
+          b[i] = codes4(w0, w1, inv);
           if (odd) {
-            if (odd_half(w0)) b[h][i] |= 0x0000007Fu;
-            if (odd_half(w0 >> 16)) b[h][i] |= 0x00007F00u;
-            if (odd_half(w1)) b[h][i] |= 0x007F0000u;
-            if (odd_half(w1 >> 16)) b[h][i] |= 0x7F000000u;
+            if (odd_half(w0)) b[i] |= 0x0000007Fu;
+            if (odd_half(w0 >> 16)) b[i] |= 0x00007F00u;
+            if (odd_half(w1)) b[i] |= 0x007F0000u;
+            if (odd_half(w1 >> 16)) b[i] |= 0x7F000000u;
           }
         }
-      // the scales of the two tokens whose results this lane holds
-      const float sx = fp8_scale_value(byte);
-      const float s0 = __shfl_sync(0xFFFFFFFFu, sx, q * 8), s1 = __shfl_sync(0xFFFFFFFFu, sx, q * 8 + 4);
+        s_codes[((kb * NT + t) * 2 + h) * 32 + lane] = make_uint4(b[0], b[1], b[2], b[3]);
+      }
+      if (q == 0) s_scale[(kb * NT + t) * 8 + g] = fp8_scale_value(byte);
+    }
+  }
+  // ---- 16 rows at a time
+  float sum[NT][4];
 #pragma unroll
-      for (int r = 0; r < R; ++r) {
+  for (int t = 0; t < NT; ++t)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) sum[t][i] = 0.0f;
+  uint32_t held = 0, slot = 0;
+  while (use.group < groups) {
+    asm volatile("cp.async.wait_group %0;" ::"n"(kAhead - 1) : "memory");
+    __syncwarp();
+    Item& it = ring[slot];
+    if (use.kb < KB) {
+      const uint32_t at = 8 * (use.kb & 3);
+      const float wl = fp8_scale_value(it.scale[g] >> at & 0xFFu), wh = fp8_scale_value(it.scale[8 + g] >> at & 0xFFu);
+      const uint4 lo[2] = {it.w[0][0][lane], it.w[0][1][lane]}, hi[2] = {it.w[1][0][lane], it.w[1][1][lane]};
+#pragma unroll
+      for (int t = 0; t < NT; ++t) {
         float c[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          const uint4 &lo = w[2 * r][h], &hi = w[2 * r + 1][h];
-          mma_e4m3(c, lo.x, hi.x, lo.y, hi.y, b[h][0], b[h][1]);
-          mma_e4m3(c, lo.z, hi.z, lo.w, hi.w, b[h][2], b[h][3]);
+          const uint4 b = s_codes[((use.kb * NT + t) * 2 + h) * 32 + lane];
+          mma_e4m3(c, lo[h].x, hi[h].x, lo[h].y, hi[h].y, b.x, b.y);
+          mma_e4m3(c, lo[h].z, hi[h].z, lo[h].w, hi[h].w, b.z, b.w);
         }
-        // (each product of two scales by itself could leave FP32's range where the result does not)
-        const float wl = fp8_scale_value(ws[2 * r]), wh = fp8_scale_value(ws[2 * r + 1]);
-        sum[r][t][0] += c[0] * wl * s0;
-        sum[r][t][1] += c[1] * wl * s1;
-        sum[r][t][2] += c[2] * wh * s0;
-        sum[r][t][3] += c[3] * wh * s1;
+        // (the scales of the two tokens whose results this lane holds; a product of two scales by itself could
+        // leave FP32's range where the result does not)
+        const float2 sx = *reinterpret_cast<const float2*>(&s_scale[(use.kb * NT + t) * 8 + 2 * q]);
+        sum[t][0] += c[0] * wl * sx.x;
+        sum[t][1] += c[1] * wl * sx.y;
+        sum[t][2] += c[2] * wh * sx.x;
+        sum[t][3] += c[3] * wh * sx.y;
+      }
+    }
+    __syncwarp();  // (the item has been read)
+    fetch(it);
+    slot = slot + 1 == kAhead ? 0 : slot + 1;
+    const uint32_t group = use.group;
+    step(use);
+    if (use.group != group) {
+#pragma unroll
+      for (int t = 0; t < NT; ++t) {
+        s_sum[held][warp][t * 8 + 2 * q][g] = sum[t][0];
+        s_sum[held][warp][t * 8 + 2 * q + 1][g] = sum[t][1];
+        s_sum[held][warp][t * 8 + 2 * q][8 + g] = sum[t][2];
+        s_sum[held][warp][t * 8 + 2 * q + 1][8 + g] = sum[t][3];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) sum[t][i] = 0.0f;
+      }
+      if (++held == kHeld || use.group >= groups) {  // the shares of K, in order
+        __syncthreads();
+        const uint32_t in = threadIdx.x % 16, token = threadIdx.x / 16 % (NT * 8), i = threadIdx.x / (NT * 128);
+        const uint32_t row = (group - (held - 1 - i) * gridDim.x) * 16 + in;
+        if (i < held && token < a.T && row < a.N) {
+          float v = s_sum[i][0][token][in];
+#pragma unroll
+          for (int w = 1; w < kWarps; ++w) v += s_sum[i][w][token][in];
+          a.y[(int64_t)token * a.ldy + row] = __float2bfloat16_rn(v);
+        }
+        held = 0;
+        __syncthreads();
       }
     }
   }
-#pragma unroll
-  for (int r = 0; r < R; ++r)
-#pragma unroll
-    for (int t = 0; t < NT; ++t) {
-      s_sum[warp][t * 8 + 2 * q][r * 16 + g] = sum[r][t][0];
-      s_sum[warp][t * 8 + 2 * q + 1][r * 16 + g] = sum[r][t][1];
-      s_sum[warp][t * 8 + 2 * q][r * 16 + 8 + g] = sum[r][t][2];
-      s_sum[warp][t * 8 + 2 * q + 1][r * 16 + 8 + g] = sum[r][t][3];
-    }
-  __syncthreads();
-  for (uint32_t i = threadIdx.x; i < NT * 8 * R * 16; i += kThreads) {
-    const uint32_t token = i / (R * 16), in = i % (R * 16);
-    if (token >= a.T || n0 + in >= a.N) continue;
-    float v = s_sum[0][token][in];
-#pragma unroll
-    for (int w = 1; w < kWarps; ++w) v += s_sum[w][token][in];
-    a.y[(int64_t)token * a.ldy + n0 + in] = __float2bfloat16_rn(v);
-  }
 }
 
-template <int NT, int R>
-static cudaError_t launch(const Args& a, bool wide, cudaStream_t s) {
-  const dim3 grid((a.N + 16 * R - 1) / (16 * R));
-  const cudaError_t e = wide ? launch_pdl(few_kernel<NT, R, true>, grid, dim3(kThreads), 0, s, a)
-                             : launch_pdl(few_kernel<NT, R, false>, grid, dim3(kThreads), 0, s, a);
+template <int NT, bool WIDE>
+static cudaError_t launch(const Args& a, int num_sms, cudaStream_t s) {
+  auto kernel = few_kernel<NT, WIDE>;
+  static const cudaError_t attr_err =
+      cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kWarps * kAhead * (int)sizeof(Item) + kFp8FewBlocks * kBlockBytes);
+  if (attr_err != cudaSuccess) return attr_err;
+  const uint32_t groups = (a.N + 15) / 16, sms = static_cast<uint32_t>(num_sms);
+  const size_t smem = kWarps * kAhead * sizeof(Item) + (size_t)((a.K + 127) / 128) * NT * kBlockBytes;
+  const cudaError_t e = launch_pdl(kernel, dim3(groups < sms ? groups : sms), dim3(kThreads), smem, s, a);
   count_launch();
   return e;
 }
 template <int NT>
-static cudaError_t launch_rows(const Args& a, bool wide, int num_sms, cudaStream_t s) {
-  // 32 rows a CTA halve the work on the tokens; 16 where 32 would leave SMs without a CTA
-  return a.N >= 32 * (uint32_t)num_sms ? launch<NT, 2>(a, wide, s) : launch<NT, 1>(a, wide, s);
+static cudaError_t launch_wide(const Args& a, bool wide, int num_sms, cudaStream_t s) {
+  return wide ? launch<NT, true>(a, num_sms, s) : launch<NT, false>(a, num_sms, s);
 }
 
 }  // namespace few
@@ -203,7 +256,7 @@ cudaError_t launch_fp8_few(const void* x, int64_t T, int64_t K, int64_t ldx, con
                     static_cast<const uint8_t*>(w_scales), static_cast<__nv_bfloat16*>(y), ldy, fp8_pitch(K),
                     static_cast<uint32_t>(T), static_cast<uint32_t>(N), static_cast<uint32_t>(K)};
   const bool wide = (reinterpret_cast<uintptr_t>(x) & 15u) == 0 && (ldx % 8 == 0 || T == 1);
-  return T <= 8 ? few::launch_rows<1>(a, wide, num_sms, s) : few::launch_rows<2>(a, wide, num_sms, s);
+  return T <= 8 ? few::launch_wide<1>(a, wide, num_sms, s) : few::launch_wide<2>(a, wide, num_sms, s);
 }
 
 }  // namespace nvfp4

@@ -248,9 +248,14 @@ cudaError_t launch_fp8_gemm(const Fp8GemmArgs& g, cudaStream_t s);
 // Two independent products, in one launch where that helps.
 cudaError_t launch_fp8_gemm_two(const Fp8GemmArgs& a, const Fp8GemmArgs& b, cudaStream_t s);
 // Y (T x N BF16, pitch ldy) = X W^T for at most 16 tokens, X quantized on the way; fp8_few() says whether that beats a
-// quantizer and the GEMM: up to 8 tokens always (5632 x 2048: 5.0 against 10.4 us, 32000 x 2048: 14 against 19), to 16
-// while the weights are small (8.9 against 10.4 us, but 28 against 19).
-inline bool fp8_few(int64_t T, int64_t N, int64_t K) { return T <= 8 || (T <= 16 && N * K <= (int64_t(16) << 20)); }
+// quantizer and the GEMM: to 8 tokens (5632 x 2048: 6.2 against 9.8 us, 32000 x 2048: 14.7 against 17.2, 8192 x 8192: 17.8
+// against 18.8), to 16 while the weights are small (8.4 against 9.8 us, but 22 against 17.2).  The tokens' codes stay in
+// shared memory, kFp8FewBlocks blocks of 128 for each eight tokens.
+constexpr int kFp8FewBlocks = 84;
+inline bool fp8_few(int64_t T, int64_t N, int64_t K) {
+  const int64_t blocks = (K + 127) / 128;
+  return (T <= 8 && blocks <= kFp8FewBlocks) || (T <= 16 && blocks * 2 <= kFp8FewBlocks && N * K <= (int64_t(16) << 20));
+}
 cudaError_t launch_fp8_few(const void* x, int64_t T, int64_t K, int64_t ldx, const void* w_codes, const void* w_scales,
                            int64_t N, void* y, int64_t ldy, int num_sms, cudaStream_t s);
 cudaError_t fp8_status_read_clear(unsigned int* out, cudaStream_t s);

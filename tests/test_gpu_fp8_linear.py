@@ -204,6 +204,22 @@ def test_few_tokens(F, M, N, K):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("M,N,K", [(1, 20011, 130), (8, 14593, 140), (5, 12200, 2500), (3, 40, 10752), (2, 40, 10900),
+                                   (12, 12000, 200), (16, 2500, 5000), (13, 100, 5500), (1, 2400, 1), (9, 2433, 100)])
+def test_few_tokens_many_rows_or_a_long_axis(F, M, N, K):
+    # several groups of 16 rows per CTA, whole and partial batches of them; more and fewer blocks of K than warps; the
+    # longest K that the one launch takes and longer ones
+    x, w = make(M, K, M).to(DEV), (make(N, K, 5).float() * 0.02).bfloat16().to(DEV)
+    Wq = F.fp4_fp8_quantize(w, 128)
+    y = torch.full((M, N + 5), 7.0, dtype=torch.bfloat16, device=DEV)
+    F.fp4_fp8_linear_fwd(x, Wq, Y=y[:, :N], save=False)
+    torch.cuda.synchronize()
+    F.fp4_check_status()
+    assert (y[:, N:] == 7.0).all()
+    near(y[:, :N], quantize(x.double().cpu().numpy(), 1)[2], quantize(w.double().cpu().numpy(), 128)[2], True, "y")
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("M,N,K", [(1, 1, 1), (1, 256, 384), (130, 300, 257), (257, 1000, 520), (640, 512, 256)])
 def test_linear(F, M, N, K):
     x, w, dy = make(M, K, 1).to(DEV), make(N, K, 2).to(DEV), make(M, N, 3).to(DEV)
