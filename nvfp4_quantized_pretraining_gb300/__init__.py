@@ -562,15 +562,14 @@ def _check_fp8(q, rows: int, cols: int, device, name: str) -> None:
 
 
 def _out_2d(t, rows: int, cols: int, dtypes, device, name: str) -> torch.Tensor:
-    """``t`` checked, or a new rows x cols tensor whose rows start on 16 bytes (so that kernels store wide)."""
+    """``t`` checked, or a new rows x cols tensor with a pitch of whole eights (so that kernels store wide)."""
     if t is not None:
         _check_out(t, (rows, cols), dtypes, device, name)
         return t
     dtype = dtypes[0]
-    unit = 16 // dtype.itemsize
-    if cols % unit == 0:
+    if cols % 8 == 0:
         return torch.empty((rows, cols), dtype=dtype, device=device)
-    return torch.empty((rows, -(-cols // unit) * unit), dtype=dtype, device=device)[:, :cols]
+    return torch.empty((rows, -(-cols // 8) * 8), dtype=dtype, device=device)[:, :cols]
 
 
 def _matrix(x: torch.Tensor, name: str):

@@ -54,7 +54,7 @@ struct Problem {
   void* C;
   int64_t ldc;
   int c_f32, tma_store;
-  uint32_t vec;                            // C rows allow 16-byte stores
+  uint32_t sectors, vec, pairs;            // C rows allow stores of 32, 16, 4 bytes
 };
 struct Maps {
   CUtensorMap a, b, sa, sb, c;
@@ -124,40 +124,66 @@ __device__ __forceinline__ void tmem_ld_32x32b_x8(uint32_t taddr, uint32_t (&r)[
       : "r"(taddr)
       : "memory");
 }
-// 32 columns (col.., accumulators of this lane's row) of the tile to C.  SWAP: tile rows are C's columns, and the 32
-// lanes of a column store 32 neighbours.
+__device__ __forceinline__ void store_one(const Problem& p, uint32_t row, uint32_t col, float v) {
+  const size_t at = (size_t)row * p.ldc + col;
+  if (p.c_f32) static_cast<float*>(p.C)[at] = v;
+  else static_cast<__nv_bfloat16*>(p.C)[at] = __float2bfloat16_rn(v);
+}
+__device__ __forceinline__ void store_sector(float* p, const uint32_t* v) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(v[0]), "r"(v[1]), "r"(v[2]),
+               "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+               : "memory");
+}
+// 32 columns (col.., accumulators of this lane's row) of the tile to C without TMA.  SWAP: tile rows are C's columns,
+// and the 32 lanes of a column store 32 neighbours.  FP32 rows that start on 16 bytes: each lane its row (a sector at a
+// time).  Else the columns are turned in shared memory (4 KB), word (r, c) at 32 r + (c ^ r), for neighbours too.
 template <bool SWAP>
-__device__ __forceinline__ void store_direct(const Problem& p, const uint32_t (&acc)[32], uint32_t row, uint32_t col) {
+__device__ __forceinline__ void store_direct(const Problem& p, const uint32_t (&acc)[32], uint32_t row0, uint32_t col,
+                                             uint32_t* turn) {
+  const uint32_t lane = threadIdx.x & 31;
   if (SWAP) {
-    if (row >= p.P) return;
-#pragma unroll
-    for (int i = 0; i < 32; ++i) {
-      if (col + i < p.Q) {
-        const float v = __uint_as_float(acc[i]);
-        const size_t at = (size_t)(col + i) * p.ldc + row;
-        if (p.c_f32) static_cast<float*>(p.C)[at] = v;
-        else static_cast<__nv_bfloat16*>(p.C)[at] = __float2bfloat16_rn(v);
-      }
-    }
-    return;
-  }
-  if (row >= p.P || col >= p.Q) return;
-  if (p.c_f32) {
-    float* dst = static_cast<float*>(p.C) + (size_t)row * p.ldc + col;
-    if (p.vec && col + 32 <= p.Q) {
-#pragma unroll
-      for (int i = 0; i < 8; ++i)
-        reinterpret_cast<uint4*>(dst)[i] = make_uint4(acc[4 * i], acc[4 * i + 1], acc[4 * i + 2], acc[4 * i + 3]);
-    } else {
-#pragma unroll
-      for (int i = 0; i < 32; ++i)
-        if (col + i < p.Q) dst[i] = __uint_as_float(acc[i]);
-    }
-  } else {
-    __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(p.C) + (size_t)row * p.ldc + col;
+    if (row0 + lane >= p.P) return;
 #pragma unroll
     for (int i = 0; i < 32; ++i)
-      if (col + i < p.Q) dst[i] = __float2bfloat16_rn(__uint_as_float(acc[i]));
+      if (col + i < p.Q) store_one(p, col + i, row0 + lane, __uint_as_float(acc[i]));
+    return;
+  }
+  if (p.vec && col + 32 <= p.Q) {
+    if (row0 + lane >= p.P) return;
+    uint4* dst = reinterpret_cast<uint4*>(static_cast<float*>(p.C) + (size_t)(row0 + lane) * p.ldc + col);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) dst[i] = make_uint4(acc[4 * i], acc[4 * i + 1], acc[4 * i + 2], acc[4 * i + 3]);
+    return;
+  }
+  __syncwarp();  // (the previous columns have been read)
+#pragma unroll
+  for (uint32_t i = 0; i < 32; ++i) turn[lane * 32 + (i ^ lane)] = acc[i];
+  __syncwarp();
+  if (col + lane < p.Q) {
+    const uint32_t rows = row0 < p.P ? min(32u, p.P - row0) : 0;
+    float* dst = static_cast<float*>(p.C) + (size_t)row0 * p.ldc + col + lane;
+#pragma unroll 8
+    for (uint32_t r = 0; r < rows; ++r, dst += p.ldc) *dst = __uint_as_float(turn[r * 32 + (lane ^ r)]);
+  }
+}
+// A 32 x 32 BF16 chunk of stage_chunk() to rows of any alignment, a row at a time, or two where pairs are aligned.  (Each
+// lane its own row from registers: 1021 x 32003 x 2048 into dense rows took 321 us.)
+__device__ __forceinline__ void store_chunk(const Problem& p, const uint8_t* chunk, uint32_t row0, uint32_t col) {
+  const uint32_t lane = threadIdx.x & 31, rows = row0 < p.P ? min(32u, p.P - row0) : 0;
+  auto at = [&](uint32_t r, uint32_t c) { return chunk + r * 64 + (((c >> 3) ^ ((r >> 1) & 3)) << 4) + (c & 7) * 2; };
+  if (p.pairs) {
+    const uint32_t c = (lane & 15) * 2;
+    uint16_t* dst = static_cast<uint16_t*>(p.C) + (size_t)(row0 + (lane >> 4)) * p.ldc + col + c;
+#pragma unroll 4
+    for (uint32_t r = lane >> 4; r < rows; r += 2, dst += 2 * p.ldc) {
+      const uint32_t w = *reinterpret_cast<const uint32_t*>(at(r, c));
+      if (col + c + 1 < p.Q) *reinterpret_cast<uint32_t*>(dst) = w;
+      else if (col + c < p.Q) *dst = static_cast<uint16_t>(w);
+    }
+  } else if (col + lane < p.Q) {
+    uint16_t* dst = static_cast<uint16_t*>(p.C) + (size_t)row0 * p.ldc + col + lane;
+#pragma unroll 8
+    for (uint32_t r = 0; r < rows; ++r, dst += p.ldc) *dst = *reinterpret_cast<const uint16_t*>(at(r, lane));
   }
 }
 __device__ __forceinline__ uint4 pack8(const float (&v)[8]) {
@@ -353,14 +379,29 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       tc_fence_after();
       if (S > 1) break;  // the partial tile is exchanged below
       const uint32_t row0 = pb * 256 + rank * 128 + quad * 32, col0 = qb * BN + h * (BN / 2);
+      // both buffers' chunks to columns col and col + 32 (TMA clips at the tensor's edges)
+      auto store_both = [&](uint32_t col) {
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (!g.tma_store) {
+          store_chunk(g, buf0, row0, col);
+          store_chunk(g, buf1, row0, col + 32);
+        } else if (lane == 0) {
+          if (row0 < g.P) {
+            if (col < g.Q) tma_store_2d(&tmap_c, buf0, (int32_t)col, (int32_t)row0);
+            if (col + 32 < g.Q) tma_store_2d(&tmap_c, buf1, (int32_t)(col + 32), (int32_t)row0);
+          }
+          bulk_commit_group();
+        }
+      };
+      auto wait_both = [&] {  // the buffers have been read
+        if (lane == 0) bulk_wait_read<0>();
+        __syncwarp();
+      };
       if constexpr (BN == 256 && !SWAP) {
-        if (g.tma_store) {
-          auto store = [&](const uint8_t* chunk, uint32_t col) {  // (clipped at the tensor's edges)
-            if (col < g.Q && row0 < g.P) tma_store_2d(&tmap_c, chunk, (int32_t)col, (int32_t)row0);
-          };
+        if (!g.c_f32) {
           uint32_t ra[32], rb[32], pk[16], pk2[16], pk3[16];
-          if (lane == 0) bulk_wait_read<0>();  // the previous tile's stores have read both buffers
-          __syncwarp();
+          wait_both();  // (by the previous tile's stores)
           tmem_ld_32x32b_x32(tacc, ra);
           tmem_ld_wait(ra);
           tmem_ld_32x32b_x32(tacc + 32, rb);
@@ -376,32 +417,39 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
           tmem_ld_wait(rb);
           release();
           convert(rb, pk3);
-          fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0) {
-            store(buf0, col0);
-            store(buf1, col0 + 32);
-            bulk_commit_group();
-            bulk_wait_read<0>();
-          }
-          __syncwarp();
+          store_both(col0);
+          wait_both();
           stage_chunk(buf0, pk2, lane);
           stage_chunk(buf1, pk3, lane);
-          fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0) {
-            store(buf0, col0 + 64);
-            store(buf1, col0 + 96);
-            bulk_commit_group();
+          store_both(col0 + 64);
+          continue;
+        }
+      }
+      if constexpr (BN >= 128 && !SWAP) {
+        // FP32 rows that start on 32 bytes: all of the warp's columns in registers, then whole sectors, each lane its row,
+        // while the next tile is computed (777 x 5003 x 2048, both gradients, FP32 dW: 32 us,
+        // 40 with the loop below)
+        if (g.c_f32 && g.sectors && col0 + BN / 2 <= g.Q) {
+          uint32_t acc[BN / 64][32];
+#pragma unroll
+          for (int j = 0; j < BN / 64; ++j) tmem_ld_32x32b_x32(tacc + j * 32, acc[j]);
+#pragma unroll
+          for (int j = 0; j < BN / 64; ++j) tmem_ld_wait(acc[j]);
+          release();
+          if (row0 + lane < g.P) {
+            float* dst = static_cast<float*>(g.C) + (size_t)(row0 + lane) * g.ldc + col0;
+#pragma unroll
+            for (int j = 0; j < BN / 64; ++j)
+#pragma unroll
+              for (int i = 0; i < 32; i += 8) store_sector(dst + j * 32 + i, &acc[j][i]);
           }
           continue;
         }
       }
       if constexpr (BN == 128 && !SWAP) {
-        if (g.tma_store) {
+        if (!g.c_f32) {
           uint32_t ra[32], rb[32], pk[16];
-          if (lane == 0) bulk_wait_read<0>();  // the previous tile's stores have read both buffers
-          __syncwarp();
+          wait_both();  // (by the previous tile's stores)
           tmem_ld_32x32b_x32(tacc, ra);
           tmem_ld_wait(ra);
           tmem_ld_32x32b_x32(tacc + 32, rb);
@@ -411,24 +459,17 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
           release();
           convert(rb, pk);
           stage_chunk(buf1, pk, lane);
-          fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0) {
-            if (row0 < g.P) {
-              if (col0 < g.Q) tma_store_2d(&tmap_c, buf0, (int32_t)col0, (int32_t)row0);
-              if (col0 + 32 < g.Q) tma_store_2d(&tmap_c, buf1, (int32_t)(col0 + 32), (int32_t)row0);
-            }
-            bulk_commit_group();
-          }
+          store_both(col0);
           continue;
         }
       }
+      if (lane == 0) bulk_wait_read<0>();  // (the other product's stores)
 #pragma unroll 1
       for (int j = 0; j < BN / 64; ++j) {
         uint32_t acc[32];
         tmem_ld_32x32b_x32(tacc + j * 32, acc);
         tmem_ld_wait(acc);
-        store_direct<SWAP>(g, acc, row0 + lane, col0 + j * 32);
+        store_direct<SWAP>(g, acc, row0, col0 + j * 32, reinterpret_cast<uint32_t*>(buf0));
       }
       release();
     }
@@ -524,15 +565,20 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
                 *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(g.C) + at) = pack8(v);
               }
             }
-          } else {
+          } else if (SWAP) {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              const uint32_t m = SWAP ? col + i : row0 + lane, k = SWAP ? row0 + lane : col + i;  // C's row and column
-              if (row0 + lane < g.P && col + i < g.Q) {
-                if (g.c_f32) static_cast<float*>(g.C)[(size_t)m * g.ldc + k] = v[i];
-                else static_cast<__nv_bfloat16*>(g.C)[(size_t)m * g.ldc + k] = __float2bfloat16_rn(v[i]);
-              }
-            }
+            for (int i = 0; i < 8; ++i)
+              if (row0 + lane < g.P && col + i < g.Q) store_one(g, col + i, row0 + lane, v[i]);
+          } else {  // turned, so that eight lanes store eight neighbours
+            float* turn = reinterpret_cast<float*>(buf);
+            __syncwarp();
+#pragma unroll
+            for (int i = 0; i < 8; ++i) turn[i * 33 + lane] = v[i];
+            __syncwarp();
+            const uint32_t c = lane % 8;
+#pragma unroll 2
+            for (uint32_t r = lane / 8; r < 32; r += 4)
+              if (row0 + r < g.P && col + c < g.Q) store_one(g, row0 + r, col + c, turn[c * 33 + r]);
           }
         }
       }
@@ -641,6 +687,8 @@ static bool set_problem(Params& p, int i, const Operand& P, const Operand& Q, co
   g.c_f32 = a.c_f32;
   const bool aligned = (reinterpret_cast<uintptr_t>(a.C) & 15u) == 0 && (a.ldc * (a.c_f32 ? 4 : 2)) % 16 == 0;
   g.vec = aligned;
+  g.sectors = (reinterpret_cast<uintptr_t>(a.C) & 31u) == 0 && (a.ldc * (a.c_f32 ? 4 : 2)) % 32 == 0;
+  g.pairs = (reinterpret_cast<uintptr_t>(a.C) & 3u) == 0 && a.ldc % 2 == 0;
   g.tma_store = aligned && !a.c_f32 && !SWAP;
   return !g.tma_store || encode_tmap_2d(&m.c, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, a.C, a.N, a.M, (uint64_t)a.ldc * 2, 32, 32,
                                         CU_TENSOR_MAP_SWIZZLE_64B);
