@@ -17,6 +17,11 @@
 //
 // Warps: TMA producer, MMA issuer (pair leader), eight epilogue warps.  Operands past M, N or K are zeros (TMA fill,
 // code padding), stores are clipped.  Every wait is bounded (FP4_ERR_TIMEOUT in the status word).
+//
+// Large products are bound by the tensor pipe and the power it may draw: 8192 x 32000 x 2048 in 309 us (3470 TFLOP/s, tensor
+// pipe 82% busy) alone, 350 in a long run; 8192^3 at 3590 TFLOP/s.  The producer and the issuer stay whole warps that
+// elect a lane per instruction (as branches of one lane they issued a stage in 345 ns instead of 294).
+// 1021 x 32000 x 2048: 48 us (seven rounds of tiles of 256 x 256).
 #include <cudaTypedefs.h>
 #include <cuda_bf16.h>
 

@@ -8,7 +8,9 @@
 //
 // Memory-bound (2 bytes read, 1 written per form and element), and close to bound by issue slots (both forms at
 // 6.8 TB/s leave 21 instructions per element): inputs whose rows start on 16 bytes come by TMA into a ring of tiles that
-// CTAs walk persistently, others by loads, a tile per CTA; both convert a tile with the same code.
+// CTAs walk persistently (two tiles, three CTAs an SM), others by loads, a tile per CTA; both convert a tile with the
+// same code.  8192 x 32000: rows 135 us, columns 143 us, both 197 us (5.3 TB/s, 78% of the copy bandwidth); 8192 x 32003
+// in dense rows: 190, 204 and 283 us.
 #include <cuda_bf16.h>
 
 #include "common.cuh"

@@ -148,6 +148,30 @@ def test_many_equal_logits_give_the_lowest_indices(F, dtype):
 
 @pytest.mark.gpu
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("T,V", [(3, 70001), (600, 20011), (470, 8200), (40, 33000)])
+def test_top_entries_close_together_or_far_apart(F, T, V, dtype):
+    # where a row's largest logits sit: in one thread's vectors, in neighbours, at both ends, spread; and values that
+    # differ by less than a BF16 step (in FP32), thousands of them within one step of the k-th largest
+    z, targets = make(T, V, dtype, V + T)
+    step = 256 * (8 if dtype == torch.bfloat16 else 4)  # elements between two vectors of one thread
+    at = torch.arange(40, device=DEV)
+    z[0, (at * step + 17) % V] = 20 + at.to(dtype) / 8
+    z[1, V // 2 + at] = 20 + at.to(dtype) / 8
+    z[2, at[:20]] = 20 + at[:20].to(dtype) / 8
+    z[2, V - 1 - at[:20]] = 30 - at[:20].to(dtype) / 8
+    if T > 10:
+        z[3] = (1 + torch.rand(V, generator=torch.Generator().manual_seed(1)) * 2.0 ** -9).to(dtype).to(DEV)
+        z[4] = (-1 - torch.rand(V, generator=torch.Generator().manual_seed(2)) * 2.0 ** -9).to(dtype).to(DEV)
+        z[5, ::7] = 15.0
+        z[6] = torch.finfo(dtype).max / 4
+        z[6, ::3] = torch.finfo(dtype).max
+        z[T - 1] = z[0]
+    for k in (1, 5, 32):
+        check_forward(F, z, targets, 1.0, k)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
 @pytest.mark.parametrize("V", [900, 32000, 131072])
 def test_few_tokens_allowed(F, dtype, V):
     # constrained decoding: all but a few tokens banned, by -inf and by the type's lowest value
