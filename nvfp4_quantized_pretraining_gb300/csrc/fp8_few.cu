@@ -1,4 +1,4 @@
-// Y = X W^T for a few tokens (at most 16), the FP8 linear layer of generation: every weight is read for a handful of
+// Y = X W^T for a few tokens (at most 32), the FP8 linear layer of generation: every weight is read for a handful of
 // rows, so the call is bound by the weights' bytes and, below some ten megabytes, by latency.  One launch, a CTA per SM:
 // its 16 warps share K by blocks of 128 and walk the rows of W, 16 at a time.  Each warp first starts its first weights on
 // their way, then quantizes the tokens' blocks that it multiplies by, once, into shared memory in the layout of the MMA's
@@ -256,7 +256,8 @@ cudaError_t launch_fp8_few(const void* x, int64_t T, int64_t K, int64_t ldx, con
                     static_cast<const uint8_t*>(w_scales), static_cast<__nv_bfloat16*>(y), ldy, fp8_pitch(K),
                     static_cast<uint32_t>(T), static_cast<uint32_t>(N), static_cast<uint32_t>(K)};
   const bool wide = (reinterpret_cast<uintptr_t>(x) & 15u) == 0 && (ldx % 8 == 0 || T == 1);
-  return T <= 8 ? few::launch_wide<1>(a, wide, num_sms, s) : few::launch_wide<2>(a, wide, num_sms, s);
+  if (T <= 8) return few::launch_wide<1>(a, wide, num_sms, s);
+  return T <= 16 ? few::launch_wide<2>(a, wide, num_sms, s) : few::launch_wide<4>(a, wide, num_sms, s);
 }
 
 }  // namespace nvfp4

@@ -247,14 +247,15 @@ struct Fp8GemmArgs {
 cudaError_t launch_fp8_gemm(const Fp8GemmArgs& g, cudaStream_t s);
 // Two independent products, in one launch where that helps.
 cudaError_t launch_fp8_gemm_two(const Fp8GemmArgs& a, const Fp8GemmArgs& b, cudaStream_t s);
-// Y (T x N BF16, pitch ldy) = X W^T for at most 16 tokens, X quantized on the way; fp8_few() says whether that beats a
-// quantizer and the GEMM: to 8 tokens (5632 x 2048: 6.2 against 9.8 us, 32000 x 2048: 14.7 against 17.2, 8192 x 8192: 17.8
-// against 18.8), to 16 while the weights are small (8.4 against 9.8 us, but 22 against 17.2).  The tokens' codes stay in
-// shared memory, kFp8FewBlocks blocks of 128 for each eight tokens.
+// Y (T x N BF16, pitch ldy) = X W^T for at most 32 tokens, X quantized on the way; fp8_few() says whether that beats a
+// quantizer and the GEMM: to 8 tokens (5632 x 2048: 6.2 against 9.8 us, 32000 x 2048: 14.7 against 17.2, 8192 x 8192:
+// 17.8 against 18.8), to 16 while the weights are small (5632 x 2048: 8.3 against 9.8 us, but 32000 x 2048: 22 against
+// 17.2), to 32 while they are smaller yet (2048 x 2048: 7.2 against 9.0 us, but 5632 x 2048: 12 against 10).  The tokens'
+// codes stay in shared memory, kFp8FewBlocks blocks of 128 for each eight tokens.
 constexpr int kFp8FewBlocks = 84;
 inline bool fp8_few(int64_t T, int64_t N, int64_t K) {
-  const int64_t blocks = (K + 127) / 128;
-  return (T <= 8 && blocks <= kFp8FewBlocks) || (T <= 16 && blocks * 2 <= kFp8FewBlocks && N * K <= (int64_t(16) << 20));
+  const int64_t groups = T <= 8 ? 1 : T <= 16 ? 2 : 4, most = T <= 8 ? INT64_MAX : int64_t(T <= 16 ? 16 : 6) << 20;
+  return T <= 32 && (K + 127) / 128 * groups <= kFp8FewBlocks && N * K <= most;
 }
 cudaError_t launch_fp8_few(const void* x, int64_t T, int64_t K, int64_t ldx, const void* w_codes, const void* w_scales,
                            int64_t N, void* y, int64_t ldy, int num_sms, cudaStream_t s);

@@ -205,7 +205,8 @@ def test_few_tokens(F, M, N, K):
 
 @pytest.mark.gpu
 @pytest.mark.parametrize("M,N,K", [(1, 20011, 130), (8, 14593, 140), (5, 12200, 2500), (3, 40, 10752), (2, 40, 10900),
-                                   (12, 12000, 200), (16, 2500, 5000), (13, 100, 5500), (1, 2400, 1), (9, 2433, 100)])
+                                   (12, 12000, 200), (16, 2500, 5000), (13, 100, 5500), (1, 2400, 1), (9, 2433, 100),
+                                   (17, 700, 2688), (32, 9001, 390), (25, 500, 2700), (30, 2500, 2600)])
 def test_few_tokens_many_rows_or_a_long_axis(F, M, N, K):
     # several groups of 16 rows per CTA, whole and partial batches of them; more and fewer blocks of K than warps; the
     # longest K that the one launch takes and longer ones
