@@ -229,9 +229,9 @@ def test_8bit_moments_near_64_bits(F, sr):
 
 
 @pytest.mark.gpu
-@pytest.mark.parametrize("spread", [0, 12, 40])
-def test_8bit_update_is_the_correctly_rounded_quotient(F, spread):
-    # size = 1, root = 2, parameters +-0: the new parameter is the quotient m / (2 sqrt(v) + eps) itself, whose
+@pytest.mark.parametrize("spread,eps", [(0, EPS), (12, EPS), (40, EPS), (12, 0.0), (40, 1e-30), (12, 1e-12), (12, 1.0), (0, 1e3)])
+def test_8bit_update_is_the_correctly_rounded_quotient(F, spread, eps):
+    # size = 1, root = 2, parameters +-0: the new parameter is the quotient -m / (2 sqrt(v) + eps) itself, whose
     # operations round to nearest, so it has to agree to the bit (zeros by their sign); moments over 2^+-spread
     n, f = 1 << 20, np.float32
     gen = torch.Generator(device=DEV).manual_seed(spread)
@@ -249,9 +249,11 @@ def test_8bit_update_is_the_correctly_rounded_quotient(F, spread):
         with np.errstate(all="ignore"):
             m1 = f(0.5) * decoded(m8, ms) + f(0.5) * g.cpu().numpy()
             v1 = f(0.75) * decoded(v8, vs) + f(0.25) * (g.cpu().numpy() * g.cpu().numpy())
-            want = p.cpu().numpy() - m1 / (np.sqrt(v1) * f(2) + f(EPS))
-        F.fp4_adamw_step(F.AdamWTensors([p], [g], [m8], [v8], [ms], [vs]), 1, 0.5, (0.5, 0.75), EPS, seed=trial)
-        assert np.array_equal(p.cpu().numpy().view(np.int32), want.view(np.int32)), trial
+            want = p.cpu().numpy() - m1 / (np.sqrt(v1) * f(2) + f(eps))
+        F.fp4_adamw_step(F.AdamWTensors([p], [g], [m8], [v8], [ms], [vs]), 1, 0.5, (0.5, 0.75), eps, seed=trial)
+        got = p.cpu().numpy()
+        bits = lambda a: np.where(np.isnan(a), 1, a.view(np.int32))  # noqa: E731  (0 / 0 without eps)
+        assert np.array_equal(bits(got), bits(want)), trial
 
 
 def test_philox_of_this_file(F, oracle_mod):
