@@ -18,7 +18,7 @@
 // Both directions are bound by memory (2 or 4 bytes per logit forward, twice that backward) and, in BF16, nearly as
 // much by issue slots: 6.8 TB/s leaves 11 instructions per logit.  So maxima are packed BF16, products, sums and
 // additions packed FP32 pairs, and the running maximum is looked at once per 4 vectors.
-// 8192 x 32000 BF16: forward 87 us (6.0 TB/s), with the top 5 104 us, gradient 151 to 163 us (6.4 to 6.9 TB/s).
+// 8192 x 32000 BF16: forward 87 us (6.0 TB/s), with the top 5 101 us, gradient 151 to 163 us (6.4 to 6.9 TB/s).
 #include <cuda_bf16.h>
 
 #include <cstring>
@@ -151,7 +151,7 @@ constexpr int kPerSm = 3;  // CTAs
 // With the top k, the 56 registers a thread that three CTAs leave are split anew: 48 to the readers (two warpgroups), 72
 // to the copying and joining warps (one): 2 x 128 x 48 + 128 x 72 = 384 x 56.  (Both roles within 56 spilled, every
 // spilled word a miss in the little L1 left; two CTAs of 72 a thread took 112 us for 8192 x 32000 BF16, top 5, when
-// these took 108; with the second reads as they are now, 104.)
+// these took 108; with the second reads as they are now, 101.)
 constexpr int kReaderRegs = 48, kJoinerRegs = 72;
 __host__ __device__ constexpr int threads_of(bool top) { return kReaders + 32 + 32 * joiners_of(top); }
 constexpr int kStageVecs = 1024;
@@ -244,15 +244,15 @@ __device__ __forceinline__ void share_top(const Share<T> h, const Partials<true>
   // the groups: readers lane, + 32, + 64, + 96, and the same from lane + 128
   auto key = [&](int i) { return order_key(part.m[lane + 32 * i]); };
   const uint32_t g0 = max(max(key(0), key(1)), max(key(2), key(3))), g1 = max(max(key(4), key(5)), max(key(6), key(7)));
-  uint32_t better0 = 0, better1 = 0;
-#pragma unroll 4
-  for (int j = 0; j < 32; ++j) {
-    const uint32_t o0 = __shfl_sync(kAll, g0, j), o1 = __shfl_sync(kAll, g1, j);
-    better0 += (o0 > g0 || (o0 == g0 && j < lane)) + (o1 > g0);
-    better1 += (o0 >= g1) + (o1 > g1 || (o1 == g1 && j < lane));
+  // their k-th largest, bit by bit; of FP32 logits the upper half alone, rounded down (a bound all the same)
+  uint32_t tau = 0;
+#pragma unroll 1
+  for (uint32_t bit = 0x80000000u; bit >= 0x10000u; bit >>= 1) {
+    const uint32_t at = tau | bit;
+    if (__popc(__ballot_sync(kAll, g0 >= at)) + __popc(__ballot_sync(kAll, g1 >= at)) >= static_cast<int>(k)) tau = at;
   }
-  const uint32_t in0 = __ballot_sync(kAll, better0 == k - 1), in1 = __ballot_sync(kAll, better1 == k - 1);
-  uint32_t tau = in0 ? __shfl_sync(kAll, g0, __ffs(in0) - 1) : __shfl_sync(kAll, g1, __ffs(in1) - 1);
+  if (N == 8 && tau < 0x80000000u) tau |= 0xFFFFu;  // (negative BF16 keys end in ones)
+  tau = max(tau, order_key(__uint_as_float(0xFF800000u)));
 
   uint32_t above = 0, equal = 0;  // entries in the lists
   // Fills the lists with the share's elements above tau and, with_equal, those equal to it; false if they do not fit
