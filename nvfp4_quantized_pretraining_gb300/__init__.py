@@ -767,7 +767,10 @@ def fp4_token_logprobs_bwd(logits: torch.Tensor, saved: TokenLogprobs, targets: 
     _check_vector(saved.top_index, (T, k), torch.int64, dev, "saved.top_index")
     for g, shape, name in ((g_logprob, (T,), "g_logprob"), (g_entropy, (T,), "g_entropy"), (g_top, (T, k), "g_top")):
         _check_vector(g, shape, f32, dev, name)
-    dlogits = torch.empty((T, V), dtype=logits.dtype, device=dev) if dlogits is None else dlogits
+    if dlogits is None:  # (rows that start on 16 bytes where the logits' do, for the kernels that read it next)
+        wide = V + (ld - V) % 8
+        dlogits = torch.empty((T, wide), dtype=logits.dtype, device=dev)
+        dlogits = dlogits if wide == V else dlogits[:, :V]
     _check_out(dlogits, (T, V), logits.dtype, dev, "dlogits")
     ldd = dlogits.stride(0) if T > 1 else max(V, 1)
     _check(lib().fp4_token_logprobs_bwd(logits.data_ptr(), dtype, T, V, ld, saved.temperature, _ptr(targets),

@@ -747,9 +747,53 @@ __global__ void __launch_bounds__(threads_of(TOP), kPerSm) logprob_kernel(const 
 // ---------------------------------------------------------------------------
 constexpr int kBwdThreads = 256, kBwdVecs = 4;
 
-template <typename T, bool TOP>
-__global__ void __launch_bounds__(kBwdThreads, 8) logprob_bwd_kernel(const LogprobBwdArgs a, uint32_t chunks,
-                                                                    const float far, const bool stream) {
+// 16 bytes at p, `off` bytes past a 16-byte boundary: from the two aligned vectors that hold them, or by elements where
+// those reach out of [begin, end).
+template <typename T>
+struct Shifted {
+  uint4 lo, hi;
+  __device__ __forceinline__ void load(const char* p, uint32_t off, const char* begin, const char* end) {
+    const char* b = p - off;
+    if (b >= begin && b + 32 <= end) {
+      lo = *reinterpret_cast<const uint4*>(b);
+      if (off) hi = *reinterpret_cast<const uint4*>(b + 16);
+    } else {
+      uint32_t w[8] = {};
+      for (uint32_t i = 0; i < 16 / sizeof(T); ++i) {
+        const uint32_t at = off + i * sizeof(T);
+        uint32_t v;
+        if (sizeof(T) == 2) v = reinterpret_cast<const uint16_t*>(p)[i];
+        else v = reinterpret_cast<const uint32_t*>(p)[i];
+#pragma unroll
+        for (uint32_t j = 0; j < 8; ++j)
+          if (j == at / 4) w[j] |= v << (at % 4 * 8);
+      }
+      lo = make_uint4(w[0], w[1], w[2], w[3]), hi = make_uint4(w[4], w[5], w[6], w[7]);
+    }
+  }
+  __device__ __forceinline__ uint4 value(uint32_t off) const {
+    uint32_t w[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+    if (off & 8) {
+#pragma unroll
+      for (int j = 0; j < 6; ++j) w[j] = w[j + 2];
+    }
+    if (off & 4) {
+#pragma unroll
+      for (int j = 0; j < 5; ++j) w[j] = w[j + 1];
+    }
+    if (sizeof(T) == 2) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) w[j] = __funnelshift_r(w[j], w[j + 1], (off & 2) * 8);
+    }
+    return make_uint4(w[0], w[1], w[2], w[3]);
+  }
+};
+
+// SHIFT: logits and gradient do not start at the same place between 16-byte boundaries in every row; rows are cut by the
+// gradient's (8192 x 32003 BF16, pitches 32008 and 32003: 193 us; 459 element by element).
+template <typename T, bool TOP, bool SHIFT>
+__global__ void __launch_bounds__(kBwdThreads, SHIFT ? 4 : 8)
+    logprob_bwd_kernel(const LogprobBwdArgs a, uint32_t chunks, const float far, const bool stream) {
   using V8 = Vec<T>;
   constexpr int N = V8::N;
   const int64_t t = blockIdx.x / chunks;
@@ -758,9 +802,7 @@ __global__ void __launch_bounds__(kBwdThreads, 8) logprob_bwd_kernel(const Logpr
   const T* row = static_cast<const T*>(a.logits) + t * a.ld;
   T* out = static_cast<T*>(a.dlogits) + t * a.ldd;
   const float neg_inf = __uint_as_float(0xFF800000u), nan = __uint_as_float(0x7FFFFFFFu);
-  // vectors where source and destination share their alignment, else single elements
-  RowCut cut = cut_row(row, V);
-  const bool wide = (((reinterpret_cast<uintptr_t>(row) ^ reinterpret_cast<uintptr_t>(out)) & 15u) == 0);
+  const RowCut cut = cut_row(out, V);
   constexpr uint32_t kVecs = kBwdThreads * kBwdVecs;
 
   const float m = a.stats[2 * t], s = a.stats[2 * t + 1];
@@ -790,10 +832,8 @@ __global__ void __launch_bounds__(kBwdThreads, 8) logprob_bwd_kernel(const Logpr
   const float own_t = gt * a.scale;
 
   // in place, the entries with gradients of their own are read before anything is written
-  const uint32_t e_lo = wide ? 0 : chunk * kVecs * N;
   auto inside = [&](int64_t at) {  // whether this CTA writes element `at`
     if (at < 0 || at >= a.V) return false;
-    if (!wide) return at >= e_lo && at < (int64_t)e_lo + kVecs * N;
     const int64_t v = at - cut.head;
     if (v < 0 || v >= (int64_t)cut.vecs * N) return chunk == 0;
     return v / N / kVecs == chunk;
@@ -813,52 +853,59 @@ __global__ void __launch_bounds__(kBwdThreads, 8) logprob_bwd_kernel(const Logpr
     if (!TOP && idx == target && z != neg_inf) d += own_t;
     V8::store(out + idx, d);
   };
-  if (wide) {
-    const uint4* vec = reinterpret_cast<const uint4*>(row + cut.head);
-    uint4* dst = reinterpret_cast<uint4*>(out + cut.head);
-    const uint32_t i0 = chunk * kVecs + tid, low = V8::low_bits(-far);
-    const int64_t target_at = target - cut.head;
-    const uint32_t target_vec = target >= 0 && target_at >= 0 && target < a.V ? (uint32_t)(target_at / N) : 0xFFFFFFFFu;
-    const int target_in = (int)(target_at % N);
-    uint4 q[kBwdVecs];
+  const uint4* vec = reinterpret_cast<const uint4*>(row + cut.head);
+  uint4* dst = reinterpret_cast<uint4*>(out + cut.head);
+  const uint32_t i0 = chunk * kVecs + tid, low = V8::low_bits(-far);
+  const int64_t target_at = target - cut.head;
+  const uint32_t target_vec = target >= 0 && target_at >= 0 && target < a.V ? (uint32_t)(target_at / N) : 0xFFFFFFFFu;
+  const int target_in = (int)(target_at % N);
+  uint4 q[kBwdVecs];
+  if constexpr (SHIFT) {
+    const char* begin = static_cast<const char*>(a.logits);
+    const char* end = begin + ((a.T - 1) * a.ld + a.V) * (int64_t)sizeof(T);
+    const uint32_t off = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(vec) & 15u);
+    Shifted<T> two[kBwdVecs];
 #pragma unroll
     for (int u = 0; u < kBwdVecs; ++u)
-      if (i0 + u * kBwdThreads < cut.vecs) q[u] = stream ? __ldcs(vec + i0 + u * kBwdThreads) : vec[i0 + u * kBwdThreads];
+      if (i0 + u * kBwdThreads < cut.vecs)
+        two[u].load(reinterpret_cast<const char*>(vec + i0 + u * kBwdThreads), off, begin, end);
 #pragma unroll
-    for (int u = 0; u < kBwdVecs; ++u) {
-      const uint32_t i = i0 + u * kBwdThreads;
-      if (i >= cut.vecs) break;
-      float f[N], d[N];
-      if (near) {
-        q[u].x = V8::max1(q[u].x, low), q[u].y = V8::max1(q[u].y, low);
-        q[u].z = V8::max1(q[u].z, low), q[u].w = V8::max1(q[u].w, low);
-        V8::unpack(q[u], f);
-#pragma unroll
-        for (int j = 0; j < N; j += 2) {
-          const float2 x = __fmul2_rn(__fadd2_rn(make_float2(f[j], f[j + 1]), make_float2(-m, -m)), make_float2(k2, k2));
-          const float2 y = __fmul2_rn(make_float2(ex2(x.x), ex2(x.y)), __ffma2_rn(make_float2(B, B), x, make_float2(A, A)));
-          d[j] = y.x, d[j + 1] = y.y;
-        }
-      } else {
-        V8::unpack(q[u], f);
-#pragma unroll
-        for (int j = 0; j < N; ++j) d[j] = base(f[j]);
-      }
-      if (!TOP && i == target_vec) {
-#pragma unroll
-        for (int j = 0; j < N; ++j)
-          if (j == target_in && V8::load(row + target) != neg_inf) d[j] += own_t;
-      }
-      if (stream) __stcs(dst + i, V8::pack(d));
-      else dst[i] = V8::pack(d);
-    }
-    if (chunk == 0 && tid < cut.head + cut.tail) one(tid < cut.head ? tid : cut.vecs * N + tid);
+    for (int u = 0; u < kBwdVecs; ++u) q[u] = two[u].value(off);
   } else {
-    for (uint32_t i = tid; i < kVecs * N; i += kBwdThreads) {
-      if (V - e_lo <= i || e_lo >= V) break;
-      one(e_lo + i);
-    }
+#pragma unroll
+    for (int u = 0; u < kBwdVecs; ++u)
+      if (i0 + u * kBwdThreads < cut.vecs)
+        q[u] = stream ? __ldcs(vec + i0 + u * kBwdThreads) : vec[i0 + u * kBwdThreads];
   }
+#pragma unroll
+  for (int u = 0; u < kBwdVecs; ++u) {
+    const uint32_t i = i0 + u * kBwdThreads;
+    if (i >= cut.vecs) break;
+    float f[N], d[N];
+    if (near) {
+      q[u].x = V8::max1(q[u].x, low), q[u].y = V8::max1(q[u].y, low);
+      q[u].z = V8::max1(q[u].z, low), q[u].w = V8::max1(q[u].w, low);
+      V8::unpack(q[u], f);
+#pragma unroll
+      for (int j = 0; j < N; j += 2) {
+        const float2 x = __fmul2_rn(__fadd2_rn(make_float2(f[j], f[j + 1]), make_float2(-m, -m)), make_float2(k2, k2));
+        const float2 y = __fmul2_rn(make_float2(ex2(x.x), ex2(x.y)), __ffma2_rn(make_float2(B, B), x, make_float2(A, A)));
+        d[j] = y.x, d[j + 1] = y.y;
+      }
+    } else {
+      V8::unpack(q[u], f);
+#pragma unroll
+      for (int j = 0; j < N; ++j) d[j] = base(f[j]);
+    }
+    if (!TOP && i == target_vec) {
+#pragma unroll
+      for (int j = 0; j < N; ++j)
+        if (j == target_in && V8::load(row + target) != neg_inf) d[j] += own_t;
+    }
+    if (stream) __stcs(dst + i, V8::pack(d));
+    else dst[i] = V8::pack(d);
+  }
+  if (chunk == 0 && tid < cut.head + cut.tail) one(tid < cut.head ? tid : cut.vecs * N + tid);
   if (TOP) {
     __syncthreads();
     if (mine >= 0 && z_mine != neg_inf) {
@@ -931,8 +978,11 @@ static cudaError_t launch_bwd_t(const LogprobBwdArgs& a, cudaStream_t s) {
   // More than L2 holds (129 MB, for the logits and their gradient): neither is worth keeping there (8192 x 32000 BF16:
   // 171 us with the default policy, 161 streaming); less is, for what reads the gradient next.
   const bool stream = (double)a.T * a.V * sizeof(T) > 64e6;
-  if (a.top_k) lp::logprob_bwd_kernel<T, true><<<grid, lp::kBwdThreads, 0, s>>>(a, (uint32_t)chunks, far, stream);
-  else lp::logprob_bwd_kernel<T, false><<<grid, lp::kBwdThreads, 0, s>>>(a, (uint32_t)chunks, far, stream);
+  const bool shift = ((reinterpret_cast<uintptr_t>(a.logits) ^ reinterpret_cast<uintptr_t>(a.dlogits)) & 15u) != 0 ||
+                     (a.T > 1 && (a.ld - a.ldd) * (int64_t)sizeof(T) % 16 != 0);
+  auto kernel = a.top_k ? (shift ? lp::logprob_bwd_kernel<T, true, true> : lp::logprob_bwd_kernel<T, true, false>)
+                        : (shift ? lp::logprob_bwd_kernel<T, false, true> : lp::logprob_bwd_kernel<T, false, false>);
+  kernel<<<grid, lp::kBwdThreads, 0, s>>>(a, (uint32_t)chunks, far, stream);
   const cudaError_t e = cudaGetLastError();
   count_launch();
   return e;

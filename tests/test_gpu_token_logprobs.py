@@ -326,6 +326,30 @@ def test_gradient_against_differences(F):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("T,V", [(1, 1), (2, 9), (3, 40), (17, 1003), (2, 9001)])
+def test_backward_between_rows_of_different_alignment(F, T, V, dtype):
+    # the same numbers whatever the two pitches and offsets, and nothing written beside the rows
+    z, targets = make(T, V, dtype, V)
+    k = min(V, 3)
+    r = F.fp4_token_logprobs(z, targets, top_k=k)
+    g = [torch.randn(s, device=DEV) for s in ((T,), (T,), (T, k))]
+    for tops in (None, g[2]):
+        want = F.fp4_token_logprobs_bwd(z, r, targets, g_logprob=g[0], g_entropy=g[1], g_top=tops)
+        for source, target, pitches in ((0, 0, (0, 1)), (1, 0, (0, 0)), (3, 6, (5, 2)), (0, 7, (8, 3)), (5, 2, (1, 4))):
+            a = torch.full((source + T * (V + pitches[0]),), math.nan, dtype=dtype, device=DEV)[source:]
+            a = a.view(T, V + pitches[0])[:, :V]
+            a.copy_(z)
+            whole = torch.full((target + T * (V + pitches[1]) + 9,), 7.0, dtype=dtype, device=DEV)
+            out = whole[target:target + T * (V + pitches[1])].view(T, V + pitches[1])[:, :V]
+            F.fp4_token_logprobs_bwd(a, r, targets, g_logprob=g[0], g_entropy=g[1], g_top=tops, dlogits=out)
+            torch.cuda.synchronize()
+            assert torch.equal(out, want), (source, target, pitches)
+            out.fill_(7.0)
+            assert (whole == 7.0).all()
+
+
+@pytest.mark.gpu
 def test_strides_streams_and_repeats(F):
     big = torch.randn((40, 3003), device=DEV)
     targets = torch.randint(0, 2999, (20,), device=DEV)
