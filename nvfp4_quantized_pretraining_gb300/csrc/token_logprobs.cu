@@ -227,11 +227,11 @@ __device__ __forceinline__ Share<T> share_of(const LogprobArgs& a, int64_t t, ui
   return h;
 }
 
-// The top k of a share by one warp, into x.top (0: nothing left).  maxima: the readers' (shared memory).
-
-template <typename T>
-__device__ __forceinline__ void share_top(const Share<T> h, const Partials<true>& part, float edge, bool odd, uint32_t k,
-                                       Scratch<true>& x) {
+// The top k of a share by one warp, into x.top (0: nothing left).  g0, g1: the lane's two groups' largest keys.  SHORT:
+// the groups are the lane's own, and every vector is read again (part is not used); else they are the readers'.
+template <typename T, bool SHORT>
+__device__ __forceinline__ void share_top(const Share<T> h, const Partials<true>& part, uint32_t g0, uint32_t g1, float edge,
+                                          bool odd, uint32_t k, Scratch<true>& x) {
   using V8 = Vec<T>;
   constexpr int N = V8::N;
   constexpr uint32_t kAll = 0xFFFFFFFFu;
@@ -241,9 +241,7 @@ __device__ __forceinline__ void share_top(const Share<T> h, const Partials<true>
   const uint32_t length = (h.v1 - h.v0) * N + h.edges, wanted = min(k, length);
   const uint32_t edge_key = order_key(edge);
   x.top[lane] = 0;
-  // the groups: readers lane, + 32, + 64, + 96, and the same from lane + 128
   auto key = [&](int i) { return order_key(part.m[lane + 32 * i]); };
-  const uint32_t g0 = max(max(key(0), key(1)), max(key(2), key(3))), g1 = max(max(key(4), key(5)), max(key(6), key(7)));
   // their k-th largest, bit by bit; of FP32 logits the upper half alone, rounded down (a bound all the same)
   uint32_t tau = 0;
 #pragma unroll 1
@@ -258,72 +256,80 @@ __device__ __forceinline__ void share_top(const Share<T> h, const Partials<true>
   // Fills the lists with the share's elements above tau and, with_equal, those equal to it; false if they do not fit
   // (the lists then hold as many of the first ones as do).
   auto collect = [&](bool with_equal) {
-    uint32_t strips = 0;
-    const uint32_t bound = with_equal ? tau : tau + 1;
-#pragma unroll 2
-    for (int i = 0; i < 8; ++i) {
-      const bool is = key(i) >= bound;
-      const uint32_t in = __ballot_sync(kAll, is);
-      if (is) x.list[strips + __popc(in & below)] = static_cast<uint8_t>(lane + 32 * i);
-      strips += __popc(in);
-    }
-    __syncwarp();
     // vectors with such an element
     const float least = key_value(tau);
-    const uint32_t stages = segment_stages(h.v1 - h.v0), per = stages * (kStageVecs / kReaders);
-    // (lane by lane over items x per; 32 lanes on is `step` items and `over_by` vectors on.  Small loops here and below:
-    // for a few rows, straight-line code costs its instruction fetches.)
-    const uint32_t step = 32 / max(per, 1u), over_by = 32 - step * per;
     uint32_t hits = 0;
-    for (uint32_t p0 = 0; p0 < strips && hits <= kCap; p0 += kItems / kSegments) {
-      uint32_t items = 0;  // segments of threads that hold such an element, up to kItems at a time
-      for (uint32_t i = p0 * kSegments + lane; i - lane < min(p0 * kSegments + kItems, strips * kSegments); i += 32) {
-        const uint32_t g = i % kSegments, who = i < strips * kSegments ? x.list[i / kSegments] : 0;
-        const bool is = i < strips * kSegments && g * stages * kStageVecs < h.v1 - h.v0 &&
-                        order_key(__uint_as_float((uint32_t)part.segment[g * kReaders + who] << 16)) >= bound;
+    auto look = [&](const uint4& w, uint32_t at) {
+      const float most = V8::widest(V8::max1(V8::max1(w.x, w.y), V8::max1(w.z, w.w)));
+      const bool hit = at < h.v1 && (with_equal ? most >= least : most > least);
+      const uint32_t in = __ballot_sync(kAll, hit), to = hits + __popc(in & below);
+      if (hit && to < kCap) x.hit[to] = w, x.hit_at[to] = at;
+      hits += __popc(in);
+    };
+    if constexpr (SHORT) {
+#pragma unroll 4
+      for (uint32_t v = h.v0; v < h.v1; v += 32) look(v + lane < h.v1 ? vec[v + lane] : make_uint4(0, 0, 0, 0), v + lane);
+    } else {
+      uint32_t strips = 0;
+      const uint32_t bound = with_equal ? tau : tau + 1;
+  #pragma unroll 2
+      for (int i = 0; i < 8; ++i) {
+        const bool is = key(i) >= bound;
         const uint32_t in = __ballot_sync(kAll, is);
-        if (is) x.item[items + __popc(in & below)] = static_cast<uint16_t>(g * kReaders + who);
-        items += __popc(in);
+        if (is) x.list[strips + __popc(in & below)] = static_cast<uint8_t>(lane + 32 * i);
+        strips += __popc(in);
       }
       __syncwarp();
-      const uint32_t total = items * per;
-      struct At {
-        uint32_t p, v;
-      } next = {lane / max(per, 1u), 0};
-      next.v = lane - next.p * per;
-      auto vector_at = [&](const At& i) {
-        if (i.p >= items) return h.v1;
-        const uint32_t item = x.item[i.p];
-        return h.v0 + item / kReaders * per * kReaders + item % kReaders + i.v * kReaders;
-      };
-      auto advance = [&](At& i) {
-        i.p += step, i.v += over_by;
-        if (i.v >= per) i.v -= per, ++i.p;
-      };
-      for (uint32_t i = 0; i < total && hits <= kCap; i += kBatch * 32) {
-        const uint32_t n = min((uint32_t)kBatch, (total - i + 31) / 32);
-        At same = next;
-        // (by asynchronous copies past L1: loads would each hold a line of the little L1 that the ring leaves)
-#pragma unroll 1
-        for (uint32_t u = 0; u < n; ++u, advance(next)) {
-          const uint32_t at = vector_at(next);
-          if (at < h.v1)
-            asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(&x.in[u * 32 + lane])), "l"(vec + at)
-                         : "memory");
+      const uint32_t stages = segment_stages(h.v1 - h.v0), per = stages * (kStageVecs / kReaders);
+      // (lane by lane over items x per; 32 lanes on is `step` items and `over_by` vectors on.  Small loops here and below:
+      // for a few rows, straight-line code costs its instruction fetches.)
+      const uint32_t step = 32 / max(per, 1u), over_by = 32 - step * per;
+      for (uint32_t p0 = 0; p0 < strips && hits <= kCap; p0 += kItems / kSegments) {
+        uint32_t items = 0;  // segments of threads that hold such an element, up to kItems at a time
+        for (uint32_t i = p0 * kSegments + lane; i - lane < min(p0 * kSegments + kItems, strips * kSegments); i += 32) {
+          const uint32_t g = i % kSegments, who = i < strips * kSegments ? x.list[i / kSegments] : 0;
+          const bool is = i < strips * kSegments && g * stages * kStageVecs < h.v1 - h.v0 &&
+                          order_key(__uint_as_float((uint32_t)part.segment[g * kReaders + who] << 16)) >= bound;
+          const uint32_t in = __ballot_sync(kAll, is);
+          if (is) x.item[items + __popc(in & below)] = static_cast<uint16_t>(g * kReaders + who);
+          items += __popc(in);
         }
-        asm volatile("cp.async.wait_all;" ::: "memory");
-#pragma unroll 1
-        for (uint32_t u = 0; u < n; ++u, advance(same)) {
-          const uint32_t at = vector_at(same);
-          const uint4 w = x.in[u * 32 + lane];  // (its own copy; a lane without a vector has no use for what is there)
-          const float most = V8::widest(V8::max1(V8::max1(w.x, w.y), V8::max1(w.z, w.w)));
-          const bool hit = at < h.v1 && (with_equal ? most >= least : most > least);
-          const uint32_t in = __ballot_sync(kAll, hit), to = hits + __popc(in & below);
-          if (hit && to < kCap) x.hit[to] = w, x.hit_at[to] = at;
-          hits += __popc(in);
+        __syncwarp();
+        const uint32_t total = items * per;
+        struct At {
+          uint32_t p, v;
+        } next = {lane / max(per, 1u), 0};
+        next.v = lane - next.p * per;
+        auto vector_at = [&](const At& i) {
+          if (i.p >= items) return h.v1;
+          const uint32_t item = x.item[i.p];
+          return h.v0 + item / kReaders * per * kReaders + item % kReaders + i.v * kReaders;
+        };
+        auto advance = [&](At& i) {
+          i.p += step, i.v += over_by;
+          if (i.v >= per) i.v -= per, ++i.p;
+        };
+        for (uint32_t i = 0; i < total && hits <= kCap; i += kBatch * 32) {
+          const uint32_t n = min((uint32_t)kBatch, (total - i + 31) / 32);
+          At same = next;
+          // (by asynchronous copies past L1: loads would each hold a line of the little L1 that the ring leaves)
+  #pragma unroll 1
+          for (uint32_t u = 0; u < n; ++u, advance(next)) {
+            const uint32_t at = vector_at(next);
+            if (at < h.v1)
+              asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(&x.in[u * 32 + lane])), "l"(vec + at)
+                           : "memory");
+          }
+          asm volatile("cp.async.wait_all;" ::: "memory");
+  #pragma unroll 1
+          for (uint32_t u = 0; u < n; ++u, advance(same)) {
+            const uint32_t at = vector_at(same);
+            const uint4 w = x.in[u * 32 + lane];  // (its own copy; a lane without a vector has no use for what is there)
+            look(w, at);
+          }
         }
+        __syncwarp();  // (the items have been read)
       }
-      __syncwarp();  // (the items have been read)
     }
     __syncwarp();
     // their elements; the edge elements, if there are any, as one more round
@@ -465,6 +471,65 @@ __device__ __forceinline__ void share_top(const Share<T> h, const Partials<true>
   __syncwarp();
 }
 
+// A row's results by one warp, from its sums, its edge elements (lane's) and its top entries.
+template <typename T, bool TOP>
+__device__ __forceinline__ void finish_row(const LogprobArgs& a, int64_t t, const Share<T>& h, const Sum& r, float edge,
+                                           int64_t target, float z_target, float far, float k2, Scratch<TOP>& x) {
+  using V8 = Vec<T>;
+  constexpr int N = V8::N;
+  const int lane = threadIdx.x & 31;
+  const float neg_inf = __uint_as_float(0xFF800000u);
+  auto near = [&](float v) { return v > -0.5f * far && v <= 0.5f * far; };
+  const float most = r.m;
+  float S, E;  // relative to the maximum
+  const bool empty = most == neg_inf;
+  if (near(most)) {
+    const float f = __fmaf_rn(-most, k2, reference(most, k2)), up = ex2(f);
+    S = r.s * up;
+    E = __fadd_rn(r.e, __fmul_rn(f, r.s)) * up;  // (uncontracted: one token alone gives exactly 0)
+  } else if (empty) {
+    S = r.s != r.s ? r.s : 0.0f, E = 0.0f;
+  } else {  // a maximum far out: the whole row again, relative to it
+    S = 0.0f, E = 0.0f;
+    auto add = [&](float z) {
+      const float y = max_nan((z - most) * k2, kFloor), p = ex2(y);
+      S += p;
+      E += p * y;
+    };
+#pragma unroll 4
+    for (uint32_t i = lane; i < h.cut.vecs; i += 32) {
+      float f[N];
+      V8::unpack(h.vec()[i], f);
+#pragma unroll
+      for (int j = 0; j < N; ++j) add(f[j]);
+    }
+    if (lane < h.edges) add(edge);
+    S = warp_sum(S), E = warp_sum(E);
+  }
+  const bool bad = S != S, none = empty && !bad;
+  const float nan = __uint_as_float(0x7FFFFFFFu);
+  const float ln_s = logf(S);
+  if (lane == 0) {
+    *reinterpret_cast<float2*>(a.stats + 2 * t) = bad ? make_float2(nan, nan) : make_float2(most, S);
+    if (a.entropy) a.entropy[t] = bad ? nan : none ? 0.0f : ln_s - kLn2 * (E / S);
+    if (a.targets) {
+      float v = 0.0f;
+      if (target >= a.V || (bad && target >= 0)) v = nan;
+      else if (target >= 0) v = none ? neg_inf : (z_target - most) * a.scale - ln_s;
+      a.logprob[t] = v;
+    }
+  }
+  if constexpr (TOP) {
+    if (lane < a.top_k) {
+      const uint64_t y = x.top[lane];
+      const float z = key_value(static_cast<uint32_t>(y >> 32));
+      a.top_index[t * a.top_k + lane] = static_cast<int64_t>(0xFFFFFFFFu - static_cast<uint32_t>(y));
+      a.top_logprob[t * a.top_k + lane] = bad ? nan : none ? neg_inf : (z - most) * a.scale - ln_s;
+    }
+    __syncwarp();
+  }
+}
+
 template <typename T, bool TOP>
 __global__ void __launch_bounds__(threads_of(TOP), kPerSm) logprob_kernel(const LogprobArgs a, const float far) {
   using V8 = Vec<T>;
@@ -590,7 +655,6 @@ __global__ void __launch_bounds__(threads_of(TOP), kPerSm) logprob_kernel(const 
   } else {
     // ---------------- joins and results ----------------
     if (TOP) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kJoinerRegs));
-    auto near = [&](float v) { return v > -0.5f * far && v <= 0.5f * far; };
     Scratch<TOP>& x = s_scratch[warp - kReaders / 32 - 1];
     uint32_t rows = warp - kReaders / 32 - 1;
     for (int64_t t = first + rows * stride; t < a.T; t += J * stride, rows += J) {
@@ -628,7 +692,10 @@ __global__ void __launch_bounds__(threads_of(TOP), kPerSm) logprob_kernel(const 
       odd = __any_sync(0xFFFFFFFFu, odd);
       if (odd) r.s = __uint_as_float(0x7FFFFFFFu);
       if constexpr (TOP) {
-        share_top<T>(h, part, edge, odd, a.top_k, x);
+        // the groups: readers lane, + 32, + 64, + 96, and the same from lane + 128
+        auto key = [&](int i) { return order_key(part.m[lane + 32 * i]); };
+        const uint32_t g0 = max(max(key(0), key(1)), max(key(2), key(3))), g1 = max(max(key(4), key(5)), max(key(6), key(7)));
+        share_top<T, false>(h, part, g0, g1, edge, odd, a.top_k, x);
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(&s_read[buf]);  // (the partials are not needed any more)
@@ -684,60 +751,103 @@ __global__ void __launch_bounds__(threads_of(TOP), kPerSm) logprob_kernel(const 
         }
         __syncwarp();
       }
-      most = r.m;
-      float S, E;  // relative to the maximum
-      const bool empty = most == neg_inf;
-      if (near(most)) {
-        const float f = __fmaf_rn(-most, k2, reference(most, k2)), up = ex2(f);
-        S = r.s * up;
-        E = __fadd_rn(r.e, __fmul_rn(f, r.s)) * up;  // (uncontracted: one token alone gives exactly 0)
-      } else if (empty) {
-        S = r.s != r.s ? r.s : 0.0f, E = 0.0f;
-      } else {  // a maximum far out: the whole row again, relative to it
-        S = 0.0f, E = 0.0f;
-        auto add = [&](float z) {
-          const float y = max_nan((z - most) * k2, kFloor), p = ex2(y);
-          S += p;
-          E += p * y;
-        };
-#pragma unroll 4
-        for (uint32_t i = lane; i < h.cut.vecs; i += 32) {
-          float f[N];
-          V8::unpack(h.vec()[i], f);
-#pragma unroll
-          for (int j = 0; j < N; ++j) add(f[j]);
-        }
-        if (lane < h.edges) add(edge);
-        S = warp_sum(S), E = warp_sum(E);
-      }
-      const bool bad = S != S, none = empty && !bad;
-      const float nan = __uint_as_float(0x7FFFFFFFu);
-      const float ln_s = logf(S);
-      if (lane == 0) {
-        *reinterpret_cast<float2*>(a.stats + 2 * t) = bad ? make_float2(nan, nan) : make_float2(most, S);
-        if (a.entropy) a.entropy[t] = bad ? nan : none ? 0.0f : ln_s - kLn2 * (E / S);
-        if (a.targets) {
-          float v = 0.0f;
-          if (target >= a.V || (bad && target >= 0)) v = nan;
-          else if (target >= 0) v = none ? neg_inf : (z_target - most) * a.scale - ln_s;
-          a.logprob[t] = v;
-        }
-      }
-      if constexpr (TOP) {
-        if (lane < a.top_k) {
-          const uint64_t y = x.top[lane];
-          const float z = key_value(static_cast<uint32_t>(y >> 32));
-          a.top_index[t * a.top_k + lane] = static_cast<int64_t>(0xFFFFFFFFu - static_cast<uint32_t>(y));
-          a.top_logprob[t * a.top_k + lane] = bad ? nan : none ? neg_inf : (z - most) * a.scale - ln_s;
-        }
-        __syncwarp();
-      }
+      finish_row<T, TOP>(a, t, h, r, edge, target, z_target, far, k2, x);
     }
   }
   if (!ok) drain_pause();  // a wait expired: let copies still in flight land first
   if (C > 1) {
     __syncwarp();
     cluster_sync();  // nobody signals a CTA that has gone
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Short rows, each by one warp: a CTA per row spends its time on the join of 256 threads' sums (8192 x 1000 BF16: 40 us).
+// The lanes' sums are made as the readers' above, two maxima a lane serve as the groups of the top k, and what is read
+// again comes from L1.
+// ---------------------------------------------------------------------------
+constexpr int kShortWarps = 4;
+// Which rows are short, by their bytes: always to 8 KB (8192 x 1000 BF16: 6 us against 39, top 20 15 against 68; one row
+// 2.6 against 3.6); with rows enough for all warps to 16 KB (8192 x 8000 BF16, top 5: 43 us against 56, but 500 rows 11.5
+// against 8.9), without the top k, which reads the row twice, to 32 KB (8192 x 8000 FP32: 44 us against 47, top 5 98
+// against 58).
+static bool short_rows(int64_t T, int64_t bytes, int top_k) {
+  return bytes <= 8192 || (T >= 1024 && bytes <= (top_k ? 16384 : 32768));
+}
+
+template <typename T, bool TOP>
+__global__ void __launch_bounds__(kShortWarps * 32) logprob_short_kernel(const LogprobArgs a, const float far) {
+  using V8 = Vec<T>;
+  constexpr int N = V8::N, U = 4;
+  __shared__ Scratch<TOP> s_scratch[kShortWarps];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const float k2 = a.scale * kLog2e, neg_inf = __uint_as_float(0xFF800000u);
+  const uint32_t low = V8::low_bits(-far);
+  Scratch<TOP>& x = s_scratch[warp];
+  for (int64_t t = (int64_t)blockIdx.x * kShortWarps + warp; t < a.T; t += (int64_t)gridDim.x * kShortWarps) {
+    const Share<T> h = share_of<T>(a, t, 0, 1);
+    const float edge = lane < h.edges ? V8::load(h.row + h.edge_index(lane)) : neg_inf;
+    const int64_t target = a.targets ? a.targets[t] : -1;
+    const float z_target = target >= 0 && target < a.V ? V8::load(h.row + target) : 0.0f;
+    float m0 = neg_inf, m1 = neg_inf, m = neg_inf, c = reference(-far, k2);
+    float2 s2 = make_float2(0.0f, 0.0f), e2 = make_float2(0.0f, 0.0f);
+    const uint4* vec = h.vec();
+#pragma unroll 1
+    for (uint32_t i = h.v0 + lane; i - lane < h.v1; i += 32 * U) {
+      uint4 q[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+        q[u] = i + 32 * u < h.v1 ? vec[i + 32 * u] : make_uint4(V8::kNone, V8::kNone, V8::kNone, V8::kNone);
+      uint32_t top[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        top[u] = V8::max1(V8::max1(q[u].x, q[u].y), V8::max1(q[u].z, q[u].w));
+        q[u].x = V8::max1(q[u].x, low), q[u].y = V8::max1(q[u].y, low);
+        q[u].z = V8::max1(q[u].z, low), q[u].w = V8::max1(q[u].w, low);
+      }
+      const float a0 = V8::widest(V8::max1(top[0], top[2])), a1 = V8::widest(V8::max1(top[1], top[3]));
+      m0 = fmaxf(m0, a0), m1 = fmaxf(m1, a1);
+      const float most = max_nan(a0, a1);
+      if (most > m) {  // (NaN: not taken, and s becomes NaN below)
+        m = most;
+        const float next = reference(fmaxf(m, -far), k2), d = c - next, f = ex2(d);
+        e2.x = (e2.x + s2.x * d) * f, e2.y = (e2.y + s2.y * d) * f;
+        s2.x *= f, s2.y *= f;
+        c = next;
+      }
+      const float2 kk = make_float2(k2, k2), cc = make_float2(-c, -c);
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        float f[N];
+        V8::unpack(q[u], f);
+#pragma unroll
+        for (int j = 0; j < N; j += 2) {
+          const float2 y = __ffma2_rn(make_float2(f[j], f[j + 1]), kk, cc), p = make_float2(ex2(y.x), ex2(y.y));
+          s2 = __fadd2_rn(s2, p);
+          e2 = __ffma2_rn(p, y, e2);
+        }
+      }
+    }
+    Sum r;
+    r.m = warp_max(fmaxf(fmaxf(edge, m), neg_inf));
+    const float to = reference(fmaxf(r.m, -far), k2), d = c - to, f = ex2(d);
+    const float s = s2.x + s2.y, e = e2.x + e2.y;
+    bool odd = s != s || edge != edge;  // NaN hides in a maximum
+    r.s = s * f, r.e = (e + s * d) * f;
+    if (lane < h.edges) {
+      const float y = __fmaf_rn(max_nan(edge, -far), k2, -to), p = ex2(y);
+      r.s += p, r.e += p * y;
+    }
+    r.s = warp_sum(r.s), r.e = warp_sum(r.e);
+    odd = __any_sync(0xFFFFFFFFu, odd);
+    if (odd) r.s = __uint_as_float(0x7FFFFFFFu);
+    if constexpr (TOP) {
+      const Partials<true>* none = nullptr;
+      share_top<T, true>(h, *none, order_key(m0), order_key(m1), edge, odd, a.top_k, x);
+    }
+    __syncwarp();
+    finish_row<T, TOP>(a, t, h, r, edge, target, z_target, far, k2, x);
+    __syncwarp();
   }
 }
 
@@ -956,9 +1066,17 @@ static cudaError_t launch_fwd_t(const LogprobArgs& a, int num_sms, cudaStream_t 
   // at least one stage of the ring): joining shares costs more than an uneven last round (515 x 50021 FP32, top 5:
   // 25 us in single CTAs, 27, 46 and 74 in clusters of 2, 4 and 8; 64 x 131072 BF16, top 20: 35 and 21 in 1 and 4).
   const int64_t slots = (int64_t)num_sms * kPerSm;
+  const float far = far_of(a.scale);
+  if (short_rows(a.T, a.V * sizeof(T), a.top_k)) {
+    auto kernel = a.top_k ? logprob_short_kernel<T, true> : logprob_short_kernel<T, false>;
+    const int64_t ctas = (a.T + kShortWarps - 1) / kShortWarps, most = (int64_t)num_sms * 16;
+    kernel<<<static_cast<uint32_t>(ctas < most ? ctas : most), kShortWarps * 32, 0, s>>>(a, far);
+    const cudaError_t e = cudaGetLastError();
+    count_launch();
+    return e;
+  }
   uint32_t cluster = 1;
   while (cluster < kMaxCluster && a.T * cluster * 2 <= slots && a.V / (cluster * 2) >= kStageVecs * Vec<T>::N) cluster *= 2;
-  const float far = far_of(a.scale);
   return a.top_k ? launch_fwd<T, true>(a, far, cluster, num_sms, s) : launch_fwd<T, false>(a, far, cluster, num_sms, s);
 }
 
