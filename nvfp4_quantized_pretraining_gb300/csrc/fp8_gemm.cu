@@ -748,6 +748,15 @@ static cudaError_t launch_two(const Fp8GemmArgs& a, const Fp8GemmArgs& b, cudaSt
 
 }  // namespace f8
 
+// The cycles of the launch that launch_fp8_gemm() would choose, for more than 128 rows.
+static double one_cost(const Fp8GemmArgs& g) {
+  using namespace f8;
+  const uint32_t num_k = (uint32_t)(fp8_pitch(g.K) / BK);
+  double c256, c128;
+  Plan<256, false>::split(g.M, g.N, num_k, c256);
+  Plan<128, false>::split(g.M, g.N, num_k, c128);
+  return c128 < c256 ? c128 : c256;
+}
 cudaError_t launch_fp8_gemm(const Fp8GemmArgs& g, cudaStream_t s) {
   using namespace f8;
   const Operand A{g.a_codes, g.a_scales, g.M}, B{g.b_codes, g.b_scales, g.N};
@@ -762,11 +771,14 @@ cudaError_t launch_fp8_gemm(const Fp8GemmArgs& g, cudaStream_t s) {
 
 cudaError_t launch_fp8_gemm_two(const Fp8GemmArgs& a, const Fp8GemmArgs& b, cudaStream_t s) {
   using namespace f8;
-  // few rows have kernels of their own; else one launch, with tiles of the width whose total is less
-  if (a.M <= 128 || b.M <= 128) {
+  // few rows have kernels of their own; else one launch, with tiles of the width whose total is less, or two launches
+  // where the split of K, which one launch does not have, outweighs the second one's start (300 x 32003 x 300 backward:
+  // 43 us instead of 65; 777 x 5003 x 2048 in one launch: 24 instead of 33)
+  auto both = [&] {
     const cudaError_t e = launch_fp8_gemm(a, s);
     return e == cudaSuccess ? launch_fp8_gemm(b, s) : e;
-  }
+  };
+  if (a.M <= 128 || b.M <= 128) return both();
   auto total = [](const Fp8GemmArgs& g, int64_t bn, double tile) {
     return double((g.M + 255) / 256 * ((g.N + bn - 1) / bn)) * tile;
   };
@@ -782,6 +794,8 @@ cudaError_t launch_fp8_gemm_two(const Fp8GemmArgs& a, const Fp8GemmArgs& b, cuda
                            P256::tile(stages(a) > stages(b) ? stages(a) : stages(b)), limits<256, false>().clusters[1]);
   const double t128 = cost(total(a, 128, P128::tile(stages(a))) + total(b, 128, P128::tile(stages(b))),
                            P128::tile(stages(a) > stages(b) ? stages(a) : stages(b)), limits<128, false>().clusters[1]);
+  constexpr double kStart = 4000;  // cycles
+  if (one_cost(a) + one_cost(b) + kStart < (t128 < t256 ? t128 : t256)) return both();
   // the longer tiles first: the shorter ones even out the end
   const bool order = stages(a) >= stages(b);
   const Fp8GemmArgs &x = order ? a : b, &y = order ? b : a;

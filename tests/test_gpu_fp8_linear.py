@@ -221,7 +221,7 @@ def test_few_tokens_many_rows_or_a_long_axis(F, M, N, K):
 
 
 @pytest.mark.gpu
-@pytest.mark.parametrize("M,N,K", [(1, 1, 1), (1, 256, 384), (130, 300, 257), (257, 1000, 520), (640, 512, 256)])
+@pytest.mark.parametrize("M,N,K", [(1, 1, 1), (1, 256, 384), (130, 300, 257), (257, 1000, 520), (640, 512, 256), (150, 20003, 136)])
 def test_linear(F, M, N, K):
     x, w, dy = make(M, K, 1).to(DEV), make(N, K, 2).to(DEV), make(M, N, 3).to(DEV)
     Wq, WqT = F.fp4_fp8_quantize_dual(w, 128)
