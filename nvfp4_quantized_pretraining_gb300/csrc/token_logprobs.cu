@@ -230,7 +230,7 @@ __device__ __forceinline__ Share<T> share_of(const LogprobArgs& a, int64_t t, ui
 // The top k of a share by one warp, into x.top (0: nothing left).  g0, g1: the lane's two groups' largest keys.  SHORT:
 // the groups are the lane's own, and every vector is read again (part is not used); else they are the readers'.
 template <typename T, bool SHORT>
-__device__ __forceinline__ void share_top(const Share<T> h, const Partials<true>& part, uint32_t g0, uint32_t g1, float edge,
+__device__ __forceinline__ void share_top(const Share<T> h, const Partials<true>* part, uint32_t g0, uint32_t g1, float edge,
                                           bool odd, uint32_t k, Scratch<true>& x) {
   using V8 = Vec<T>;
   constexpr int N = V8::N;
@@ -241,7 +241,7 @@ __device__ __forceinline__ void share_top(const Share<T> h, const Partials<true>
   const uint32_t length = (h.v1 - h.v0) * N + h.edges, wanted = min(k, length);
   const uint32_t edge_key = order_key(edge);
   x.top[lane] = 0;
-  auto key = [&](int i) { return order_key(part.m[lane + 32 * i]); };
+  auto key = [&](int i) { return order_key(part->m[lane + 32 * i]); };
   // their k-th largest, bit by bit; of FP32 logits the upper half alone, rounded down (a bound all the same)
   uint32_t tau = 0;
 #pragma unroll 1
@@ -289,7 +289,7 @@ __device__ __forceinline__ void share_top(const Share<T> h, const Partials<true>
         for (uint32_t i = p0 * kSegments + lane; i - lane < min(p0 * kSegments + kItems, strips * kSegments); i += 32) {
           const uint32_t g = i % kSegments, who = i < strips * kSegments ? x.list[i / kSegments] : 0;
           const bool is = i < strips * kSegments && g * stages * kStageVecs < h.v1 - h.v0 &&
-                          order_key(__uint_as_float((uint32_t)part.segment[g * kReaders + who] << 16)) >= bound;
+                          order_key(__uint_as_float((uint32_t)part->segment[g * kReaders + who] << 16)) >= bound;
           const uint32_t in = __ballot_sync(kAll, is);
           if (is) x.item[items + __popc(in & below)] = static_cast<uint16_t>(g * kReaders + who);
           items += __popc(in);
@@ -695,7 +695,7 @@ __global__ void __launch_bounds__(threads_of(TOP), kPerSm) logprob_kernel(const 
         // the groups: readers lane, + 32, + 64, + 96, and the same from lane + 128
         auto key = [&](int i) { return order_key(part.m[lane + 32 * i]); };
         const uint32_t g0 = max(max(key(0), key(1)), max(key(2), key(3))), g1 = max(max(key(4), key(5)), max(key(6), key(7)));
-        share_top<T, false>(h, part, g0, g1, edge, odd, a.top_k, x);
+        share_top<T, false>(h, &part, g0, g1, edge, odd, a.top_k, x);
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(&s_read[buf]);  // (the partials are not needed any more)
@@ -842,8 +842,7 @@ __global__ void __launch_bounds__(kShortWarps * 32) logprob_short_kernel(const L
     odd = __any_sync(0xFFFFFFFFu, odd);
     if (odd) r.s = __uint_as_float(0x7FFFFFFFu);
     if constexpr (TOP) {
-      const Partials<true>* none = nullptr;
-      share_top<T, true>(h, *none, order_key(m0), order_key(m1), edge, odd, a.top_k, x);
+      share_top<T, true>(h, nullptr, order_key(m0), order_key(m1), edge, odd, a.top_k, x);
     }
     __syncwarp();
     finish_row<T, TOP>(a, t, h, r, edge, target, z_target, far, k2, x);
@@ -1103,8 +1102,9 @@ static cudaError_t launch_bwd_threads(const LogprobBwdArgs& a, cudaStream_t s) {
   const bool stream = (double)a.T * a.V * sizeof(T) > 64e6;
   const bool shift = ((reinterpret_cast<uintptr_t>(a.logits) ^ reinterpret_cast<uintptr_t>(a.dlogits)) & 15u) != 0 ||
                      (a.T > 1 && (a.ld - a.ldd) * (int64_t)sizeof(T) % 16 != 0);
-  auto kernel = a.top_k ? (shift ? lp::logprob_bwd_kernel<T, true, true, kThreads> : lp::logprob_bwd_kernel<T, true, false, kThreads>)
-                        : (shift ? lp::logprob_bwd_kernel<T, false, true, kThreads> : lp::logprob_bwd_kernel<T, false, false, kThreads>);
+  auto kernel = lp::logprob_bwd_kernel<T, false, false, kThreads>;
+  if (a.top_k) kernel = shift ? lp::logprob_bwd_kernel<T, true, true, kThreads> : lp::logprob_bwd_kernel<T, true, false, kThreads>;
+  else if (shift) kernel = lp::logprob_bwd_kernel<T, false, true, kThreads>;
   kernel<<<grid, kThreads, 0, s>>>(a, (uint32_t)chunks, far, stream);
   const cudaError_t e = cudaGetLastError();
   count_launch();
