@@ -10,7 +10,7 @@
 // 6.8 TB/s leave 21 instructions per element): inputs whose rows start on 16 bytes come by TMA into a ring of tiles that
 // CTAs walk persistently (two tiles, three CTAs an SM), others by loads, a tile per CTA; both convert a tile with the
 // same code.  8192 x 32000: rows 134 us, columns 140 us, both 183 us (5.7 TB/s, 84% of the copy bandwidth); 8192 x 32003
-// in dense rows: 190, 204 and 283 us.
+// in dense rows: 140, 153 and 203 us.
 #include <cuda_bf16.h>
 
 #include "common.cuh"
@@ -280,14 +280,40 @@ __global__ void __launch_bounds__(kThreads) quantize_kernel(const __nv_bfloat16*
   pdl_wait();
   const uint32_t kb = blockIdx.x, rb = blockIdx.y, col = kb * 128 + (threadIdx.x & 63) * 2;
   uint32_t* words = reinterpret_cast<uint32_t*>(s_tile);
+  const uint16_t* p = reinterpret_cast<const uint16_t*>(x) + (int64_t)(rb * 128 + (threadIdx.x >> 6)) * ld + col;
+  // Whole tiles by words, all of a thread's 32 loads in flight and so nothing conditional between them (8192 x 32003, both
+  // forms: 203 us; 283 by elements, 540 by words with conditions).  Its rows are four
+  // apart, so all of them start on a word or none does; in those that do not, it takes the word after its first
+  // element (the last thread the one before) and stores halves, and what that leaves, the rows' first and last elements,
+  // is one more element for each thread.
+  if (rb * 128 + 128 <= t.rows && kb * 128 + 128 <= t.cols) {
+    const uint32_t pair = threadIdx.x & 63;
+    if ((reinterpret_cast<uintptr_t>(p) & 3u) == 0) {
+#pragma unroll 32
+      for (uint32_t i = threadIdx.x >> 6; i < 128; i += 4, p += 4 * ld)
+        words[i * 64 + pair] = *reinterpret_cast<const uint32_t*>(p);
+    } else {
+      const int off = pair == 63 ? -1 : 1;
+      uint16_t* halves = reinterpret_cast<uint16_t*>(s_tile) + pair * 2 + off;
+      p += off;
+#pragma unroll 32
+      for (uint32_t i = threadIdx.x >> 6; i < 128; i += 4, p += 4 * ld) {
+        const uint32_t w = *reinterpret_cast<const uint32_t*>(p);
+        halves[i * 128] = static_cast<uint16_t>(w), halves[i * 128 + 1] = static_cast<uint16_t>(w >> 16);
+      }
+    }
+    const uint32_t row = threadIdx.x >> 1, e = (threadIdx.x & 1) * 127;
+    const uint16_t* first = reinterpret_cast<const uint16_t*>(x) + (int64_t)(rb * 128 + row) * ld + kb * 128;
+    if (reinterpret_cast<uintptr_t>(first) & 2u) reinterpret_cast<uint16_t*>(s_tile)[row * 128 + e] = first[e];
+  } else {
 #pragma unroll 8
-  for (uint32_t i = threadIdx.x >> 6; i < 128; i += 4) {
-    const uint32_t row = rb * 128 + i;
-    const uint16_t* p = reinterpret_cast<const uint16_t*>(x) + (int64_t)row * ld + col;
-    uint32_t w = 0;
-    if (row < t.rows && col < t.cols) w = p[0];
-    if (row < t.rows && col + 1 < t.cols) w |= (uint32_t)p[1] << 16;
-    words[i * 64 + (threadIdx.x & 63)] = w;
+    for (uint32_t i = threadIdx.x >> 6; i < 128; i += 4, p += 4 * ld) {
+      const uint32_t row = rb * 128 + i;
+      uint32_t w = 0;
+      if (row < t.rows && col < t.cols) w = p[0];
+      if (row < t.rows && col + 1 < t.cols) w |= (uint32_t)p[1] << 16;
+      words[i * 64 + (threadIdx.x & 63)] = w;
+    }
   }
   __syncthreads();
   convert_tile<ROW, COL, SQUARE>(s_tile, s_max, rb, kb, t, r, c, [] {});
