@@ -535,16 +535,39 @@ class FP8Tensor:
     codes: uint8 [rows, cols rounded up to 128], E4M3; scales: uint8, UE8M0 bytes in the MMA layout."""
 
     def __init__(self, codes: torch.Tensor, scales: torch.Tensor, rows: int, cols: int):
-        self.codes, self.scales, self.rows, self.cols = codes, scales, rows, cols
-        self._c = CFP8Tensor(codes.data_ptr(), scales.data_ptr(), rows, cols)
+        self._views, self.device = (codes, scales), codes.device
+        self._describe(codes.data_ptr(), scales.data_ptr(), rows, cols)
+
+    def _describe(self, codes: int, scales: int, rows: int, cols: int) -> None:
+        self.rows, self.cols = rows, cols
+        self._c = CFP8Tensor(codes, scales, rows, cols)
         self._ref = ctypes.addressof(self._c)
 
     @staticmethod
     def empty(rows: int, cols: int, device="cuda") -> "FP8Tensor":
-        pitch = -(-cols // FP8_BLOCK) * FP8_BLOCK
-        codes = torch.empty((rows, pitch), dtype=torch.uint8, device=device)
-        scales = torch.empty(-(-rows // 128) * -(-cols // 512) * 512, dtype=torch.uint8, device=device)
-        return FP8Tensor(codes, scales, rows, cols)
+        # one allocation for both, and no views of it before someone asks (small calls are bound by the host)
+        size = rows * (-(-cols // FP8_BLOCK) * FP8_BLOCK)
+        q = FP8Tensor.__new__(FP8Tensor)
+        q._buffer = torch.empty(size + -(-rows // 128) * -(-cols // 512) * 512, dtype=torch.uint8, device=device)
+        q._views, q.device = None, q._buffer.device
+        at = q._buffer.data_ptr()
+        q._describe(at, at + size, rows, cols)
+        return q
+
+    def _both(self):
+        if self._views is None:
+            pitch = -(-self.cols // FP8_BLOCK) * FP8_BLOCK
+            codes, scales = self._buffer.split_with_sizes((self.rows * pitch, self._buffer.numel() - self.rows * pitch))
+            self._views = codes.view(self.rows, pitch), scales
+        return self._views
+
+    @property
+    def codes(self) -> torch.Tensor:
+        return self._both()[0]
+
+    @property
+    def scales(self) -> torch.Tensor:
+        return self._both()[1]
 
     def c(self) -> int:
         """Address of the C descriptor (valid while this object lives)."""
@@ -552,12 +575,15 @@ class FP8Tensor:
 
     def values(self) -> torch.Tensor:
         """The codes as a float8_e4m3fn view [rows, cols] (values in units of their block's scale)."""
+        if self._views is None:
+            pitch = -(-self.cols // FP8_BLOCK) * FP8_BLOCK
+            return self._buffer.view(torch.float8_e4m3fn).as_strided((self.rows, self.cols), (pitch, 1))
         return self.codes.view(torch.float8_e4m3fn)[:, :self.cols]
 
 
 def _check_fp8(q, rows: int, cols: int, device, name: str) -> None:
-    if not isinstance(q, FP8Tensor) or (q.rows, q.cols) != (rows, cols) or q.codes.device != device:
-        what = f"{q.rows} x {q.cols} on {q.codes.device}" if isinstance(q, FP8Tensor) else type(q).__name__
+    if not isinstance(q, FP8Tensor) or (q.rows, q.cols) != (rows, cols) or q.device != device:
+        what = f"{q.rows} x {q.cols} on {q.device}" if isinstance(q, FP8Tensor) else type(q).__name__
         raise ValueError(f"{name} must be a {rows} x {cols} FP8Tensor on {device} (got {what})")
 
 
@@ -623,7 +649,7 @@ def fp4_fp8_quantize_dual(x: torch.Tensor, block_rows: int = 1, out_row: FP8Tens
 
 def fp4_fp8_gemm(A: FP8Tensor, B: FP8Tensor, out=None, out_dtype=torch.bfloat16, stream=None) -> torch.Tensor:
     """A B^T (M x N) of two FP8 tensors with the same number of columns."""
-    dev = A.codes.device
+    dev = A.device
     _check_fp8(B, B.rows, A.cols, dev, "B")
     if out is None and out_dtype not in (torch.bfloat16, torch.float32):
         raise ValueError(f"out_dtype must be bfloat16 or float32 (got {out_dtype})")
